@@ -14,3 +14,10 @@ from .api import (  # noqa: F401
     calibrate,
     prefill,
 )
+from .cache4 import (  # noqa: F401
+    KVCache4,
+    cache4_empty,
+    cache4_read,
+    cache4_write,
+    decode4,
+)

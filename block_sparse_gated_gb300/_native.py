@@ -36,6 +36,39 @@ class FwdParams(ctypes.Structure):
     ]
 
 
+class Cache4(ctypes.Structure):
+    """Mirror of bsfa_cache4."""
+    _fields_ = [
+        ("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
+        ("k_exp", c_void_p), ("v_exp", c_void_p),
+        ("k_stride", c_int64 * 3), ("v_stride", c_int64 * 3),
+        ("k_scale_stride", c_int64 * 3), ("v_scale_stride", c_int64 * 3),
+        ("num_pages", c_int), ("page_size", c_int), ("num_heads_kv", c_int),
+        ("head_dim", c_int),
+        ("block_table", c_void_p), ("block_table_stride", c_int), ("block_table_width", c_int),
+    ]
+
+
+class Cache4Rows(ctypes.Structure):
+    """Mirror of bsfa_cache4_rows."""
+    _fields_ = [
+        ("k", c_void_p), ("v", c_void_p), ("k_stride", c_int64 * 3), ("v_stride", c_int64 * 3),
+        ("batch", c_int), ("seqlen", c_int), ("cu_seqlens", c_void_p), ("start", c_void_p),
+        ("dtype", c_int),
+    ]
+
+
+class Decode4Params(ctypes.Structure):
+    """Mirror of bsfa_decode4_params."""
+    _fields_ = [
+        ("q", c_void_p), ("o", c_void_p), ("q_stride", c_int64 * 3), ("o_stride", c_int64 * 3),
+        ("batch", c_int), ("num_heads_q", c_int), ("q_len", c_int),
+        ("seqlens", c_void_p), ("max_seqlen", c_int), ("softmax_scale", c_float),
+        ("causal", c_int), ("lse", c_void_p),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("dtype", c_int),
+    ]
+
+
 # bsfa_dtype
 DTYPE_BF16, DTYPE_F16 = 0, 1
 # bsfa_flag
@@ -58,6 +91,11 @@ SIGNATURES = [
         ctypes.POINTER(c_int), c_int, c_void_p, c_void_p, c_size_t, c_void_p]),
     ("bsfa_device_error", c_int, [c_void_p, ctypes.POINTER(ctypes.c_uint)]),
     ("bsfa_prefill_fwd_noalloc", c_int, [ctypes.POINTER(FwdParams), c_void_p]),
+    ("bsfa_cache4_write", c_int, [ctypes.POINTER(Cache4), ctypes.POINTER(Cache4Rows), c_void_p]),
+    ("bsfa_cache4_read", c_int, [ctypes.POINTER(Cache4), ctypes.POINTER(Cache4Rows), c_void_p]),
+    ("bsfa_decode4_workspace_size", c_size_t, [ctypes.POINTER(Cache4),
+                                               ctypes.POINTER(Decode4Params)]),
+    ("bsfa_decode4", c_int, [ctypes.POINTER(Cache4), ctypes.POINTER(Decode4Params), c_void_p]),
     ("bsfa_selftest_wait_guard", c_int, [ctypes.c_uint, c_void_p]),
 ]
 

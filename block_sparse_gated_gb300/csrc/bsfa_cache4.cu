@@ -1,0 +1,320 @@
+// bsfa_cache4.cu -- bsfa_cache4_write and bsfa_cache4_read: 16-bit keys and
+// values quantised into the pages of a 4-bit cache, and read back.
+//
+// One thread owns 16 consecutive elements of a row (one scale) and walks over
+// the planes it is given, a plane being the keys or the values of one KV head.
+// Both kernels move each byte once and are bound by HBM: the write reads 32
+// and stores 9 bytes per 16 elements, the read the other way round.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "bsfa.h"
+#include "bsfa_cache4.h"
+#include "fp4.cuh"
+
+namespace bsfa {
+
+namespace {
+
+struct RowsArgs {
+  const uint8_t *kc, *vc, *ks, *vs;  // written by the write, read by the read
+  const int32_t *kexp, *vexp;
+  long long kc_s[3], vc_s[3], ks_s[3], vs_s[3];  // {page, head, token} bytes
+  const uint16_t *k, *v;
+  long long k_s[3], v_s[3];  // {batch, head, token} elements
+  const int32_t *table, *cu, *start;
+  int table_stride, table_width, page_size, num_pages;
+  int heads, batch, seqlen;
+  long long rows;        // batch * seqlen, or the packed rows; below 2^31
+  int planes_per_block;  // planes that one thread walks over
+};
+
+// Where row t of the call lies.
+struct Slot {
+  int b;         // its sequence; negative: none (packed rows outside every sequence)
+  int i;         // its row of the 16-bit tensors (within the sequence, or packed)
+  int page;      // negative: the position names no cache row
+  int token;     // within the page
+};
+
+__device__ __forceinline__ Slot find_slot(const RowsArgs& a, int t) {
+  Slot s;
+  int pos;
+  if (a.cu == nullptr) {
+    s.b = t / a.seqlen;
+    s.i = t - s.b * a.seqlen;
+    pos = s.i;
+  } else {
+    // The last sequence that begins at or before row t.
+    int lo = 0, hi = a.batch;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(a.cu + mid) <= t)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    s.b = lo - 1;
+    s.i = t;
+    if (s.b >= 0 && t >= __ldg(a.cu + s.b + 1)) s.b = -1;
+    if (s.b < 0) return s;
+    pos = s.i - __ldg(a.cu + s.b);
+  }
+  s.page = -1;
+  s.token = 0;
+  const long long p = static_cast<long long>(pos) + (a.start ? __ldg(a.start + s.b) : 0);
+  if (p >= 0 && p < static_cast<long long>(a.table_width) * a.page_size) {
+    const int col = static_cast<int>(p) / a.page_size;
+    const int page = __ldg(a.table + static_cast<long long>(s.b) * a.table_stride + col);
+    if (page >= 0 && page < a.num_pages) {
+      s.page = page;
+      s.token = static_cast<int>(p) - col * a.page_size;
+    }
+  }
+  return s;
+}
+
+// 16 elements -> 16 codes and a scale.
+//
+// scale = e4m3(a / 6): the division is correctly rounded and a has at most 11
+// significant bits, so a quotient that lies between two e4m3 values is exactly
+// so in fp32 too and no border moves.  x / scale is formed as x * (1 / scale),
+// off by less than 2^-21 where it matters, and then rounded to a multiple of
+// 2^-16 by adding and subtracting 1.5 * 2^7: a quotient halfway between two
+// codes becomes exactly that, and any other stays on its side of it, because
+// the short x and scale keep it at least 2^-13 away.
+template <bool F16>
+__device__ __forceinline__ void quantise16(const uint32_t (&x)[8], float down, uint2& codes,
+                                           uint32_t& scale) {
+  // Largest magnitude: 16-bit patterns without the sign order like the values,
+  // with infinity and NaN above every finite one.
+  uint32_t m = x[0] & 0x7fff7fffu;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = __vmaxu2(m, x[i] & 0x7fff7fffu);
+  m = max(m & 0xffffu, m >> 16);
+  const bool finite = m < (F16 ? 0x7c00u : 0x7f80u);
+  const float a = x2_to_f32(m, F16).x * down;
+  uint32_t byte = max(f32_to_e4m3(__fdiv_rn(a, 6.f)), 1u);  // 1: the scale 2^-9
+  const float r = __frcp_rn(f16x2_to_f32(e4m3x2_to_f16(byte)).x) * down;
+  float y[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = x2_to_f32(x[i], F16);
+    y[2 * i] = __fsub_rn(__fadd_rn(__fmul_rn(f.x, r), 192.f), 192.f);
+    y[2 * i + 1] = __fsub_rn(__fadd_rn(__fmul_rn(f.y, r), 192.f), 192.f);
+  }
+  codes.x = finite ? f32x8_to_e2m1(y) : 0u;
+  codes.y = finite ? f32x8_to_e2m1(y + 8) : 0u;
+  scale = finite ? byte : 0x7fu;
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(128) cache4_write_kernel(const RowsArgs a) {
+  constexpr int groups = D / FP4_GROUP;
+  const int g = threadIdx.x & (groups - 1);
+  const long long row = static_cast<long long>(blockIdx.x) * (128 / groups) + threadIdx.x / groups;
+  if (row >= a.rows) return;
+  const int t = static_cast<int>(row);
+  const Slot s = find_slot(a, t);
+  if (s.b < 0 || s.page < 0) return;
+  const long long bb = a.cu == nullptr ? s.b : 0;
+  const int p0 = blockIdx.y * a.planes_per_block;
+  const int p1 = min(p0 + a.planes_per_block, 2 * a.heads);
+#pragma unroll 4
+  for (int p = p0; p < p1; ++p) {
+    const bool value = p >= a.heads;
+    const int h = value ? p - a.heads : p;
+    const uint16_t* src =
+        value ? a.v + bb * a.v_s[0] + h * a.v_s[1] + s.i * a.v_s[2]
+              : a.k + bb * a.k_s[0] + h * a.k_s[1] + s.i * a.k_s[2];
+    const uint4* in = reinterpret_cast<const uint4*>(src + g * FP4_GROUP);
+    const uint4 u0 = __ldg(in), u1 = __ldg(in + 1);
+    const uint32_t x[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+    uint2 codes;
+    uint32_t scale;
+    quantise16<F16>(x, pow2f(-head_exp(value ? a.vexp : a.kexp, h)), codes, scale);
+    const long long* cs = value ? a.vc_s : a.kc_s;
+    const long long* ss = value ? a.vs_s : a.ks_s;
+    uint8_t* c = const_cast<uint8_t*>(value ? a.vc : a.kc) + s.page * cs[0] + h * cs[1] +
+                 s.token * cs[2];
+    uint8_t* z = const_cast<uint8_t*>(value ? a.vs : a.ks) + s.page * ss[0] + h * ss[1] +
+                 s.token * ss[2];
+    reinterpret_cast<uint2*>(c)[g] = codes;
+    z[g] = static_cast<uint8_t>(scale);
+  }
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(128) cache4_read_kernel(const RowsArgs a) {
+  constexpr int groups = D / FP4_GROUP;
+  const int g = threadIdx.x & (groups - 1);
+  const long long row = static_cast<long long>(blockIdx.x) * (128 / groups) + threadIdx.x / groups;
+  if (row >= a.rows) return;
+  const int t = static_cast<int>(row);
+  const Slot s = find_slot(a, t);
+  if (s.b < 0) return;
+  const long long bb = a.cu == nullptr ? s.b : 0;
+  const int p0 = blockIdx.y * a.planes_per_block;
+  const int p1 = min(p0 + a.planes_per_block, 2 * a.heads);
+#pragma unroll 4
+  for (int p = p0; p < p1; ++p) {
+    const bool value = p >= a.heads;
+    const int h = value ? p - a.heads : p;
+    uint2 codes = make_uint2(0u, 0u);
+    uint32_t scale = 0u;
+    if (s.page >= 0) {
+      const long long* cs = value ? a.vc_s : a.kc_s;
+      const long long* ss = value ? a.vs_s : a.ks_s;
+      const uint8_t* c =
+          (value ? a.vc : a.kc) + s.page * cs[0] + h * cs[1] + s.token * cs[2];
+      const uint8_t* z =
+          (value ? a.vs : a.ks) + s.page * ss[0] + h * ss[1] + s.token * ss[2];
+      codes = __ldg(reinterpret_cast<const uint2*>(c) + g);
+      scale = __ldg(z + g);
+    }
+    // code * scale has 6 significant bits: exact in fp32, and so is the power
+    // of two; one rounding, to the output's type.
+    const float f = f16x2_to_f32(e4m3x2_to_f16(scale)).x *
+                    pow2f(head_exp(value ? a.vexp : a.kexp, h));
+    uint32_t out[8];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      uint32_t e[4];
+      e2m1x8_to_f16(w ? codes.y : codes.x, e);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 y = f16x2_to_f32(e[j]);
+        out[4 * w + j] = f32_to_x2(y.x * f, y.y * f, F16);
+      }
+    }
+    uint16_t* dst = const_cast<uint16_t*>(
+        value ? a.v + bb * a.v_s[0] + h * a.v_s[1] + s.i * a.v_s[2]
+              : a.k + bb * a.k_s[0] + h * a.k_s[1] + s.i * a.k_s[2]);
+    uint4* o = reinterpret_cast<uint4*>(dst + g * FP4_GROUP);
+    o[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    o[1] = make_uint4(out[4], out[5], out[6], out[7]);
+  }
+}
+
+bsfa_status validate_rows(const bsfa_cache4* c, const bsfa_cache4_rows* r) {
+  if (c == nullptr || r == nullptr) return BSFA_ERR_INVALID_ARG;
+  if (r->batch < 0 || r->seqlen < 0) return BSFA_ERR_INVALID_ARG;
+  const bsfa_status v = validate_cache4(c);
+  if (v != BSFA_OK) return v;
+  if (r->dtype != BSFA_DTYPE_BF16 && r->dtype != BSFA_DTYPE_F16) return BSFA_ERR_UNSUPPORTED;
+  if (r->batch > CACHE4_MAX_BATCH) return BSFA_ERR_UNSUPPORTED;
+  if (!r->cu_seqlens && static_cast<long long>(r->batch) * r->seqlen > 0x7fffffffLL)
+    return BSFA_ERR_UNSUPPORTED;
+  if (r->batch == 0 || r->seqlen == 0) return BSFA_OK;
+  const bsfa_status q = validate_cache4_pointers(c);
+  if (q != BSFA_OK) return q;
+  if (!r->k || !r->v) return BSFA_ERR_INVALID_ARG;
+  const int64_t extent[3] = {r->cu_seqlens ? 1 : r->batch, c->num_heads_kv, r->seqlen};
+  if (!rows_aligned(r->k, r->k_stride, extent) || !rows_aligned(r->v, r->v_stride, extent))
+    return BSFA_ERR_UNSUPPORTED;
+  return BSFA_OK;
+}
+
+bsfa_status launch_rows(const bsfa_cache4* c, const bsfa_cache4_rows* r, bool write,
+                        bsfa_stream_t stream_) {
+  const bsfa_status v = validate_rows(c, r);
+  if (v != BSFA_OK || r->batch == 0 || r->seqlen == 0) return v;
+  RowsArgs a{};
+  a.kc = c->k;
+  a.vc = c->v;
+  a.ks = c->k_scale;
+  a.vs = c->v_scale;
+  a.kexp = c->k_exp;
+  a.vexp = c->v_exp;
+  for (int i = 0; i < 3; ++i) {
+    a.kc_s[i] = c->k_stride[i];
+    a.vc_s[i] = c->v_stride[i];
+    a.ks_s[i] = c->k_scale_stride[i];
+    a.vs_s[i] = c->v_scale_stride[i];
+    a.k_s[i] = r->k_stride[i];
+    a.v_s[i] = r->v_stride[i];
+  }
+  a.k = static_cast<const uint16_t*>(r->k);
+  a.v = static_cast<const uint16_t*>(r->v);
+  a.table = c->block_table;
+  a.cu = r->cu_seqlens;
+  a.start = r->start;
+  a.table_stride = c->block_table_stride;
+  a.table_width = c->block_table_width;
+  a.page_size = c->page_size;
+  a.num_pages = c->num_pages;
+  a.heads = c->num_heads_kv;
+  a.batch = r->batch;
+  a.seqlen = r->seqlen;
+  a.rows = r->cu_seqlens ? r->seqlen : static_cast<long long>(r->batch) * r->seqlen;
+  const int per_block = 128 / (c->head_dim / FP4_GROUP);
+  const long long blocks = (a.rows + per_block - 1) / per_block;
+  // A thread that walks over more planes finds its page once for all of them;
+  // with few rows the planes go to separate blocks, so that the call still
+  // fills the GPU.
+  const int planes = 2 * c->num_heads_kv;
+  long long split = (4096 + blocks - 1) / blocks;
+  split = split < 1 ? 1 : split > planes ? planes : split;
+  a.planes_per_block = static_cast<int>((planes + split - 1) / split);
+  const dim3 grid(static_cast<unsigned>(blocks),
+                  (planes + a.planes_per_block - 1) / a.planes_per_block);
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  using Kernel = void (*)(RowsArgs);
+  static const Kernel kernels[2][2][2] = {  // [write][fp16][d = 128]
+      {{cache4_read_kernel<64, false>, cache4_read_kernel<128, false>},
+       {cache4_read_kernel<64, true>, cache4_read_kernel<128, true>}},
+      {{cache4_write_kernel<64, false>, cache4_write_kernel<128, false>},
+       {cache4_write_kernel<64, true>, cache4_write_kernel<128, true>}}};
+  kernels[write][r->dtype == BSFA_DTYPE_F16][c->head_dim == 128]<<<grid, 128, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? BSFA_OK : BSFA_ERR_CUDA;
+}
+
+}  // namespace
+
+bsfa_status validate_cache4(const bsfa_cache4* c) {
+  if (c->num_heads_kv <= 0 || c->num_pages < 1 || c->page_size <= 0 || c->block_table_width < 0 ||
+      c->block_table_stride < c->block_table_width)
+    return BSFA_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128) return BSFA_ERR_UNSUPPORTED;
+  if (c->page_size % 16) return BSFA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(c->block_table_width) * c->page_size > 0x7fffffffLL)
+    return BSFA_ERR_UNSUPPORTED;
+  if (c->num_heads_kv > CACHE4_MAX_HEADS) return BSFA_ERR_UNSUPPORTED;
+  return BSFA_OK;
+}
+
+bsfa_status validate_cache4_pointers(const bsfa_cache4* c) {
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->block_table)
+    return BSFA_ERR_INVALID_ARG;
+  const int64_t unit = c->head_dim / FP4_GROUP;  // bytes of a row's scales
+  const uintptr_t code_bits = reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v);
+  const uintptr_t scale_bits =
+      reinterpret_cast<uintptr_t>(c->k_scale) | reinterpret_cast<uintptr_t>(c->v_scale);
+  if ((code_bits & 15u) || (scale_bits & (unit - 1))) return BSFA_ERR_UNSUPPORTED;
+  for (int i = 0; i < 3; ++i) {
+    if (c->k_stride[i] <= 0 || c->v_stride[i] <= 0 || c->k_scale_stride[i] <= 0 ||
+        c->v_scale_stride[i] <= 0)
+      return BSFA_ERR_UNSUPPORTED;
+    if (c->k_stride[i] % 16 || c->v_stride[i] % 16 || c->k_scale_stride[i] % unit ||
+        c->v_scale_stride[i] % unit)
+      return BSFA_ERR_UNSUPPORTED;
+  }
+  return BSFA_OK;
+}
+
+}  // namespace bsfa
+
+extern "C" {
+
+bsfa_status bsfa_cache4_write(const bsfa_cache4* cache, const bsfa_cache4_rows* rows,
+                              bsfa_stream_t stream) {
+  return bsfa::launch_rows(cache, rows, true, stream);
+}
+
+bsfa_status bsfa_cache4_read(const bsfa_cache4* cache, const bsfa_cache4_rows* rows,
+                             bsfa_stream_t stream) {
+  return bsfa::launch_rows(cache, rows, false, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,860 @@
+// bsfa_decode4.cu -- bsfa_decode4: attention of a few new tokens per sequence
+// over the 4-bit cache.
+//
+// Mathematics.  With k_t = code * scale (exact in fp16) and the query row
+// scaled by a power of two into fp16's range, S^T = K Q^T and O^T = V^T P^T are
+// fp16 tensor-core products with fp32 sums.  The softmax is streamed: a
+// reference m (log2 units) is subtracted, p = 2^(y - m), and m is raised, with
+// O and the sum l rescaled, only when some score passes it by more than
+// 2^HEADROOM; p carries a factor 2^SHIFT that cancels in O / l and keeps small
+// weights out of fp16's subnormals.
+//
+// Layout.  Cached tokens are the rows (M) of the products and query rows
+// (Hq/Hkv heads times q_len tokens) the columns (N = 8 per tile), so that a
+// decode step of up to 8 query heads per KV head wastes no tensor work, and so
+// that a lane owns whole scale groups: of a key it needs d/4 consecutive
+// elements, of a value d/8.  The codes go from shared memory to fragments with
+// one conversion and one product per pair of elements and no transposition:
+// keys pair neighbours of one token, values pair two tokens by merging nibbles.
+//
+// Work split.  A unit is 64 cached tokens of one (sequence, KV head, row tile)
+// segment.  The units of all segments form one line, which is cut into equal
+// pieces, one per CTA, from the lengths on the device: long and short
+// sequences balance without the host knowing them, and a captured call stays
+// right as they grow.  A segment that a cut crosses leaves partial sums in the
+// workspace, which a second kernel joins in a fixed order.
+//
+// Bound.  HBM: 144 bytes per (token, KV head) at d = 128, against about 240
+// issued warp instructions per 16 tokens and head.  Each warp streams its own
+// 16-token tiles through a private ring of asynchronous copies; no barrier is
+// met inside a segment.
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include "bsfa.h"
+#include "bsfa_cache4.h"
+#include "fp4.cuh"
+
+namespace bsfa {
+
+namespace {
+
+constexpr int WARPS = 4;
+constexpr int THREADS = 32 * WARPS;
+constexpr int TOK = 16;             // tokens of a warp's tile
+constexpr int UNIT = TOK * WARPS;   // tokens of a work unit
+constexpr float HEADROOM = 5.f;     // log2 a score may pass the reference by
+constexpr float SHIFT = 10.f;       // log2 of the factor that p carries: p < 2^15
+constexpr int MIN_UNITS = 2;        // shortest piece of the line worth a CTA
+
+// Per row-tile width (NT tiles of 8 query rows): CTAs per SM, ring stages, and
+// the most CTAs a launch has (the workspace holds two partial results each).
+template <int NT>
+struct Shape;
+template <>
+struct Shape<1> {
+  static constexpr int CTAS = 4, STAGES = 5, MAX_GRID = 640;
+};
+template <>
+struct Shape<2> {
+  static constexpr int CTAS = 3, STAGES = 6, MAX_GRID = 480;
+};
+template <>
+struct Shape<4> {
+  static constexpr int CTAS = 2, STAGES = 8, MAX_GRID = 320;
+};
+
+struct DecArgs {
+  const uint8_t *kc, *vc, *ks, *vs;
+  const int32_t *kexp, *vexp;
+  long long kc_s[3], vc_s[3], ks_s[3], vs_s[3];  // {page, head, token} bytes
+  const int32_t* table;
+  int table_stride, num_pages, tiles_per_page;
+  const uint16_t* q;
+  uint16_t* o;
+  long long q_s[3], o_s[3];
+  const int32_t* seqlens;
+  int batch, heads_kv, group, q_len, rows, row_tiles, max_len;
+  int causal, f16, split;
+  float sigma_log2;
+  float* lse;
+  long long lse_pitch;
+  float* part_o;    // [grid][2][8 * NT][d]
+  float2* part_ml;  // [grid][2][8 * NT]
+  int4* joins;      // [grid]: {sequence, kvh * row_tiles + row tile, last CTA, 0}, or x < 0
+};
+
+// The sequence length that the call sees.
+__device__ __forceinline__ int clamp_len(const DecArgs& a, int b) {
+  return max(0, min(__ldg(a.seqlens + b), a.max_len));
+}
+__device__ __forceinline__ int units_of(int len) { return max(1, (len + UNIT - 1) / UNIT); }
+
+// Byte offset in a warp's stage of row `t` (0..15), 16-byte chunk `c`.  Rows
+// are paired into 128-byte lines and chunks permuted so that both readers --
+// for keys the rows {0,4,1,5,2,6,3,7}, two (four at d = 64) at a time, for
+// values rows 4e..4e+3 at once -- touch every bank once.
+template <int D>
+__device__ __forceinline__ uint32_t swizzle(int t, int c) {
+  if constexpr (D == 128)
+    return ((t >> 1) << 7) + (((t ^ (t >> 2)) & 1) << 6) + ((c ^ (t & 2)) << 4);
+  else
+    return ((t >> 2) << 7) + (((t ^ ((t >> 2) << 1)) & 3) << 5) + (c << 4);
+}
+
+template <int D>
+struct Stage {
+  static constexpr int CODES = TOK * D / 2;           // bytes of 16 rows of codes
+  static constexpr int SCALES = TOK * D / FP4_GROUP;  // ... of scales
+  static constexpr int BYTES = 2 * CODES + 2 * SCALES;
+};
+
+// Row stride of a merged partial result in shared memory: d floats with one
+// more after every 16 (D/8 at d = 64), rounded so that the eight row groups and
+// four columns of a fragment fall into different banks.
+template <int D>
+__device__ __forceinline__ int merge_pos(int d) {
+  return d + d / (D / 8);
+}
+template <int D>
+constexpr int MERGE_ROW = D + 12;
+
+template <int D, int NT>
+constexpr int smem_bytes() {
+  constexpr int ring = WARPS * Shape<NT>::STAGES * Stage<D>::BYTES;
+  constexpr int merge = WARPS * 8 * NT * MERGE_ROW<D> * 4;
+  return ring > merge ? ring : merge;
+}
+
+// Where a CTA's piece of the line begins.
+struct Piece {
+  int begin, end;   // units
+  int b, base;      // sequence of `begin`, and the units before it
+  int per_cta;
+};
+
+// Cuts the line.  Every CTA adds up the lengths by itself: a few loads per
+// thread, no extra launch.
+__device__ __forceinline__ Piece cut(const DecArgs& a, int* sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int chunk = (a.batch + THREADS - 1) / THREADS;
+  const int b0 = min(a.batch, tid * chunk), b1 = min(a.batch, b0 + chunk);
+  const int per_unit = a.heads_kv * a.row_tiles;
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) sum += units_of(clamp_len(a, b));
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) sh[warp] = incl;
+  __syncthreads();
+  int before = incl - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) before += sh[w];
+    total += sh[w];
+  }
+  Piece p;
+  const int all = total * per_unit;
+  p.per_cta = max(MIN_UNITS, (all + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+  p.begin = static_cast<int>(min(static_cast<long long>(all),
+                                 static_cast<long long>(blockIdx.x) * p.per_cta));
+  p.end = min(all, p.begin + p.per_cta);
+  const int at = p.begin / per_unit;
+  if (at >= before && at < before + sum) {
+    int base = before;
+    for (int b = b0; b < b1; ++b) {
+      const int n = units_of(clamp_len(a, b));
+      if (at < base + n) {
+        sh[WARPS] = b;
+        sh[WARPS + 1] = base * per_unit;
+        break;
+      }
+      base += n;
+    }
+  }
+  __syncthreads();
+  p.b = sh[WARPS];
+  p.base = sh[WARPS + 1];
+  return p;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const DecArgs a) {
+  constexpr int STAGES = Shape<NT>::STAGES;
+  constexpr int KSTEPS = D / 16;  // 16-element steps of K Q^T
+  constexpr int MT = D / 16;      // 16-element row tiles of V^T P^T
+  constexpr int ROWS = 8 * NT;
+  using St = Stage<D>;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ int sh_cut[WARPS + 2];
+  __shared__ uint2 sh_q[NT * KSTEPS * 32];
+  __shared__ float sh_sc[ROWS];
+  __shared__ float2 sh_ml[WARPS][ROWS];
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, c = lane & 3;
+
+  Piece piece;
+  if (a.split) {
+    if (tid == 0) a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    piece = cut(a, sh_cut);
+  } else {  // one whole segment per CTA
+    piece.b = static_cast<int>(blockIdx.x) / (a.heads_kv * a.row_tiles);
+    const int n = units_of(clamp_len(a, piece.b));
+    piece.base = 0;
+    piece.begin = (static_cast<int>(blockIdx.x) - piece.b * a.heads_kv * a.row_tiles) * n;
+    piece.end = piece.begin + n;
+    piece.per_cta = n;
+  }
+
+  const uint32_t my_ring = smem_u32(ring) + warp * STAGES * St::BYTES;
+  int u = piece.begin, b = piece.b, base = piece.base;
+  while (u < piece.end) {
+    const int len = clamp_len(a, b);
+    const int n_units = units_of(len);
+    const int seg = (u - base) / n_units;  // kvh * row_tiles + row tile
+    const int u0 = u - base - seg * n_units;
+    const int u1 = min(n_units, u0 + piece.end - u);
+    const int kvh = seg / a.row_tiles;
+    const int r0 = (seg - kvh * a.row_tiles) * ROWS;  // first query row
+    const int n_rows = min(ROWS, a.rows - r0);
+
+    // Positions that the rows of this tile see: each row its own limit, all of
+    // them below max_lim, and everything below min_lim by all.
+    const int first_i = r0 / a.group, last_i = (r0 + n_rows - 1) / a.group;
+    const int min_lim = a.causal ? max(0, len - a.q_len + first_i + 1) : len;
+    const int max_lim = a.causal ? max(0, len - a.q_len + last_i + 1) : len;
+
+    // ---- this warp's tiles: u0 * WARPS + warp, and every WARPS-th after it
+    const int t_begin = u0 * WARPS + warp;
+    const int t_end = min(u1 * WARPS, (max_lim + TOK - 1) / TOK);
+    const int n_tiles = t_begin < t_end ? (t_end - t_begin + WARPS - 1) / WARPS : 0;
+
+    const int32_t* table = a.table + static_cast<long long>(b) * a.table_stride;
+    const uint8_t* kc = a.kc + kvh * a.kc_s[1];
+    const uint8_t* vc = a.vc + kvh * a.vc_s[1];
+    // Lanes 0-15 copy the keys' scales of a token each, lanes 16-31 the values'.
+    const uint8_t* sc_src = lane < 16 ? a.ks + kvh * a.ks_s[1] + (lane & 15) * a.ks_s[2]
+                                      : a.vs + kvh * a.vs_s[1] + (lane & 15) * a.vs_s[2];
+    const long long sc_page = lane < 16 ? a.ks_s[0] : a.vs_s[0];
+    const long long sc_tok = lane < 16 ? a.ks_s[2] : a.vs_s[2];
+
+    // Prefetch cursor: the next tile to copy, as page column and tile in it.
+    int pf_tile = t_begin;
+    int pf_col = t_begin / a.tiles_per_page;
+    int pf_off = t_begin - pf_col * a.tiles_per_page;
+    int pf_entry = pf_tile < t_end ? __ldg(table + pf_col) : -1;
+    auto copy_tile = [&](int slot) {
+      if (pf_tile < t_end) {
+        const bool ok = pf_entry >= 0 && pf_entry < a.num_pages;
+        const long long page = ok ? pf_entry : 0;
+        const int row = ok ? pf_off * TOK : 0;
+        const uint32_t dst = my_ring + slot * St::BYTES;
+        const uint8_t* k_src = kc + page * a.kc_s[0] + row * a.kc_s[2];
+        const uint8_t* v_src = vc + page * a.vc_s[0] + row * a.vc_s[2];
+        constexpr int CHUNKS = D / 32;  // 16-byte chunks of a row
+#pragma unroll
+        for (int j = 0; j < TOK * CHUNKS / 32; ++j) {
+          const int id = lane + 32 * j;
+          const int t = id / CHUNKS, ch = id % CHUNKS;
+          cp_async16(dst + swizzle<D>(t, ch), k_src + t * a.kc_s[2] + ch * 16, ok);
+          cp_async16(dst + St::CODES + swizzle<D>(t, ch), v_src + t * a.vc_s[2] + ch * 16, ok);
+        }
+        cp_async_small<D / FP4_GROUP>(dst + 2 * St::CODES + lane * (D / FP4_GROUP),
+                                      sc_src + page * sc_page + row * sc_tok, ok);
+        pf_tile += WARPS;
+        pf_off += WARPS;
+        while (pf_off >= a.tiles_per_page) {
+          pf_off -= a.tiles_per_page;
+          ++pf_col;
+        }
+        if (pf_tile < t_end) pf_entry = __ldg(table + pf_col);
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) copy_tile(s);
+
+    // ---- queries: fragments of Q^T (fp16, row scaled to [2^14, 2^15)) and the
+    // factor that turns a product into a score in log2 units
+    for (int nt = warp; nt < NT; nt += WARPS) {
+      const int r = r0 + nt * 8 + g;
+      float f[D / 4];
+      float amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 4; ++j) f[j] = 0.f;
+      if (r < a.rows) {
+        const int i = r / a.group, h = kvh * a.group + (r - i * a.group);
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + b * a.q_s[0] + h * a.q_s[1] +
+                                                          i * a.q_s[2] + c * (D / 4));
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          const uint4 x = __ldg(src + j);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 y = x2_to_f32(w[e], a.f16);
+            f[8 * j + 2 * e] = y.x;
+            f[8 * j + 2 * e + 1] = y.y;
+            amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
+          }
+        }
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // A row with an infinity or a NaN stays as it is: its scores are not
+      // numbers in any scaling.
+      const int ex = (__float_as_int(amax) >> 23) - 127;
+      const int up = amax == 0.f || ex > 127 ? 0 : min(14 - ex, 100);
+      const float mul = pow2f(up);
+      if (c == 0)
+        sh_sc[nt * 8 + g] = a.sigma_log2 * pow2f(-up) * pow2f(head_exp(a.kexp, kvh));
+#pragma unroll
+      for (int j = 0; j < KSTEPS; ++j)
+        sh_q[(nt * KSTEPS + j) * 32 + lane] =
+            make_uint2(pack_f16x2(f[4 * j] * mul, f[4 * j + 1] * mul),
+                       pack_f16x2(f[4 * j + 2] * mul, f[4 * j + 3] * mul));
+    }
+    __syncthreads();
+
+    // ---- per-lane columns: 2c and 2c + 1 of each row tile
+    float acc[NT][MT][4];
+    float ref[NT][2], sum[NT][2], sc[NT][2];
+    int lim[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[nt][mt][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = r0 + nt * 8 + 2 * c + e;
+        ref[nt][e] = -INFINITY;
+        sum[nt][e] = 0.f;
+        sc[nt][e] = sh_sc[nt * 8 + 2 * c + e];
+        // Rows past the last are computed along with the rest and not stored.
+        lim[nt][e] = !a.causal || r >= a.rows ? len : len - a.q_len + r / a.group + 1;
+      }
+    }
+    // Row m of a 8-token half tile is token 4 (m & 1) + (m >> 1), the order in
+    // which the values' fragments pair tokens.
+    const int my_tok = ((g & 1) << 2) + (g >> 1);
+
+    for (int n = 0; n < n_tiles; ++n) {
+      cp_async_wait<STAGES - 2>();
+      __syncwarp();  // every lane's copies of tile n are in, and tile n - 1 is read
+      copy_tile((n + STAGES - 1) % STAGES);
+      const uint8_t* stp = ring + (warp * STAGES + n % STAGES) * St::BYTES;
+      const int tok0 = (t_begin + n * WARPS) * TOK;
+      const bool masked = tok0 + TOK > min_lim;
+
+      // ---- S^T = K Q^T
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+      {
+        uint32_t ka[D / 32], kb[D / 32];  // d/4 codes of tokens my_tok, my_tok + 8
+        uint32_t sa[2], sb[2];            // their scales, each twice
+        const uint8_t* sk = stp + 2 * St::CODES;
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(stp + swizzle<D>(my_tok, c));
+          const uint4 y = *reinterpret_cast<const uint4*>(stp + swizzle<D>(my_tok + 8, c));
+          ka[0] = x.x, ka[1] = x.y, ka[2] = x.z, ka[3] = x.w;
+          kb[0] = y.x, kb[1] = y.y, kb[2] = y.z, kb[3] = y.w;
+          const uint32_t za = e4m3x2_to_f16(
+              *reinterpret_cast<const uint16_t*>(sk + my_tok * 8 + 2 * c));
+          const uint32_t zb = e4m3x2_to_f16(
+              *reinterpret_cast<const uint16_t*>(sk + (my_tok + 8) * 8 + 2 * c));
+          sa[0] = __byte_perm(za, 0, 0x1010), sa[1] = __byte_perm(za, 0, 0x3232);
+          sb[0] = __byte_perm(zb, 0, 0x1010), sb[1] = __byte_perm(zb, 0, 0x3232);
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(stp + swizzle<D>(my_tok, c >> 1) +
+                                                          (c & 1) * 8);
+          const uint2 y = *reinterpret_cast<const uint2*>(stp + swizzle<D>(my_tok + 8, c >> 1) +
+                                                          (c & 1) * 8);
+          ka[0] = x.x, ka[1] = x.y;
+          kb[0] = y.x, kb[1] = y.y;
+          const uint32_t za = e4m3x2_to_f16(sk[my_tok * 4 + c]);
+          const uint32_t zb = e4m3x2_to_f16(sk[(my_tok + 8) * 4 + c]);
+          sa[0] = sa[1] = __byte_perm(za, 0, 0x1010);
+          sb[0] = sb[1] = __byte_perm(zb, 0, 0x1010);
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          uint32_t fa[4], fb[4];
+          e2m1x8_to_f16(ka[w], fa);
+          e2m1x8_to_f16(kb[w], fb);
+          const uint32_t xa = sa[w >> 1], xb = sb[w >> 1];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            fa[j] = mul_f16x2(fa[j], xa);
+            fb[j] = mul_f16x2(fb[j], xb);
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint2 qf = sh_q[(nt * KSTEPS + 2 * w + j) * 32 + lane];
+              mma_f16_16816(s[nt], fa[2 * j], fb[2 * j], fa[2 * j + 1], fb[2 * j + 1], qf.x, qf.y);
+            }
+        }
+      }
+
+      // ---- scores, masks, reference
+      bool over = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] *= sc[nt][e & 1];
+        if (masked) {
+          const int ta = tok0 + my_tok, tb = ta + 8;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (ta >= lim[nt][e]) s[nt][e] = -INFINITY;
+            if (tb >= lim[nt][e]) s[nt][e + 2] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) over |= s[nt][e] > ref[nt][e & 1] + HEADROOM;
+      }
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(s[nt][e], s[nt][e + 2]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float m1 = fmaxf(ref[nt][e], mx);
+            const float f = m1 == -INFINITY ? 1.f : ex2_approx(ref[nt][e] - m1);
+            ref[nt][e] = m1;
+            sum[nt][e] *= f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              acc[nt][mt][e] *= f;
+              acc[nt][mt][e + 2] *= f;
+            }
+          }
+      }
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float z0 = (ref[nt][0] == -INFINITY ? 0.f : ref[nt][0]) - SHIFT;
+        const float z1 = (ref[nt][1] == -INFINITY ? 0.f : ref[nt][1]) - SHIFT;
+        const float p0 = ex2_approx(s[nt][0] - z0), p1 = ex2_approx(s[nt][1] - z1);
+        const float p2 = ex2_approx(s[nt][2] - z0), p3 = ex2_approx(s[nt][3] - z1);
+        sum[nt][0] += p0 + p2;
+        sum[nt][1] += p1 + p3;
+        pb[nt][0] = movmatrix_trans(pack_f16x2(p0, p1));
+        pb[nt][1] = movmatrix_trans(pack_f16x2(p2, p3));
+      }
+
+      // ---- O^T += V^T P^T
+      {
+        // This lane: elements [g * d/8, (g + 1) * d/8) of tokens c + 4j.
+        const uint8_t* vp = stp + St::CODES;
+        const uint8_t* sv = stp + 2 * St::CODES + St::SCALES;
+        uint32_t v[4][D / 64], z[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t = c + 4 * j;
+          if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(vp + swizzle<D>(t, g >> 1) +
+                                                            (g & 1) * 8);
+            v[j][0] = x.x, v[j][1] = x.y;
+            z[j] = sv[t * 8 + g];
+          } else {
+            v[j][0] = *reinterpret_cast<const uint32_t*>(vp + swizzle<D>(t, g >> 2) +
+                                                         (g & 3) * 4);
+            z[j] = sv[t * 4 + (g >> 1)];
+          }
+        }
+        if (masked) {
+          // A hidden value weighs nothing even where it is not a number: past
+          // max_lim the scale becomes 0.  Below it, a NaN that only some rows
+          // see is taken out and put into those rows.
+          uint32_t nans = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int t = c + 4 * j;
+            if (tok0 + t >= max_lim) z[j] = 0;
+            if ((z[j] & 0x7fu) == 0x7fu) {
+              z[j] = 0;
+              nans |= 1u << t;
+            }
+          }
+          if (__any_sync(0xffffffffu, nans != 0)) {
+            nans |= __shfl_xor_sync(0xffffffffu, nans, 1);
+            nans |= __shfl_xor_sync(0xffffffffu, nans, 2);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int seen = min(max(lim[nt][e] - tok0, 0), TOK);
+                if (nans & ((1u << seen) - 1u)) {
+#pragma unroll
+                  for (int mt = 0; mt < MT; ++mt)
+                    acc[nt][mt][e] = acc[nt][mt][e + 2] = NAN;
+                }
+              }
+          }
+        }
+        const uint32_t z01 = e4m3x2_to_f16(z[0] | z[1] << 8);
+        const uint32_t z23 = e4m3x2_to_f16(z[2] | z[3] << 8);
+#pragma unroll
+        for (int w = 0; w < D / 64; ++w) {
+          // f16x2 fragments want {token 4j', token 4j' + 4} of one element.
+          const uint32_t even01 = (v[0][w] & 0x0f0f0f0fu) | ((v[1][w] << 4) & 0xf0f0f0f0u);
+          const uint32_t odd01 = ((v[0][w] >> 4) & 0x0f0f0f0fu) | (v[1][w] & 0xf0f0f0f0u);
+          const uint32_t even23 = (v[2][w] & 0x0f0f0f0fu) | ((v[3][w] << 4) & 0xf0f0f0f0u);
+          const uint32_t odd23 = ((v[2][w] >> 4) & 0x0f0f0f0fu) | (v[3][w] & 0xf0f0f0f0u);
+          uint32_t a0[4], a1[4], a2[4], a3[4];
+          e2m1x8_to_f16(even01, a0);
+          e2m1x8_to_f16(odd01, a1);
+          e2m1x8_to_f16(even23, a2);
+          e2m1x8_to_f16(odd23, a3);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t x0 = mul_f16x2(a0[j], z01), x1 = mul_f16x2(a1[j], z01);
+            const uint32_t x2 = mul_f16x2(a2[j], z23), x3 = mul_f16x2(a3[j], z23);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16_16816(acc[nt][4 * w + j], x0, x1, x2, x3, pb[nt][0], pb[nt][1]);
+          }
+        }
+      }
+    }
+    cp_async_wait<0>();
+
+    // ---- join the warps: common reference, then one sum of the scaled parts
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = sum[nt][e];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (g == 0) sh_ml[warp][nt * 8 + 2 * c + e] = make_float2(ref[nt][e], l);
+      }
+    __syncthreads();  // also: every warp is done with its ring, which the sums reuse
+    float* merge = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = nt * 8 + 2 * c + e;
+        float m = sh_ml[0][r].x;
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w) m = fmaxf(m, sh_ml[w][r].x);
+        const float f = m == -INFINITY ? 1.f : ex2_approx(ref[nt][e] - m);
+        float* dst = merge + (warp * ROWS + r) * MERGE_ROW<D>;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          dst[merge_pos<D>(g * (D / 8) + 2 * mt)] = acc[nt][mt][e] * f;
+          dst[merge_pos<D>(g * (D / 8) + 2 * mt + 1)] = acc[nt][mt][e + 2] * f;
+        }
+      }
+    __syncthreads();
+    const bool whole = u0 == 0 && u1 == n_units;
+    const int part = 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0);
+    const float v_up = pow2f(head_exp(a.vexp, kvh));
+    for (int x = tid; x < n_rows * (D / 8); x += THREADS) {
+      const int r = x / (D / 8), d0 = (x % (D / 8)) * 8;
+      float m = sh_ml[0][r].x;
+#pragma unroll
+      for (int w = 1; w < WARPS; ++w) m = fmaxf(m, sh_ml[w][r].x);
+      float l = 0.f, y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float2 ml = sh_ml[w][r];
+        l += m == -INFINITY ? ml.y : ml.y * ex2_approx(ml.x - m);
+        const float* src = merge + (w * ROWS + r) * MERGE_ROW<D> + merge_pos<D>(d0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] += src[e];
+      }
+      if (whole) {
+        const int row = r0 + r, i = row / a.group, h = kvh * a.group + (row - i * a.group);
+        const float inv = l == 0.f ? 0.f : v_up / l;
+        uint4 w;
+        w.x = f32_to_x2(y[0] * inv, y[1] * inv, a.f16);
+        w.y = f32_to_x2(y[2] * inv, y[3] * inv, a.f16);
+        w.z = f32_to_x2(y[4] * inv, y[5] * inv, a.f16);
+        w.w = f32_to_x2(y[6] * inv, y[7] * inv, a.f16);
+        *reinterpret_cast<uint4*>(a.o + b * a.o_s[0] + h * a.o_s[1] + i * a.o_s[2] + d0) = w;
+        if (a.lse != nullptr && d0 == 0)
+          a.lse[h * a.lse_pitch + static_cast<long long>(b) * a.q_len + i] =
+              l == 0.f ? -INFINITY : (m - SHIFT + log2f(l)) * 0.6931471805599453f;
+      } else {
+        float4* dst = reinterpret_cast<float4*>(
+            a.part_o + (static_cast<long long>(part) * ROWS + r) * D + d0);
+        dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+        dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+        if (d0 == 0) a.part_ml[static_cast<long long>(part) * ROWS + r] = make_float2(m, l);
+      }
+    }
+    if (!whole && u0 == 0 && tid == 0)
+      a.joins[blockIdx.x] = make_int4(b, seg, (u + n_units - 1) / piece.per_cta, 0);
+    __syncthreads();  // the ring and sh_ml are free again
+
+    u += u1 - u0;
+    if (u1 == n_units && seg == a.heads_kv * a.row_tiles - 1) {
+      base += n_units * a.heads_kv * a.row_tiles;
+      ++b;
+    }
+  }
+}
+
+// Joins the parts of the segments that a cut crossed: block (x, r) takes row r
+// of the segment that CTA x began and did not finish, if there is one.  The
+// parts lie in the CTAs x (its second slot) .. last (their first slots).
+template <int D, int ROWS>
+__global__ void __launch_bounds__(THREADS) decode4_join_kernel(const DecArgs a) {
+  constexpr int LANES = D / 4;              // threads that cover a row, four elements each
+  constexpr int PARTS = THREADS / LANES;    // parts read at once
+  __shared__ float4 sh_y[PARTS][LANES];
+  __shared__ float2 sh_ml[PARTS];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 job = a.joins[blockIdx.x];
+  if (job.x < 0) return;
+  const int b = job.x, kvh = job.y / a.row_tiles;
+  const int r = blockIdx.y, row = (job.y - kvh * a.row_tiles) * ROWS + r;
+  if (row >= a.rows) return;
+  const int first = blockIdx.x, count = job.z - first + 1;
+  const int lane = threadIdx.x % LANES, p0 = threadIdx.x / LANES;
+  float m = -INFINITY, l = 0.f;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = p0; p < count; p += PARTS) {
+    const long long part = 2LL * (first + p) + (p == 0 ? 1 : 0);
+    const float2 ml = a.part_ml[part * ROWS + r];
+    const float4 x = reinterpret_cast<const float4*>(a.part_o + (part * ROWS + r) * D)[lane];
+    const float m1 = fmaxf(m, ml.x);
+    const float f = m1 == -INFINITY ? 1.f : ex2_approx(m - m1);
+    const float e = m1 == -INFINITY ? 1.f : ex2_approx(ml.x - m1);
+    m = m1;
+    l = l * f + ml.y * e;
+    y.x = y.x * f + x.x * e;
+    y.y = y.y * f + x.y * e;
+    y.z = y.z * f + x.z * e;
+    y.w = y.w * f + x.w * e;
+  }
+  sh_y[p0][lane] = y;
+  if (lane == 0) sh_ml[p0] = make_float2(m, l);
+  __syncthreads();
+  if (p0 != 0) return;
+#pragma unroll
+  for (int p = 1; p < PARTS; ++p) m = fmaxf(m, sh_ml[p].x);
+  l = 0.f;
+  y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p) {
+    const float2 ml = sh_ml[p];
+    const float e = m == -INFINITY ? 1.f : ex2_approx(ml.x - m);
+    const float4 x = sh_y[p][lane];
+    l += ml.y * e;
+    y.x += x.x * e;
+    y.y += x.y * e;
+    y.z += x.z * e;
+    y.w += x.w * e;
+  }
+  const int i = row / a.group, h = kvh * a.group + (row - i * a.group);
+  const float inv = l == 0.f ? 0.f : pow2f(head_exp(a.vexp, kvh)) / l;
+  uint2 w;
+  w.x = f32_to_x2(y.x * inv, y.y * inv, a.f16);
+  w.y = f32_to_x2(y.z * inv, y.w * inv, a.f16);
+  *reinterpret_cast<uint2*>(a.o + b * a.o_s[0] + h * a.o_s[1] + i * a.o_s[2] + 4 * lane) = w;
+  if (a.lse != nullptr && lane == 0)
+    a.lse[h * a.lse_pitch + static_cast<long long>(b) * a.q_len + i] =
+        l == 0.f ? -INFINITY : (m - SHIFT + log2f(l)) * 0.6931471805599453f;
+}
+
+// Query row tiles of a call: as few tensor-core columns as hold its rows, up
+// to 32 to a CTA.
+struct Plan {
+  int nt, row_tiles, units, max_grid;
+  long long all_units;
+  bool split;
+};
+
+Plan plan_of(const bsfa_cache4* c, const bsfa_decode4_params* p) {
+  Plan pl;
+  const long long rows = static_cast<long long>(p->num_heads_q / c->num_heads_kv) * p->q_len;
+  pl.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  pl.row_tiles = static_cast<int>((rows + 8 * pl.nt - 1) / (8 * pl.nt));
+  pl.units = (p->max_seqlen + UNIT - 1) / UNIT;
+  if (pl.units < 1) pl.units = 1;
+  pl.all_units = static_cast<long long>(p->batch) * c->num_heads_kv * pl.row_tiles * pl.units;
+  pl.max_grid = pl.nt == 1 ? Shape<1>::MAX_GRID : pl.nt == 2 ? Shape<2>::MAX_GRID
+                                                             : Shape<4>::MAX_GRID;
+  // A segment of so few units is one CTA's work: no parts, no second kernel.
+  pl.split = pl.units > 2 * MIN_UNITS;
+  return pl;
+}
+
+struct Carve {
+  size_t part_o, part_ml, joins, bytes;
+};
+
+Carve carve(const Plan& pl, int d) {
+  Carve c{};
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t grid = pl.split ? static_cast<size_t>(pl.max_grid) : 0, rows = 8u * pl.nt;
+  c.part_o = 0;
+  c.part_ml = up(c.part_o + grid * 2 * rows * d * sizeof(float));
+  c.joins = up(c.part_ml + grid * 2 * rows * sizeof(float2));
+  c.bytes = up(c.joins + grid * sizeof(int4));
+  if (c.bytes == 0) c.bytes = 256;
+  return c;
+}
+
+bsfa_status validate_sizes(const bsfa_cache4* c, const bsfa_decode4_params* p) {
+  if (c == nullptr || p == nullptr) return BSFA_ERR_INVALID_ARG;
+  if (p->batch < 0 || p->q_len < 0 || p->max_seqlen < 0) return BSFA_ERR_INVALID_ARG;
+  const bsfa_status v = validate_cache4(c);
+  if (v != BSFA_OK) return v;
+  if (p->num_heads_q <= 0 || p->num_heads_q % c->num_heads_kv) return BSFA_ERR_INVALID_ARG;
+  if (p->dtype != BSFA_DTYPE_BF16 && p->dtype != BSFA_DTYPE_F16) return BSFA_ERR_UNSUPPORTED;
+  if (p->batch > CACHE4_MAX_BATCH) return BSFA_ERR_UNSUPPORTED;
+  if (p->max_seqlen > static_cast<long long>(c->block_table_width) * c->page_size)
+    return BSFA_ERR_INVALID_ARG;
+  const long long rows = static_cast<long long>(p->num_heads_q / c->num_heads_kv) * p->q_len;
+  if (rows > (1 << 24) || plan_of(c, p).all_units > 0x7fffffffLL - 4096) return BSFA_ERR_UNSUPPORTED;
+  return BSFA_OK;
+}
+
+template <int D, int NT>
+bsfa_status launch(const DecArgs& a, const Plan& pl, int sms, int dev, cudaStream_t stream) {
+  constexpr int smem = smem_bytes<D, NT>();
+  // The shared-memory size of a kernel is set once per device.
+  static std::atomic<uint64_t> ready{0};
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    if (cudaFuncSetAttribute(decode4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem) != cudaSuccess)
+      return BSFA_ERR_CUDA;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  long long grid = static_cast<long long>(a.batch) * a.heads_kv * a.row_tiles;
+  if (pl.split) {
+    const long long full = static_cast<long long>(sms) * Shape<NT>::CTAS;
+    grid = full < pl.max_grid ? full : pl.max_grid;
+    const long long most = (pl.all_units + MIN_UNITS - 1) / MIN_UNITS;
+    if (most < grid) grid = most;
+  }
+  decode4_kernel<D, NT><<<static_cast<unsigned>(grid), THREADS, smem, stream>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return BSFA_ERR_CUDA;
+  if (!pl.split) return BSFA_OK;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), a.rows < 8 * NT ? a.rows : 8 * NT);
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode4_join_kernel<D, 8 * NT>, a) == cudaSuccess
+             ? BSFA_OK
+             : BSFA_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace bsfa
+
+using namespace bsfa;
+
+extern "C" {
+
+size_t bsfa_decode4_workspace_size(const bsfa_cache4* cache, const bsfa_decode4_params* p) {
+  if (validate_sizes(cache, p) != BSFA_OK) return 0;
+  return carve(plan_of(cache, p), cache->head_dim).bytes;
+}
+
+bsfa_status bsfa_decode4(const bsfa_cache4* cache, const bsfa_decode4_params* p,
+                         bsfa_stream_t stream_) {
+  bsfa_status v = validate_sizes(cache, p);
+  if (v != BSFA_OK) return v;
+  if (p->batch == 0 || p->q_len == 0) return BSFA_OK;
+  v = validate_cache4_pointers(cache);
+  if (v != BSFA_OK) return v;
+  if (!p->q || !p->o || !p->seqlens) return BSFA_ERR_INVALID_ARG;
+  const int64_t extent[3] = {p->batch, p->num_heads_q, p->q_len};
+  if (!rows_aligned(p->q, p->q_stride, extent) || !rows_aligned(p->o, p->o_stride, extent))
+    return BSFA_ERR_UNSUPPORTED;
+  const Plan pl = plan_of(cache, p);
+  const Carve cv = carve(pl, cache->head_dim);
+  if (p->workspace == nullptr || (reinterpret_cast<uintptr_t>(p->workspace) & 255u) ||
+      p->workspace_bytes < cv.bytes)
+    return BSFA_ERR_WORKSPACE;
+
+  DecArgs a{};
+  a.kc = cache->k;
+  a.vc = cache->v;
+  a.ks = cache->k_scale;
+  a.vs = cache->v_scale;
+  a.kexp = cache->k_exp;
+  a.vexp = cache->v_exp;
+  for (int i = 0; i < 3; ++i) {
+    a.kc_s[i] = cache->k_stride[i];
+    a.vc_s[i] = cache->v_stride[i];
+    a.ks_s[i] = cache->k_scale_stride[i];
+    a.vs_s[i] = cache->v_scale_stride[i];
+    a.q_s[i] = p->q_stride[i];
+    a.o_s[i] = p->o_stride[i];
+  }
+  a.table = cache->block_table;
+  a.table_stride = cache->block_table_stride;
+  a.num_pages = cache->num_pages;
+  a.tiles_per_page = cache->page_size / TOK;
+  a.q = static_cast<const uint16_t*>(p->q);
+  a.o = static_cast<uint16_t*>(p->o);
+  a.seqlens = p->seqlens;
+  a.batch = p->batch;
+  a.heads_kv = cache->num_heads_kv;
+  a.group = p->num_heads_q / cache->num_heads_kv;
+  a.q_len = p->q_len;
+  a.rows = a.group * p->q_len;
+  a.row_tiles = pl.row_tiles;
+  a.max_len = p->max_seqlen;
+  a.causal = p->causal != 0;
+  a.f16 = p->dtype == BSFA_DTYPE_F16;
+  a.split = pl.split;
+  const float sigma =
+      p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt((float)cache->head_dim);
+  a.sigma_log2 = sigma * 1.4426950408889634f;
+  a.lse = p->lse;
+  a.lse_pitch = static_cast<long long>(p->batch) * p->q_len;
+  uint8_t* ws = static_cast<uint8_t*>(p->workspace);
+  a.part_o = reinterpret_cast<float*>(ws + cv.part_o);
+  a.part_ml = reinterpret_cast<float2*>(ws + cv.part_ml);
+  a.joins = reinterpret_cast<int4*>(ws + cv.joins);
+
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+    return BSFA_ERR_CUDA;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (cache->head_dim == 128)
+    return pl.nt == 1   ? launch<128, 1>(a, pl, sms, dev, stream)
+           : pl.nt == 2 ? launch<128, 2>(a, pl, sms, dev, stream)
+                        : launch<128, 4>(a, pl, sms, dev, stream);
+  return pl.nt == 1   ? launch<64, 1>(a, pl, sms, dev, stream)
+         : pl.nt == 2 ? launch<64, 2>(a, pl, sms, dev, stream)
+                      : launch<64, 4>(a, pl, sms, dev, stream);
+}
+
+}  // extern "C"

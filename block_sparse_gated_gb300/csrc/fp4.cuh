@@ -1,0 +1,133 @@
+// fp4.cuh -- one-instruction wrappers for the 4-bit cache kernels: e2m1 and
+// e4m3 conversions, the warp-level fp16 matrix product, 16-byte asynchronous
+// copies.
+#pragma once
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace bsfa {
+
+constexpr int FP4_GROUP = 16;  // elements that share an e4m3 scale
+
+// Eight e2m1 codes (element 0 in the low bits) as four f16x2: r[i] = {element
+// 2i (low half), element 2i + 1}.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+
+// Eight floats as e2m1 codes, element 0 in the low bits; nearest, ties to the
+// even code, magnitudes saturate at 6.
+__device__ __forceinline__ uint32_t f32x8_to_e2m1(const float* f) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+  return w;
+}
+
+// Two e4m3 bytes (low byte first) as f16x2; 0x7f and 0xff become NaN.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t two_bytes) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}"
+      : "=r"(r)
+      : "r"(two_bytes));
+  return r;
+}
+
+// A float as an e4m3 byte, nearest, ties to even, saturating at 448.
+__device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %2, %1;\n\tcvt.u32.u16 %0, h;\n\t}"
+      : "=r"(r)
+      : "f"(x), "f"(0.f));
+  return r & 0xffu;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ float2 f16x2_to_f32(uint32_t x) {
+  float2 r;
+  asm("{\n\t.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "cvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(x));
+  return r;
+}
+
+// The two 16-bit elements of a word as floats (bf16, or fp16 where `f16`).
+__device__ __forceinline__ float2 x2_to_f32(uint32_t x, bool f16) {
+  if (f16) return f16x2_to_f32(x);
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+
+// Two floats rounded to 16 bits.
+__device__ __forceinline__ uint32_t f32_to_x2(float lo, float hi, bool f16) {
+  return f16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+}
+
+// 2^k as a float, k in [-126, 127].
+__device__ __forceinline__ float pow2f(int k) { return __int_as_float((k + 127) << 23); }
+
+// A head's exponent, clamped to the documented range; 0 where there is none.
+__device__ __forceinline__ int head_exp(const int32_t* e, int head) {
+  return e == nullptr ? 0 : max(-100, min(100, __ldg(e + head)));
+}
+
+// c += A (16 x 16, row major) * B (16 x 8, column major) in fp16 with fp32 sums.
+// Lane 4g + c holds A rows g, g + 8 at columns {2c, 2c+1}, {2c+8, 2c+9}
+// (a0, a1: rows at the first pair; a2, a3: at the second), B column g at the
+// same rows (b0, b1), and C rows g, g + 8 at columns {2c, 2c+1}.
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8 x 8 matrix of 16-bit elements held two to a lane.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// Asynchronous copies global -> shared; `ok` false writes zeros and reads nothing.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool ok) {
+  static_assert(BYTES == 4 || BYTES == 8, "copies of 4 or 8 bytes");
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES),
+               "r"(ok ? BYTES : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+}  // namespace bsfa

@@ -287,6 +287,129 @@ bsfa_status bsfa_calibrate(const void* const* q_samples, const void* const* k_sa
                            const int* ks, int n_k, float* thresholds_out,
                            void* workspace, size_t workspace_bytes, bsfa_stream_t stream);
 
+/*
+ * ------------------------------------------------------------ 4-bit K/V cache
+ * bsfa_cache4_write, bsfa_cache4_read and bsfa_decode4 keep the keys and values
+ * of a prefill in a paged cache of 4-bit values and attend to it with the
+ * tokens that follow: quantise as the cache is written, read it back in 16
+ * bits, and attention of one or a few new tokens per sequence over it.
+ *
+ * Format.  A cached row is one token of one KV head: head_dim e2m1 codes, two
+ * to a byte (the even element in the low four bits: sign, two exponent bits,
+ * one mantissa bit; magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6), and one e4m3 scale
+ * (4 exponent bits with bias 7, 3 mantissa bits, 0x7f = NaN) for every 16
+ * consecutive elements.  With one exponent e per KV head (0 where k_exp or
+ * v_exp is NULL) element i of a row stands for
+ *     code[i] * scale[i / 16] * 2^e,
+ * a value of at most 6 significant bits, so bf16 and fp16 hold it exactly
+ * within their ranges.  72 bytes at head_dim 128 where 16-bit rows take 256.
+ *
+ * Writing.  With x' = x * 2^-e and a the largest |x'| of the 16 elements,
+ *     scale = min(max(e4m3(a / 6), 2^-9), 448),  code = e2m1(x' / scale),
+ * both rounded to nearest, ties to the even code; magnitudes beyond 6 scales
+ * saturate.  A group that holds an infinity or a NaN is stored as scale NaN
+ * and reads back as NaN.  Scales keep 3 mantissa bits for a in [0.09, 2880];
+ * exponents move that window to a head's values (e = ceil(log2(amax / 2688))
+ * puts the largest value amax of a head at its top).  A value that rounds to
+ * zero loses its sign.
+ */
+typedef struct {
+  uint8_t* k;                 /* code bytes of the keys' pages */
+  uint8_t* v;                 /* ... and of the values' */
+  uint8_t* k_scale;           /* e4m3 scale bytes of the keys' pages */
+  uint8_t* v_scale;
+  const int32_t* k_exp;       /* device int32 [Hkv] head exponents, nullable (0); clamped to */
+  const int32_t* v_exp;       /* [-100, 100] */
+  /* Strides in BYTES as {page, head, token}: token t of page p of head h
+   * begins at base + p*stride[0] + h*stride[1] + t*stride[2].  Codes: bases
+   * and strides are multiples of 16; scales: multiples of head_dim / 16 (the
+   * bytes of a row). */
+  int64_t k_stride[3], v_stride[3], k_scale_stride[3], v_scale_stride[3];
+  int num_pages;              /* pages in each pool (>= 1) */
+  int page_size;              /* tokens per page: a positive multiple of 16 */
+  int num_heads_kv;           /* Hkv, at most 4096 */
+  int head_dim;               /* 64 or 128 */
+  /* Position pos of sequence b is token pos % page_size of page
+   * block_table[b*block_table_stride + pos/page_size].  An entry outside
+   * [0, num_pages), or a position outside [0, block_table_width*page_size),
+   * names no row: a write there is dropped, a read gives zeros, and attention
+   * sees a zero key and a zero value (a prefill's page table does the same). */
+  const int32_t* block_table; /* device int32 [batch][block_table_stride] */
+  int block_table_stride;     /* elements between two sequences' rows, >= width */
+  int block_table_width;      /* entries of each row that may be read */
+} bsfa_cache4;
+
+/* 16-bit rows that bsfa_cache4_write takes or bsfa_cache4_read gives.
+ * Layouts as in bsfa_fwd_params: batched (cu_seqlens == NULL, `seqlen` rows of
+ * each of `batch` sequences) or varlen (`seqlen` packed rows, sequence b owns
+ * [cu_seqlens[b], cu_seqlens[b+1]); rows outside every sequence are neither
+ * read nor written; offsets need not be checked by the caller: a row belongs
+ * to the last sequence that begins at or before it, if that one reaches it).
+ * Row i of sequence b is cache position start[b] + i. */
+typedef struct {
+  void* k;                    /* [.., Hkv, .., d], read by the write, written by the read */
+  void* v;
+  int64_t k_stride[3], v_stride[3]; /* {batch, head, token} in ELEMENTS, multiples of 8 */
+  int batch;                  /* 0 .. 4096 (0 is a no-op) */
+  int seqlen;                 /* rows per sequence (batched; batch * seqlen < 2^31) or in
+                                 total (varlen) */
+  const int32_t* cu_seqlens;  /* device int32 [batch+1], non-decreasing; nullable */
+  const int32_t* start;       /* device int32 [batch], nullable (0) */
+  int dtype;                  /* bsfa_dtype of k and v */
+} bsfa_cache4_rows;
+
+/* Quantises the rows into their cache positions, keys and values in one
+ * launch.  Positions of one call must differ: where two rows share one, it
+ * holds some mixture of the two. */
+bsfa_status bsfa_cache4_write(const bsfa_cache4* cache, const bsfa_cache4_rows* rows,
+                              bsfa_stream_t stream);
+
+/* The rows that the cache positions stand for, each rounded once to dtype
+ * (exact without head exponents). */
+bsfa_status bsfa_cache4_read(const bsfa_cache4* cache, const bsfa_cache4_rows* rows,
+                             bsfa_stream_t stream);
+
+/*
+ * Attention of q_len new tokens of each sequence over its cached keys and
+ * values (the new tokens' own rows are in the cache already).  Query i of
+ * sequence b attends to positions t <= seqlens[b] - q_len + i (causal) or to
+ * every t < seqlens[b].  A query without a visible position (an empty
+ * sequence, or seqlens[b] < q_len) gives zeros and a log-sum-exp of -inf.
+ * seqlens stays on the device; entries are clamped to [0, max_seqlen].
+ *
+ * Products run on the tensor cores in fp16 with fp32 accumulation: cached
+ * values are exact in fp16, queries are scaled per row by a power of two, and
+ * the weights are rounded to fp16 (11 bits).  O is rounded to dtype once.
+ */
+typedef struct {
+  const void* q;              /* [batch, Hq, q_len, d] by strides */
+  void* o;                    /* same shape */
+  int64_t q_stride[3], o_stride[3]; /* {batch, head, token} in ELEMENTS, multiples of 8 */
+  int batch;                  /* 0 .. 4096 (0 is a no-op) */
+  int num_heads_q;            /* Hq, a multiple of Hkv; q-head h reads KV head h / (Hq/Hkv) */
+  int q_len;                  /* new tokens per sequence (0 is a no-op) */
+  const int32_t* seqlens;     /* device int32 [batch]: cached tokens, the new ones included */
+  int max_seqlen;             /* an upper bound on them, <= block_table_width * page_size */
+  float softmax_scale;        /* <= 0 selects 1/sqrt(d) */
+  int causal;                 /* nonzero: as above; 0: every cached position is visible */
+  float* lse;                 /* nullable device fp32 [Hq][batch*q_len]: natural-log
+                                 log-sum-exp of the visible scaled scores, row b*q_len + i */
+  void* workspace;            /* device scratch, >= bsfa_decode4_workspace_size bytes,
+                                 256-byte aligned; its contents are not preserved.  Calls that
+                                 may overlap on the GPU need separate workspaces. */
+  size_t workspace_bytes;
+  int dtype;                  /* bsfa_dtype of q and o */
+} bsfa_decode4_params;
+
+/* Bytes of workspace bsfa_decode4 needs (reads shape fields only; 0 for
+ * invalid parameters). */
+size_t bsfa_decode4_workspace_size(const bsfa_cache4* cache, const bsfa_decode4_params* p);
+
+/* Limits (BSFA_ERR_UNSUPPORTED beyond them): 4096 sequences, and
+ * batch * Hkv * (query row tiles) * ceil(max_seqlen / 64) < 2^31. */
+bsfa_status bsfa_decode4(const bsfa_cache4* cache, const bsfa_decode4_params* p,
+                         bsfa_stream_t stream);
+
 /* Synchronises `stream`, then reports (and clears) the device error word set
  * by a kernel whose bounded wait ran out.  *code receives the raw word (0 if
  * none).  Returns BSFA_ERR_DEVICE_TIMEOUT if it was set, BSFA_ERR_CUDA if the

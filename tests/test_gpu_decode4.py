@@ -1,0 +1,295 @@
+"""Attention of new tokens over the 4-bit cache against the fp64 oracle, with
+the elementwise bound that the kernel's arithmetic allows."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import cache4_util as cu
+
+pytestmark = pytest.mark.gpu
+
+BF, HF = torch.bfloat16, torch.float16
+
+
+def _bsfa():
+    import block_sparse_gated_gb300 as b
+    return b
+
+
+def _queries(B, Hq, n, d, dtype, seed, device, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(B, Hq, n, d, generator=g) * scale).to(dtype).to(device)
+
+
+def _i32(x, device):
+    return torch.tensor(x, dtype=torch.int32, device=device)
+
+
+# (heads q, heads kv, query tokens): rows of one KV head 1 .. 40, so that every
+# width of the query row tile and more than one tile of them occur.
+HEADS = [(2, 2, 1), (8, 2, 1), (8, 1, 1), (9, 3, 2), (12, 1, 1), (4, 1, 4), (8, 2, 5), (6, 2, 8),
+         (8, 1, 5)]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("short", [True, False])
+def test_against_the_oracle(cuda_device, d, heads, short):
+    """Ragged batches from an empty sequence to several pieces per sequence;
+    rows past each end hold NaN scales."""
+    b = _bsfa()
+    Hq, Hkv, n = heads
+    lens = [1, 0, 16, 250, 17] if short else [700, 1, 0, 64, 1301, 129]
+    page, layout = (16, "pthd") if (Hq + d) % 3 == 0 else (48, "phtd")
+    dtype = BF if n % 2 else HF
+    cache, table, rows = cu.random_cache(b, lens, page, Hkv, d, 10 * Hq + n, cuda_device,
+                                         layout=layout, exps=Hkv == 2)
+    q = _queries(len(lens), Hq, n, d, dtype, Hq, cuda_device, 1.5)
+    res = b.decode4(q, cache, table, _i32(lens, cuda_device), return_lse=True,
+                    max_seqlen=256 if short else None)
+    cu.check_decode(res, q, rows, lens, dtype, d)
+
+
+@pytest.mark.parametrize("length", [1, 2, 15, 16, 17, 63, 64, 65, 127, 256, 257, 511, 1000])
+def test_every_kind_of_length(cuda_device, length):
+    """One sequence, whole and cut, at tile, unit and page borders."""
+    b = _bsfa()
+    cache, table, rows = cu.random_cache(b, [length], 32, 2, 128, length, cuda_device)
+    q = _queries(1, 8, 1, 128, BF, length, cuda_device, 2.0)
+    for most in (None, length):
+        res = b.decode4(q, cache, table, _i32([length], cuda_device), return_lse=True,
+                        max_seqlen=most)
+        cu.check_decode(res, q, rows, [length], BF, 128)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n", [1, 3, 33, 100])
+def test_queries_longer_than_the_cache(cuda_device, causal, n):
+    """Rows that see nothing give zeros and -inf; without the causal mask every
+    row sees the whole cache."""
+    b = _bsfa()
+    lens = [2, 90, 0, 40]
+    cache, table, rows = cu.random_cache(b, lens, 16, 2, 64, n, cuda_device)
+    q = _queries(4, 4, n, 64, HF, n, cuda_device)
+    res = b.decode4(q, cache, table, _i32(lens, cuda_device), causal=causal, return_lse=True)
+    cu.check_decode(res, q, rows, lens, HF, 64, causal=causal)
+    if causal and n > 2:
+        assert not res["out"][0, :, :n - 2].any()
+        assert bool(torch.isneginf(res["lse"][:, :n - 2]).all())
+
+
+def test_layouts_strides_and_scale(cuda_device):
+    """q and out as [B, n, Hq, d], as slices, with gaps, one sequence in 3-D."""
+    b = _bsfa()
+    lens, d = [77, 300], 128
+    cache, table, rows = cu.random_cache(b, lens, 64, 2, d, 5, cuda_device)
+    n32 = _i32(lens, cuda_device)
+    big = _queries(2, 5, 12, d + 8, BF, 3, cuda_device)  # [B, tokens, heads + 4, d + 8]
+    q = big[:, 1:4, 2:10, 8:]
+    out = torch.full((2, 6, 10, d), 3.0, dtype=BF, device=cuda_device)
+    res = b.decode4(q, cache, table, n32, layout="blhd", out=out[:, 2:5, 1:9], softmax_scale=0.21,
+                    return_lse=True)
+    cu.check_decode({"out": res["out"].transpose(1, 2), "lse": res["lse"]}, q.transpose(1, 2),
+                    rows, lens, BF, d, sigma=float(np.float32(0.21)))
+    keep = torch.ones(2, 6, 10, dtype=torch.bool, device=cuda_device)
+    keep[:, 2:5, 1:9] = False
+    assert bool((out[keep] == 3.0).all())
+    one = b.decode4(q[1].transpose(0, 1), cache, table[1:], n32[1:], softmax_scale=0.21)["out"]
+    assert one.shape == (8, 3, d)
+    two = b.decode4(q[1:].transpose(1, 2).contiguous(), cache, table[1:], n32[1:],
+                    softmax_scale=0.21)["out"][0]
+    assert torch.equal(one, two)
+
+
+def test_lengths_beyond_the_bound_are_cut(cuda_device):
+    """Entries of seqlens past max_seqlen, past the table or below zero."""
+    b = _bsfa()
+    lens = [400, 400, 400, 400]
+    cache, table, rows = cu.random_cache(b, lens, 16, 1, 64, 8, cuda_device)
+    q = _queries(4, 4, 1, 64, BF, 8, cuda_device)
+    given = _i32([400, 1 << 30, -5, -(1 << 31)], cuda_device)
+    res = b.decode4(q, cache, table[:, :25], given, max_seqlen=390, return_lse=True)
+    cu.check_decode(res, q, rows, [390, 390, 0, 0], BF, 64)
+
+
+def test_entries_outside_the_pool_read_as_zero_rows(cuda_device):
+    """A position whose page does not exist is a zero key and a zero value."""
+    b = _bsfa()
+    lens = [200]
+    cache, table, rows = cu.random_cache(b, lens, 16, 2, 128, 12, cuda_device)
+    table[0, 3], table[0, 7], table[0, 12] = -1, cache.k.shape[0], 1 << 30
+    for k in rows[0]:
+        for j in (3, 7, 12):
+            k[:, 16 * j:16 * j + 16] = 0.0
+    q = _queries(1, 4, 1, 128, BF, 12, cuda_device)
+    res = b.decode4(q, cache, table, _i32(lens, cuda_device), return_lse=True)
+    cu.check_decode(res, q, rows, lens, BF, 128)
+
+
+@pytest.mark.parametrize("where", ["value", "key"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_rows_reach_only_the_queries_that_see_them(cuda_device, where, d):
+    """A group stored as NaN: a value poisons its 16 elements of the queries
+    that see the token, a key everything of them; no other query or element."""
+    b = _bsfa()
+    L, n = 85, 6
+    cache, table, rows = cu.random_cache(b, [L], 32, 1, d, 3, cuda_device)
+    q = _queries(1, 2, n, d, BF, 3, cuda_device)
+    clean = b.decode4(q, cache, table, _i32([L], cuda_device), return_lse=True)
+    t, group = 82, 2  # seen by queries i with 82 <= 85 - 6 + i, that is i >= 3
+    pool = cache.v_scale if where == "value" else cache.k_scale
+    pool.view(torch.uint8)[table[0, t // 32].item(), 0, t % 32, group] = 0x7F
+    got = b.decode4(q, cache, table, _i32([L], cuda_device), return_lse=True)
+    nan = torch.isnan(got["out"])
+    want = torch.zeros_like(nan)
+    if where == "value":
+        want[:, :, 3:, 32:48] = True
+        assert torch.equal(got["lse"], clean["lse"])
+    else:
+        want[:, :, 3:] = True
+    assert torch.equal(nan, want)
+    assert torch.equal(got["out"][~want], clean["out"][~want])
+    # the same token in an older place, seen by all
+    pool.view(torch.uint8)[table[0, 0].item(), 0, 4, group] = 0x7F
+    got = b.decode4(q, cache, table, _i32([L], cuda_device))
+    nan = torch.isnan(got["out"])
+    assert bool(nan[..., 32:48].all()) and bool(nan.all()) == (where == "key")
+
+
+def test_infinite_and_huge_queries(cuda_device):
+    """A row with an infinity or a NaN gives NaN (its scores are not numbers);
+    rows beside it are untouched; rows of any finite size are exact."""
+    b = _bsfa()
+    lens = [120]
+    cache, table, rows = cu.random_cache(b, lens, 16, 1, 64, 3, cuda_device)
+    q = _queries(1, 8, 1, 64, BF, 2, cuda_device)
+    clean = b.decode4(q, cache, table, _i32(lens, cuda_device))["out"]
+    bad = q.clone()
+    bad[0, 1, 0, 7], bad[0, 4, 0, 9] = float("nan"), float("inf")
+    got = b.decode4(bad, cache, table, _i32(lens, cuda_device))["out"]
+    nan = torch.isnan(got).all(-1)[0, :, 0].tolist()
+    assert nan == [i in (1, 4) for i in range(8)]
+    assert torch.equal(got[0, [0, 2, 3, 5, 6, 7]], clean[0, [0, 2, 3, 5, 6, 7]])
+    for power in (-60, -20, 20, 60):  # the score is the same: q up, sigma down
+        r = b.decode4(q * 2.0 ** power, cache, table, _i32(lens, cuda_device),
+                      softmax_scale=2.0 ** -power / 8, return_lse=True)
+        assert torch.equal(r["out"], clean)
+
+
+def test_sharp_and_flat_rows(cuda_device):
+    """Scores that rise along the sequence by thousands (the reference moves at
+    every tile), fall, or are all equal."""
+    b = _bsfa()
+    L, d = 900, 64
+    cache, table, rows = cu.random_cache(b, [L], 16, 1, d, 14, cuda_device)
+    q = torch.zeros(1, 4, 1, d, dtype=BF, device=cuda_device)
+    q[0, 0] = 400.0
+    q[0, 1] = -400.0
+    q[0, 2] = 0.0
+    q[0, 3] = 3.0
+    res = b.decode4(q, cache, table, _i32([L], cuda_device), return_lse=True)
+    cu.check_decode(res, q, rows, [L], BF, d)
+
+
+def test_runs_repeat_bit_for_bit_whatever_the_workspace_holds(cuda_device):
+    b = _bsfa()
+    from block_sparse_gated_gb300 import cache4
+    lens = [3000, 10, 777]
+    cache, table, rows = cu.random_cache(b, lens, 64, 2, 128, 4, cuda_device)
+    q = _queries(3, 16, 1, 128, BF, 4, cuda_device)
+    n32 = _i32(lens, cuda_device)
+    need = cache4.decode4_workspace_bytes(q, cache, table, n32)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=cuda_device)
+    first = b.decode4(q, cache, table, n32, workspace=ws, return_lse=True)
+    cu.check_decode(first, q, rows, lens, BF, 128)
+    for fill in (0x00, 0x3C, 0xFF):
+        ws.fill_(fill)
+        again = b.decode4(q, cache, table, n32, workspace=ws, return_lse=True)
+        assert torch.equal(again["out"], first["out"]) and torch.equal(again["lse"], first["lse"])
+    with pytest.raises(b.BsfaError, match="workspace"):
+        b.decode4(q, cache, table, n32, workspace=ws[:need - 256])
+
+
+def test_graphs_follow_the_lengths_and_streams_do_not_mix(cuda_device):
+    """A captured call reads the lengths at replay; two graphs with workspaces
+    of their own run on two streams at once."""
+    b = _bsfa()
+    from block_sparse_gated_gb300 import cache4
+    lens = [2000, 1500]
+    cache, table, rows = cu.random_cache(b, lens, 32, 2, 64, 21, cuda_device)
+    q = [_queries(2, 8, 1, 64, HF, s, cuda_device) for s in (1, 2)]
+    n32 = [_i32(lens, cuda_device) for _ in range(2)]
+    need = cache4.decode4_workspace_bytes(q[0], cache, table, n32[0])
+    ws = [torch.empty(need, dtype=torch.uint8, device=cuda_device) for _ in range(2)]
+    outs = [torch.empty_like(x) for x in q]
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            b.decode4(q[i], cache, table, n32[i], out=outs[i], workspace=ws[i])
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for now in ([2000, 1500], [3, 900], [0, 1], [1024, 64]):
+        for t in n32:
+            t.copy_(_i32(now, cuda_device))
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                for _ in range(3):
+                    g.replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            cu.check_decode({"out": outs[i]}, q[i], rows, now, HF, 64)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    r = b.decode4(q[0], cache, table, n32[0], stream=side)
+    side.synchronize()
+    assert torch.equal(r["out"], outs[0])
+
+
+def test_a_batch_of_many_short_and_one_long(cuda_device):
+    """300 sequences over more than one piece each, and pieces over many."""
+    b = _bsfa()
+    lens = [int(x) for x in np.random.default_rng(1).integers(0, 40, 299)] + [5000]
+    cache, table, rows = cu.random_cache(b, lens, 16, 1, 64, 2, cuda_device)
+    q = _queries(300, 2, 1, 64, BF, 2, cuda_device)
+    res = b.decode4(q, cache, table, _i32(lens, cuda_device), return_lse=True)
+    cu.check_decode(res, q, rows, lens, BF, 64)
+
+
+def test_prefill_then_decode_as_they_are_used(cuda_device):
+    """A prompt's prefill, its keys and values into the cache, then tokens one
+    at a time: each is written and attends to everything before it.  The same
+    rows read back and given to the prefill agree with the cache's attention
+    over all of them."""
+    b = _bsfa()
+    Hq, Hkv, L, steps, d, page = 8, 2, 300, 5, 128, 128
+    g = torch.Generator().manual_seed(31)
+    total = L + steps
+    q, k, v = (torch.randn(1, h, total, d, generator=g).to(BF).to(cuda_device)
+               for h in (Hq, Hkv, Hkv))
+    pages = math.ceil(total / page)
+    cache = b.cache4_empty(pages, Hkv, page, d, device=cuda_device)
+    table = torch.arange(pages, dtype=torch.int32, device=cuda_device).flip(0)[None].contiguous()
+    b.prefill(q[:, :, :L], k[:, :, :L], v[:, :, :L], mode="none")
+    b.cache4_write(cache, k[:, :, :L], v[:, :, :L], table)
+    n32 = _i32([L], cuda_device)
+    outs = []
+    for i in range(L, total):
+        b.cache4_write(cache, k[:, :, i:i + 1], v[:, :, i:i + 1], table, start=n32)
+        n32 += 1
+        outs.append(b.decode4(q[:, :, i:i + 1], cache, table, n32)["out"])
+    kr, vr = b.cache4_read(cache, table, seqlen=total)
+    rows = [(kr[0].cpu().double().numpy(), vr[0].cpu().double().numpy())]
+    for j, o in enumerate(outs):
+        cu.check_decode({"out": o}, q[:, :, L + j:L + j + 1], rows, [L + j + 1], BF, d)
+    whole = b.prefill(q, kr, vr, mode="none", return_lse=True)
+    chunk = b.decode4(q, cache, table, n32, return_lse=True)
+    cu.check_decode(chunk, q, rows, [total], BF, d)
+    # two kernels, each within bf16's rounding and the weights' of the truth
+    assert (whole["out"].float() - chunk["out"].float()).abs().max().item() < 2e-2
+    assert (whole["lse"] - chunk["lse"]).abs().max().item() < 2e-3
+    assert torch.equal(chunk["out"][:, :, -1:], outs[-1]) or \
+        (chunk["out"][:, :, -1:].float() - outs[-1].float()).abs().max().item() < 2e-2
