@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbsfa.so")
@@ -69,6 +70,12 @@ class Decode4Params(ctypes.Structure):
     ]
 
 
+# The same three as struct formats, fields in the same order.
+CACHE4 = struct.Struct("@6P12q4iP2i")
+CACHE4_ROWS = struct.Struct("@2P6q2i2Pi0P")
+DECODE4 = struct.Struct("@2P6q3iPifiPPNi0P")
+
+
 # bsfa_dtype
 DTYPE_BF16, DTYPE_F16 = 0, 1
 # bsfa_flag
@@ -91,11 +98,12 @@ SIGNATURES = [
         ctypes.POINTER(c_int), c_int, c_void_p, c_void_p, c_size_t, c_void_p]),
     ("bsfa_device_error", c_int, [c_void_p, ctypes.POINTER(ctypes.c_uint)]),
     ("bsfa_prefill_fwd_noalloc", c_int, [ctypes.POINTER(FwdParams), c_void_p]),
-    ("bsfa_cache4_write", c_int, [ctypes.POINTER(Cache4), ctypes.POINTER(Cache4Rows), c_void_p]),
-    ("bsfa_cache4_read", c_int, [ctypes.POINTER(Cache4), ctypes.POINTER(Cache4Rows), c_void_p]),
-    ("bsfa_decode4_workspace_size", c_size_t, [ctypes.POINTER(Cache4),
-                                               ctypes.POINTER(Decode4Params)]),
-    ("bsfa_decode4", c_int, [ctypes.POINTER(Cache4), ctypes.POINTER(Decode4Params), c_void_p]),
+    # Structs by address: the binding passes them packed as bytes (CACHE4 and so
+    # on below), which costs a tenth of setting the fields one by one.
+    ("bsfa_cache4_write", c_int, [c_void_p, c_void_p, c_void_p]),
+    ("bsfa_cache4_read", c_int, [c_void_p, c_void_p, c_void_p]),
+    ("bsfa_decode4_workspace_size", c_size_t, [c_void_p, c_void_p]),
+    ("bsfa_decode4", c_int, [c_void_p, c_void_p, c_void_p]),
     ("bsfa_selftest_wait_guard", c_int, [ctypes.c_uint, c_void_p]),
 ]
 

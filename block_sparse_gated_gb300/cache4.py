@@ -7,13 +7,12 @@ that follow, and ``cache4_read`` gives the 16-bit rows back.
 """
 from __future__ import annotations
 
-import ctypes
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import _native
-from .api import _DTYPES, _check, _dtype_code, _nbytes, _on_device, _stream, _strides_bhtd
+from .api import _DTYPES, _check, _dtype_code, _nbytes, _on_device, _strides_bhtd
 
 GROUP = 16  # elements that share a scale
 
@@ -54,111 +53,126 @@ def cache4_empty(num_pages: int, num_heads_kv: int, page_size: int, head_dim: in
     return KVCache4(*codes, *scales, k_exp, v_exp, layout)
 
 
-def _pool(c, t: torch.Tensor, what: str, dtype, shape, order, field):
-    if t.dtype != dtype or t.dim() != 4 or tuple(t.shape) != shape or t.stride(3) != 1:
-        raise ValueError(f"{what} must be a {dtype} {list(shape)} tensor with rows contiguous")
-    s = t.stride()
-    getattr(c, field)[:] = s[0], s[order[0]], s[order[1]]
-    return t.data_ptr()
-
-
-def _cache_params(cache: KVCache4, block_table: torch.Tensor, device, batch: int):
-    """The bsfa_cache4 of a call on ``device`` with ``batch`` sequences."""
-    k = cache.k
-    if cache.layout == "phtd":
-        order = (1, 2)
-    elif cache.layout == "pthd":
-        order = (2, 1)
-    else:
-        raise ValueError(cache.layout)
-    if k.dim() != 4:
-        raise ValueError("code pools are 4-D")
-    _on_device(device, k=k, v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale,
-               k_exp=cache.k_exp, v_exp=cache.v_exp, block_table=block_table)
-    shape = tuple(k.shape)
-    d = 2 * shape[3]
-    scales = shape[:3] + (d // GROUP,)
-    c = _native.Cache4()
-    c.k = _pool(c, k, "k", torch.uint8, shape, order, "k_stride")
-    c.v = _pool(c, cache.v, "v", torch.uint8, shape, order, "v_stride")
-    c.k_scale = _pool(c, cache.k_scale, "k_scale", torch.float8_e4m3fn, scales, order,
-                      "k_scale_stride")
-    c.v_scale = _pool(c, cache.v_scale, "v_scale", torch.float8_e4m3fn, scales, order,
-                      "v_scale_stride")
-    c.num_pages, c.num_heads_kv, c.page_size = shape[0], shape[order[0]], shape[order[1]]
-    c.head_dim = d
+def _bad_pool(cache, device):
+    """Says what is wrong with a cache that _cache_fields found fault with."""
+    _on_device(device, k=cache.k, v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale,
+               k_exp=cache.k_exp, v_exp=cache.v_exp)
+    shape = tuple(cache.k.shape)
+    for name, t, dtype, want in (
+            ("k", cache.k, torch.uint8, shape), ("v", cache.v, torch.uint8, shape),
+            ("k_scale", cache.k_scale, torch.float8_e4m3fn, shape[:3] + (shape[3] // 8,)),
+            ("v_scale", cache.v_scale, torch.float8_e4m3fn, shape[:3] + (shape[3] // 8,))):
+        if t.dtype != dtype or tuple(t.shape) != want or t.stride(3) != 1:
+            raise ValueError(f"{name} must be a {dtype} {list(want)} tensor with rows contiguous")
+    heads, _ = _heads_and_dim(cache)
     for name, e in (("k_exp", cache.k_exp), ("v_exp", cache.v_exp)):
-        if e is not None:
-            if e.dtype != torch.int32 or tuple(e.shape) != (c.num_heads_kv,) or \
-                    not e.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous int32 [{c.num_heads_kv}] tensor")
-            setattr(c, name, e.data_ptr())
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
+        if e is not None and (e.dtype != torch.int32 or tuple(e.shape) != (heads,) or
+                              not e.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 [{heads}] tensor")
+    raise ValueError("the cache's tensors disagree")
+
+
+def _cache_fields(cache: KVCache4, block_table: torch.Tensor, device, batch: int):
+    """The packed bsfa_cache4 of a call on ``device`` with ``batch`` sequences,
+    and the tokens that a row of the block table can hold."""
+    k, v, ks, vs, ke, ve, layout = cache
+    heads, d = _heads_and_dim(cache)
+    shape = k.shape
+    n, _, _, row = shape
+    scales = (n, shape[1], shape[2], row // 8)
+    a, b, e, f = k.stride(), v.stride(), ks.stride(), vs.stride()
+    u8, f8 = torch.uint8, torch.float8_e4m3fn
+    if not (k.dtype is u8 and v.dtype is u8 and ks.dtype is f8 and vs.dtype is f8 and
+            v.shape == shape and ks.shape == scales and vs.shape == scales and
+            len(b) == len(e) == len(f) == 4 and a[3] == b[3] == e[3] == f[3] == 1 and
+            k.device == device and v.device == device and ks.device == device and
+            vs.device == device):
+        _bad_pool(cache, device)
+    for x in (ke, ve):
+        if x is not None and not (x.dtype is torch.int32 and x.shape == (heads,) and
+                                  x.is_contiguous() and x.device == device):
+            _bad_pool(cache, device)
+    if block_table.device != device:
+        _on_device(device, block_table=block_table)
+    if block_table.dtype is not torch.int32 or block_table.dim() != 2 or \
             (block_table.shape[1] > 1 and block_table.stride(1) != 1):
         raise ValueError("block_table must be an int32 [batch, pages_per_sequence] tensor")
     rows, width = block_table.shape
     if rows < batch:
         raise ValueError("block_table has fewer rows than sequences")
-    c.block_table, c.block_table_width = block_table.data_ptr(), width
-    c.block_table_stride = block_table.stride(0) if rows > 1 else width
-    return c
+    i, j = (1, 2) if layout == "phtd" else (2, 1)
+    page = shape[j]
+    return _native.CACHE4.pack(
+        k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+        0 if ke is None else ke.data_ptr(), 0 if ve is None else ve.data_ptr(),
+        a[0], a[i], a[j], b[0], b[i], b[j], e[0], e[i], e[j], f[0], f[i], f[j],
+        n, page, heads, d, block_table.data_ptr(),
+        block_table.stride(0) if rows > 1 else width, width), width * page
 
 
 def _int32_vector(t, n: int, what: str):
-    if t.dtype != torch.int32 or tuple(t.shape) != (n,) or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 [{n}] tensor")
     return t.data_ptr()
 
 
-def _rows_params(k, v, layout, cu_seqlens, start, heads: int, d: int):
+def _rows_fields(k, v, layout, cu_seqlens, start, heads: int, d: int):
+    """The packed bsfa_cache4_rows of a call, and its number of sequences."""
     varlen = cu_seqlens is not None
     if layout is None:
         layout = "htd" if varlen else "bhld"
-    r = _native.Cache4Rows()
-    ks, Hk, L = _strides_bhtd(k, layout, varlen)
-    vs, Hv, Lv = _strides_bhtd(v, layout, varlen)
-    if k.shape != v.shape or (Hk, L) != (Hv, Lv):
+    if k.shape != v.shape:
         raise ValueError("K and V shapes disagree")
     if k.dtype != v.dtype:
         raise TypeError("K and V must share one element type")
-    if Hk != heads or k.shape[-1] != d:
+    ks, hk, n = _strides_bhtd(k, layout, varlen)
+    vs, _, _ = _strides_bhtd(v, layout, varlen)
+    if hk != heads or k.shape[-1] != d:
         raise ValueError("K and V must have the cache's heads and head dimension")
-    r.k, r.v = k.data_ptr(), v.data_ptr()
-    r.k_stride[:], r.v_stride[:] = ks, vs
-    r.seqlen, r.dtype = L, _dtype_code(k)
+    cu = 0
     if varlen:
-        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or \
+        if cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or \
                 not cu_seqlens.is_contiguous() or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be a contiguous int32 [batch + 1] tensor")
-        r.batch, r.cu_seqlens = cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
+        batch, cu = cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
     else:
-        r.batch = 1 if k.dim() == 3 else k.shape[0]
-    if start is not None:
-        r.start = _int32_vector(start, r.batch, "start")
-    return r
+        batch = 1 if k.dim() == 3 else k.shape[0]
+    first = 0 if start is None else _int32_vector(start, batch, "start")
+    return _native.CACHE4_ROWS.pack(k.data_ptr(), v.data_ptr(), *ks, *vs, batch, n, cu, first,
+                                    _dtype_code(k)), batch
 
 
 def _heads_and_dim(cache: KVCache4):
-    if cache.k.dim() != 4:
+    """KV heads and head dimension of a cache."""
+    shape, layout = cache.k.shape, cache.layout
+    if len(shape) != 4:
         raise ValueError("code pools are 4-D")
-    return cache.k.shape[1 if cache.layout == "phtd" else 2], 2 * cache.k.shape[3]
+    if layout == "phtd":
+        return shape[1], 2 * shape[3]
+    if layout == "pthd":
+        return shape[2], 2 * shape[3]
+    raise ValueError(layout)
 
 
 def _call(name, device, stream, *args):
     """One library call on ``stream`` (default: the device's current one), with
     the tensors' device current."""
     fn = getattr(_native.lib(), name)
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream, device)), name)
+    raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else \
+        stream.cuda_stream
+    if torch._C._cuda_getDevice() == device.index:
+        status = fn(*args, raw)
     else:
-        _check(fn(*args, _stream(stream, device)), name)
+        with torch.cuda.device(device):
+            status = fn(*args, raw)
+    if status:
+        _check(status, name)
 
 
 def _made_here(stream, device, *tensors):
     """Tensors allocated by a call that runs on ``stream``: their memory must
     not be handed out again before that stream is done with it."""
-    if stream is not None and stream != torch.cuda.current_stream(device):
+    if stream != torch.cuda.current_stream(device):
         for t in tensors:
             t.record_stream(stream)
 
@@ -179,9 +193,9 @@ def cache4_write(cache: KVCache4, k, v, block_table, *, start=None, cu_seqlens=N
     code.  A group that holds an infinity or a NaN reads back as NaN."""
     dev = k.device
     _on_device(dev, v=v, start=start, cu_seqlens=cu_seqlens)
-    r = _rows_params(k, v, layout, cu_seqlens, start, *_heads_and_dim(cache))
-    c = _cache_params(cache, block_table, dev, r.batch)
-    _call("bsfa_cache4_write", dev, stream, ctypes.byref(c), ctypes.byref(r))
+    r, batch = _rows_fields(k, v, layout, cu_seqlens, start, *_heads_and_dim(cache))
+    c, _ = _cache_fields(cache, block_table, dev, batch)
+    _call("bsfa_cache4_write", dev, stream, c, r)
 
 
 def cache4_read(cache: KVCache4, block_table, *, seqlen=None, total=None, start=None,
@@ -215,36 +229,37 @@ def cache4_read(cache: KVCache4, block_table, *, seqlen=None, total=None, start=
     else:
         k, v = out
     _on_device(dev, k=k, v=v, start=start, cu_seqlens=cu_seqlens)
-    r = _rows_params(k, v, layout, cu_seqlens, start, heads, d)
-    c = _cache_params(cache, block_table, dev, r.batch)
-    _call("bsfa_cache4_read", dev, stream, ctypes.byref(c), ctypes.byref(r))
+    r, batch = _rows_fields(k, v, layout, cu_seqlens, start, heads, d)
+    c, _ = _cache_fields(cache, block_table, dev, batch)
+    _call("bsfa_cache4_read", dev, stream, c, r)
     return k, v
 
 
-def _decode_params(q, cache, block_table, seqlens, out, *, layout, max_seqlen, softmax_scale,
-                   causal):
-    p = _native.Decode4Params()
-    qs, Hq, n = _strides_bhtd(q, layout or "bhld", False)
-    os_, Ho, no = _strides_bhtd(out, layout or "bhld", False)
+def _decode_fields(q, cache, block_table, seqlens, out, *, layout, max_seqlen, softmax_scale,
+                   causal, lse=0):
+    """The packed bsfa_cache4 of a decode call, and a function of a workspace's
+    address and size that gives its packed bsfa_decode4_params."""
+    if layout is None:
+        layout = "bhld"
     if q.shape != out.shape or q.dtype != out.dtype:
         raise ValueError("q and out must have one shape and type")
+    qs, hq, n = _strides_bhtd(q, layout, False)
+    os_ = qs if out is q else _strides_bhtd(out, layout, False)[0]
     heads, d = _heads_and_dim(cache)
-    if q.shape[-1] != d or Hq % heads:
+    shape = q.shape
+    if shape[-1] != d or heads == 0 or hq % heads:
         raise ValueError("q must have the cache's head dimension and a multiple of its heads")
-    p.batch = 1 if q.dim() == 3 else q.shape[0]
-    c = _cache_params(cache, block_table, q.device, p.batch)
-    p.q, p.o = q.data_ptr(), out.data_ptr()
-    p.q_stride[:], p.o_stride[:] = qs, os_
-    p.num_heads_q, p.q_len = Hq, n
-    p.seqlens = _int32_vector(seqlens, p.batch, "seqlens")
-    most = c.block_table_width * c.page_size
-    p.max_seqlen = most if max_seqlen is None else int(max_seqlen)
-    if p.max_seqlen > most:
+    batch = 1 if len(shape) == 3 else shape[0]
+    c, most = _cache_fields(cache, block_table, q.device, batch)
+    if max_seqlen is None:
+        max_seqlen = most
+    elif max_seqlen > most:
         raise ValueError("block_table has too few pages per row for max_seqlen")
-    p.softmax_scale = float(softmax_scale) if softmax_scale else 0.0
-    p.causal = 1 if causal else 0
-    p.dtype = _dtype_code(q)
-    return p, c
+    fixed = (q.data_ptr(), out.data_ptr(), *qs, *os_, batch, hq, n,
+             _int32_vector(seqlens, batch, "seqlens"), int(max_seqlen),
+             float(softmax_scale) if softmax_scale else 0.0, 1 if causal else 0, lse)
+    code = _dtype_code(q)
+    return c, lambda ws, size: _native.DECODE4.pack(*fixed, ws, size, code)
 
 
 def decode4(q, cache: KVCache4, block_table, seqlens, *, max_seqlen=None, softmax_scale=None,
@@ -268,33 +283,33 @@ def decode4(q, cache: KVCache4, block_table, seqlens, *, max_seqlen=None, softma
         out = torch.empty_like(q)
         made.append(out)
     dev = q.device
-    _on_device(dev, out=out, seqlens=seqlens)
-    p, c = _decode_params(q, cache, block_table, seqlens, out, layout=layout,
-                          max_seqlen=max_seqlen, softmax_scale=softmax_scale, causal=causal)
+    _on_device(dev, out=out, seqlens=seqlens, workspace=workspace)
     res = {"out": out}
+    lse = 0
     if return_lse:
-        lse = torch.empty((p.num_heads_q, p.batch * p.q_len), dtype=torch.float32, device=dev)
-        p.lse = lse.data_ptr()
-        res["lse"] = lse
-        made.append(lse)
-    need = _native.lib().bsfa_decode4_workspace_size(ctypes.byref(c), ctypes.byref(p))
+        _, hq, n = _strides_bhtd(q, layout or "bhld", False)
+        rows = n if q.dim() == 3 else q.shape[0] * n
+        res["lse"] = torch.empty((hq, rows), dtype=torch.float32, device=dev)
+        made.append(res["lse"])
+        lse = res["lse"].data_ptr()
+    c, fields = _decode_fields(q, cache, block_table, seqlens, out, layout=layout,
+                               max_seqlen=max_seqlen, softmax_scale=softmax_scale, causal=causal,
+                               lse=lse)
     if workspace is None:
+        need = _native.lib().bsfa_decode4_workspace_size(c, fields(0, 0))
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
         made.append(workspace)
-    else:
-        if not workspace.is_contiguous():
-            raise ValueError("the workspace must be contiguous")
-        _on_device(dev, workspace=workspace)
-    p.workspace, p.workspace_bytes = workspace.data_ptr(), _nbytes(workspace)
+    elif not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
     if stream is not None:
         _made_here(stream, dev, *made)
-    _call("bsfa_decode4", dev, stream, ctypes.byref(c), ctypes.byref(p))
+    _call("bsfa_decode4", dev, stream, c, fields(workspace.data_ptr(), _nbytes(workspace)))
     return res
 
 
 def decode4_workspace_bytes(q, cache: KVCache4, block_table, seqlens, *, max_seqlen=None,
                             layout=None) -> int:
     """Workspace bytes that decode4 needs for this call's shapes."""
-    p, c = _decode_params(q, cache, block_table, seqlens, q, layout=layout,
-                          max_seqlen=max_seqlen, softmax_scale=None, causal=True)
-    return int(_native.lib().bsfa_decode4_workspace_size(ctypes.byref(c), ctypes.byref(p)))
+    c, fields = _decode_fields(q, cache, block_table, seqlens, q, layout=layout,
+                               max_seqlen=max_seqlen, softmax_scale=None, causal=True)
+    return int(_native.lib().bsfa_decode4_workspace_size(c, fields(0, 0)))

@@ -296,6 +296,12 @@ bsfa_status validate_cache4_pointers(const bsfa_cache4* c) {
     if (c->k_stride[i] <= 0 || c->v_stride[i] <= 0 || c->k_scale_stride[i] <= 0 ||
         c->v_scale_stride[i] <= 0)
       return BSFA_ERR_UNSUPPORTED;
+    // The attention kernel's address arithmetic: page strides below 2^34 bytes,
+    // offsets within a page below 2^31.
+    const int64_t most = i == 0 ? (1LL << 34) - 1 : i == 2 ? 0x7fffffffLL / c->page_size : INT64_MAX;
+    if (c->k_stride[i] > most || c->v_stride[i] > most || c->k_scale_stride[i] > most ||
+        c->v_scale_stride[i] > most)
+      return BSFA_ERR_UNSUPPORTED;
     if (c->k_stride[i] % 16 || c->v_stride[i] % 16 || c->k_scale_stride[i] % unit ||
         c->v_scale_stride[i] % unit)
       return BSFA_ERR_UNSUPPORTED;

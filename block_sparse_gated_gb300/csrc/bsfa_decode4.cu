@@ -33,6 +33,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "bsfa.h"
 #include "bsfa_cache4.h"
@@ -70,7 +71,9 @@ struct Shape<4> {
 struct DecArgs {
   const uint8_t *kc, *vc, *ks, *vs;
   const int32_t *kexp, *vexp;
-  long long kc_s[3], vc_s[3], ks_s[3], vs_s[3];  // {page, head, token} bytes
+  long long kc_sh, vc_sh, ks_sh, vs_sh;        // head strides in bytes
+  uint32_t kc_sp4, vc_sp4, ks_sp4, vs_sp4;     // page strides in units of 4 bytes
+  int kc_st, vc_st, ks_st, vs_st;              // token strides in bytes
   const int32_t* table;
   int table_stride, num_pages, tiles_per_page;
   const uint16_t* q;
@@ -231,55 +234,66 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
     const int min_lim = a.causal ? max(0, len - a.q_len + first_i + 1) : len;
     const int max_lim = a.causal ? max(0, len - a.q_len + last_i + 1) : len;
 
-    // ---- this warp's tiles: u0 * WARPS + warp, and every WARPS-th after it
-    const int t_begin = u0 * WARPS + warp;
-    const int t_end = min(u1 * WARPS, (max_lim + TOK - 1) / TOK);
-    const int n_tiles = t_begin < t_end ? (t_end - t_begin + WARPS - 1) / WARPS : 0;
+    // ---- this warp's tiles: an equal run of the piece's
+    const int t0 = u0 * WARPS, t1 = min(u1 * WARPS, (max_lim + TOK - 1) / TOK);
+    const int run = (max(0, t1 - t0) + WARPS - 1) / WARPS;
+    const int t_begin = t0 + warp * run, t_end = min(t1, t_begin + run);
+    const int n_tiles = max(0, t_end - t_begin);
 
+    // ---- copies: each lane keeps its source addresses, which step through a
+    // page and are formed anew where one begins; the next page's table entry is
+    // in flight meanwhile.  Lanes 0-15 copy the keys' scales of a token each,
+    // lanes 16-31 the values'.
+    constexpr int CHUNKS = D / 32;  // 16-byte chunks of a row of codes
+    const int cp_tok = lane / CHUNKS, cp_chunk = lane % CHUNKS;
+    const bool cp_val = lane >= 16;
     const int32_t* table = a.table + static_cast<long long>(b) * a.table_stride;
-    const uint8_t* kc = a.kc + kvh * a.kc_s[1];
-    const uint8_t* vc = a.vc + kvh * a.vc_s[1];
-    // Lanes 0-15 copy the keys' scales of a token each, lanes 16-31 the values'.
-    const uint8_t* sc_src = lane < 16 ? a.ks + kvh * a.ks_s[1] + (lane & 15) * a.ks_s[2]
-                                      : a.vs + kvh * a.vs_s[1] + (lane & 15) * a.vs_s[2];
-    const long long sc_page = lane < 16 ? a.ks_s[0] : a.vs_s[0];
-    const long long sc_tok = lane < 16 ? a.ks_s[2] : a.vs_s[2];
-
-    // Prefetch cursor: the next tile to copy, as page column and tile in it.
-    int pf_tile = t_begin;
-    int pf_col = t_begin / a.tiles_per_page;
-    int pf_off = t_begin - pf_col * a.tiles_per_page;
-    int pf_entry = pf_tile < t_end ? __ldg(table + pf_col) : -1;
-    auto copy_tile = [&](int slot) {
-      if (pf_tile < t_end) {
-        const bool ok = pf_entry >= 0 && pf_entry < a.num_pages;
-        const long long page = ok ? pf_entry : 0;
-        const int row = ok ? pf_off * TOK : 0;
-        const uint32_t dst = my_ring + slot * St::BYTES;
-        const uint8_t* k_src = kc + page * a.kc_s[0] + row * a.kc_s[2];
-        const uint8_t* v_src = vc + page * a.vc_s[0] + row * a.vc_s[2];
-        constexpr int CHUNKS = D / 32;  // 16-byte chunks of a row
-#pragma unroll
-        for (int j = 0; j < TOK * CHUNKS / 32; ++j) {
-          const int id = lane + 32 * j;
-          const int t = id / CHUNKS, ch = id % CHUNKS;
-          cp_async16(dst + swizzle<D>(t, ch), k_src + t * a.kc_s[2] + ch * 16, ok);
-          cp_async16(dst + St::CODES + swizzle<D>(t, ch), v_src + t * a.vc_s[2] + ch * 16, ok);
+    const uint8_t* k_base = a.kc + kvh * a.kc_sh + (cp_tok * a.kc_st + cp_chunk * 16);
+    const uint8_t* v_base = a.vc + kvh * a.vc_sh + (cp_tok * a.vc_st + cp_chunk * 16);
+    const int z_st = cp_val ? a.vs_st : a.ks_st;
+    const uint32_t z_sp4 = cp_val ? a.vs_sp4 : a.ks_sp4;
+    const uint8_t* z_base =
+        (cp_val ? a.vs + kvh * a.vs_sh : a.ks + kvh * a.ks_sh) + (lane & 15) * z_st;
+    const uint32_t cp_dst = swizzle<D>(cp_tok, cp_chunk);
+    int cp_left = n_tiles;                  // tiles of pages not opened yet
+    int cp_col = t_begin / a.tiles_per_page;
+    int cp_run = 0;                         // tiles of the open page still to copy
+    int cp_entry = cp_left > 0 ? __ldg(table + cp_col) : -1;
+    bool cp_ok = false;
+    const uint8_t *k_src = k_base, *v_src = v_base, *z_src = z_base;
+    auto open_page = [&](int off) {  // the page cp_entry names, from its tile `off`
+      const bool ok = static_cast<uint32_t>(cp_entry) < static_cast<uint32_t>(a.num_pages);
+      const uint32_t page = ok ? cp_entry : 0;
+      const int row = off * TOK;
+      cp_ok = ok;
+      k_src = k_base + (static_cast<uint64_t>(page) * a.kc_sp4 << 2) + row * a.kc_st;
+      v_src = v_base + (static_cast<uint64_t>(page) * a.vc_sp4 << 2) + row * a.vc_st;
+      z_src = z_base + (static_cast<uint64_t>(page) * z_sp4 << 2) + row * z_st;
+      cp_run = min(cp_left, a.tiles_per_page - off);
+      cp_left -= cp_run;
+      if (cp_left > 0) cp_entry = __ldg(table + ++cp_col);
+    };
+    if (cp_left > 0) open_page(t_begin - cp_col * a.tiles_per_page);
+    auto copy_tile = [&](uint32_t dst) {
+      if (cp_run > 0) {
+        const uint32_t at = dst + cp_dst;
+        cp_async16(at, k_src, cp_ok);
+        cp_async16(at + St::CODES, v_src, cp_ok);
+        if constexpr (D == 128) {  // rows 8 .. 15: swizzle(t + 8) = swizzle(t) + 512
+          cp_async16(at + 512, k_src + 8 * a.kc_st, cp_ok);
+          cp_async16(at + St::CODES + 512, v_src + 8 * a.vc_st, cp_ok);
         }
-        cp_async_small<D / FP4_GROUP>(dst + 2 * St::CODES + lane * (D / FP4_GROUP),
-                                      sc_src + page * sc_page + row * sc_tok, ok);
-        pf_tile += WARPS;
-        pf_off += WARPS;
-        while (pf_off >= a.tiles_per_page) {
-          pf_off -= a.tiles_per_page;
-          ++pf_col;
-        }
-        if (pf_tile < t_end) pf_entry = __ldg(table + pf_col);
+        cp_async_small<D / FP4_GROUP>(dst + 2 * St::CODES + lane * (D / FP4_GROUP), z_src,
+                                      cp_ok);
+        k_src += TOK * a.kc_st;
+        v_src += TOK * a.vc_st;
+        z_src += TOK * z_st;
+        if (--cp_run == 0 && cp_left > 0) open_page(0);
       }
       cp_async_commit();
     };
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) copy_tile(s);
+    for (int s = 0; s < STAGES - 1; ++s) copy_tile(my_ring + s * St::BYTES);
 
     // ---- queries: fragments of Q^T (fp16, row scaled to [2^14, 2^15)) and the
     // factor that turns a product into a score in log2 units
@@ -326,7 +340,9 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
     // ---- per-lane columns: 2c and 2c + 1 of each row tile
     float acc[NT][MT][4];
     float ref[NT][2], sum[NT][2], sc[NT][2];
+    float zn[NT][2];  // SHIFT - ref: a weight is 2^(sc * product + zn)
     int lim[NT][2];
+    uint2 qf[NT == 1 ? KSTEPS : 1];  // one row tile's queries stay in registers
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -337,24 +353,34 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
       for (int e = 0; e < 2; ++e) {
         const int r = r0 + nt * 8 + 2 * c + e;
         ref[nt][e] = -INFINITY;
+        zn[nt][e] = INFINITY;
         sum[nt][e] = 0.f;
         sc[nt][e] = sh_sc[nt * 8 + 2 * c + e];
         // Rows past the last are computed along with the rest and not stored.
         lim[nt][e] = !a.causal || r >= a.rows ? len : len - a.q_len + r / a.group + 1;
       }
     }
+    if constexpr (NT == 1) {
+#pragma unroll
+      for (int j = 0; j < KSTEPS; ++j) qf[j] = sh_q[j * 32 + lane];
+    }
+    const uint32_t q_addr = smem_u32(sh_q) + lane * 8;
     // Row m of a 8-token half tile is token 4 (m & 1) + (m >> 1), the order in
     // which the values' fragments pair tokens.
     const int my_tok = ((g & 1) << 2) + (g >> 1);
+    // This lane's places in a stage: its d/4 codes of key my_tok (key my_tok + 8
+    // lies half a tile on), its d/8 codes of values c, c + 4, c + 8, c + 12 (each
+    // a quarter tile on, the odd ones in the other 64 bytes of their lines).
+    const uint32_t k_at = D == 128 ? swizzle<D>(my_tok, c)
+                                   : swizzle<D>(my_tok, c >> 1) + (c & 1) * 8;
+    const uint32_t v_at = St::CODES + (D == 128 ? swizzle<D>(c, g >> 1) + (g & 1) * 8
+                                                : swizzle<D>(c, g >> 2) + (g & 3) * 4);
+    const uint32_t v_at1 = v_at ^ 64u;
+    const uint32_t zk_at = 2 * St::CODES + (D == 128 ? my_tok * 8 + 2 * c : my_tok * 4 + c);
+    const uint32_t zv_at = 2 * St::CODES + St::SCALES + (D == 128 ? c * 8 + g : c * 4 + (g >> 1));
 
-    for (int n = 0; n < n_tiles; ++n) {
-      cp_async_wait<STAGES - 2>();
-      __syncwarp();  // every lane's copies of tile n are in, and tile n - 1 is read
-      copy_tile((n + STAGES - 1) % STAGES);
-      const uint8_t* stp = ring + (warp * STAGES + n % STAGES) * St::BYTES;
-      const int tok0 = (t_begin + n * WARPS) * TOK;
-      const bool masked = tok0 + TOK > min_lim;
-
+    auto tile = [&](const uint32_t st, const int tok0, auto masked_tag) {
+      constexpr bool MASKED = decltype(masked_tag)::value;
       // ---- S^T = K Q^T
       float s[NT][4];
 #pragma unroll
@@ -364,27 +390,20 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
       {
         uint32_t ka[D / 32], kb[D / 32];  // d/4 codes of tokens my_tok, my_tok + 8
         uint32_t sa[2], sb[2];            // their scales, each twice
-        const uint8_t* sk = stp + 2 * St::CODES;
         if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(stp + swizzle<D>(my_tok, c));
-          const uint4 y = *reinterpret_cast<const uint4*>(stp + swizzle<D>(my_tok + 8, c));
+          const uint4 x = lds128(st + k_at), y = lds128(st + k_at + 512);
           ka[0] = x.x, ka[1] = x.y, ka[2] = x.z, ka[3] = x.w;
           kb[0] = y.x, kb[1] = y.y, kb[2] = y.z, kb[3] = y.w;
-          const uint32_t za = e4m3x2_to_f16(
-              *reinterpret_cast<const uint16_t*>(sk + my_tok * 8 + 2 * c));
-          const uint32_t zb = e4m3x2_to_f16(
-              *reinterpret_cast<const uint16_t*>(sk + (my_tok + 8) * 8 + 2 * c));
+          const uint32_t za = e4m3x2_to_f16(lds16(st + zk_at));
+          const uint32_t zb = e4m3x2_to_f16(lds16(st + zk_at + 64));
           sa[0] = __byte_perm(za, 0, 0x1010), sa[1] = __byte_perm(za, 0, 0x3232);
           sb[0] = __byte_perm(zb, 0, 0x1010), sb[1] = __byte_perm(zb, 0, 0x3232);
         } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(stp + swizzle<D>(my_tok, c >> 1) +
-                                                          (c & 1) * 8);
-          const uint2 y = *reinterpret_cast<const uint2*>(stp + swizzle<D>(my_tok + 8, c >> 1) +
-                                                          (c & 1) * 8);
+          const uint2 x = lds64(st + k_at), y = lds64(st + k_at + 256);
           ka[0] = x.x, ka[1] = x.y;
           kb[0] = y.x, kb[1] = y.y;
-          const uint32_t za = e4m3x2_to_f16(sk[my_tok * 4 + c]);
-          const uint32_t zb = e4m3x2_to_f16(sk[(my_tok + 8) * 4 + c]);
+          const uint32_t za = e4m3x2_to_f16(lds8(st + zk_at));
+          const uint32_t zb = e4m3x2_to_f16(lds8(st + zk_at + 32));
           sa[0] = sa[1] = __byte_perm(za, 0, 0x1010);
           sb[0] = sb[1] = __byte_perm(zb, 0, 0x1010);
         }
@@ -403,41 +422,44 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const uint2 qf = sh_q[(nt * KSTEPS + 2 * w + j) * 32 + lane];
-              mma_f16_16816(s[nt], fa[2 * j], fb[2 * j], fa[2 * j + 1], fb[2 * j + 1], qf.x, qf.y);
+              const uint2 q2 = NT == 1 ? qf[NT == 1 ? 2 * w + j : 0]
+                                       : lds64(q_addr + (nt * KSTEPS + 2 * w + j) * 256);
+              mma_f16_16816(s[nt], fa[2 * j], fb[2 * j], fa[2 * j + 1], fb[2 * j + 1], q2.x, q2.y);
             }
         }
       }
 
-      // ---- scores, masks, reference
-      bool over = false;
+      // ---- weights; the reference moves where one would pass 2^(SHIFT + HEADROOM)
+      float y[NT][4];
+      auto weigh = [&]() {
+        bool over = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] *= sc[nt][e & 1];
-        if (masked) {
-          const int ta = tok0 + my_tok, tb = ta + 8;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (ta >= lim[nt][e]) s[nt][e] = -INFINITY;
-            if (tb >= lim[nt][e]) s[nt][e + 2] = -INFINITY;
+          for (int e = 0; e < 4; ++e) {
+            y[nt][e] = fmaf(s[nt][e], sc[nt][e & 1], zn[nt][e & 1]);
+            if (MASKED && tok0 + my_tok + (e & 2) * 4 >= lim[nt][e & 1]) y[nt][e] = -INFINITY;
+            over |= y[nt][e] > SHIFT + HEADROOM;
           }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) over |= s[nt][e] > ref[nt][e & 1] + HEADROOM;
-      }
-      if (__any_sync(0xffffffffu, over)) {
+        return over;
+      };
+      if (__any_sync(0xffffffffu, weigh())) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(s[nt][e], s[nt][e + 2]);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float m1 = fmaxf(ref[nt][e], mx);
+            float lo = s[nt][e] * sc[nt][e], hi = s[nt][e + 2] * sc[nt][e];
+            if (MASKED) {
+              if (tok0 + my_tok >= lim[nt][e]) lo = -INFINITY;
+              if (tok0 + my_tok + 8 >= lim[nt][e]) hi = -INFINITY;
+            }
+            float m1 = fmaxf(ref[nt][e], fmaxf(lo, hi));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 4));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 8));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 16));
             const float f = m1 == -INFINITY ? 1.f : ex2_approx(ref[nt][e] - m1);
             ref[nt][e] = m1;
+            zn[nt][e] = SHIFT - m1;
             sum[nt][e] *= f;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -445,41 +467,36 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
               acc[nt][mt][e + 2] *= f;
             }
           }
+        weigh();
       }
       uint32_t pb[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float z0 = (ref[nt][0] == -INFINITY ? 0.f : ref[nt][0]) - SHIFT;
-        const float z1 = (ref[nt][1] == -INFINITY ? 0.f : ref[nt][1]) - SHIFT;
-        const float p0 = ex2_approx(s[nt][0] - z0), p1 = ex2_approx(s[nt][1] - z1);
-        const float p2 = ex2_approx(s[nt][2] - z0), p3 = ex2_approx(s[nt][3] - z1);
-        sum[nt][0] += p0 + p2;
-        sum[nt][1] += p1 + p3;
-        pb[nt][0] = movmatrix_trans(pack_f16x2(p0, p1));
-        pb[nt][1] = movmatrix_trans(pack_f16x2(p2, p3));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[nt][e] = ex2_approx(y[nt][e]);
+          sum[nt][e & 1] += y[nt][e];
+        }
+        pb[nt][0] = movmatrix_trans(pack_f16x2(y[nt][0], y[nt][1]));
+        pb[nt][1] = movmatrix_trans(pack_f16x2(y[nt][2], y[nt][3]));
       }
 
-      // ---- O^T += V^T P^T
+      // ---- O^T += V^T P^T; this lane: elements [g d/8, (g + 1) d/8) of tokens c + 4j
       {
-        // This lane: elements [g * d/8, (g + 1) * d/8) of tokens c + 4j.
-        const uint8_t* vp = stp + St::CODES;
-        const uint8_t* sv = stp + 2 * St::CODES + St::SCALES;
+        constexpr int STEP = St::CODES / 4;  // bytes from token c + 4j to the next
         uint32_t v[4][D / 64], z[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int t = c + 4 * j;
+          const uint32_t at = st + (j & 1 ? v_at1 : v_at) + j * STEP;
           if constexpr (D == 128) {
-            const uint2 x = *reinterpret_cast<const uint2*>(vp + swizzle<D>(t, g >> 1) +
-                                                            (g & 1) * 8);
+            const uint2 x = lds64(at);
             v[j][0] = x.x, v[j][1] = x.y;
-            z[j] = sv[t * 8 + g];
           } else {
-            v[j][0] = *reinterpret_cast<const uint32_t*>(vp + swizzle<D>(t, g >> 2) +
-                                                         (g & 3) * 4);
-            z[j] = sv[t * 4 + (g >> 1)];
+            v[j][0] = lds32(at);
           }
+          z[j] = lds8(st + zv_at + j * (St::SCALES / 4));
         }
-        if (masked) {
+        if (MASKED) {
           // A hidden value weighs nothing even where it is not a number: past
           // max_lim the scale becomes 0.  Below it, a NaN that only some rows
           // see is taken out and put into those rows.
@@ -533,6 +550,20 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
           }
         }
       }
+    };
+
+    uint32_t rd = my_ring, wr = my_ring + (STAGES - 1) * St::BYTES;
+    const uint32_t ring_end = my_ring + STAGES * St::BYTES;
+    for (int tok0 = t_begin * TOK; tok0 < t_end * TOK; tok0 += TOK) {
+      cp_async_wait<STAGES - 2>();
+      __syncwarp();  // every lane's copies of this tile are in, and the last one is read
+      copy_tile(wr);
+      if (tok0 + TOK <= min_lim)
+        tile(rd, tok0, std::false_type{});
+      else
+        tile(rd, tok0, std::true_type{});
+      rd = rd + St::BYTES == ring_end ? my_ring : rd + St::BYTES;
+      wr = wr + St::BYTES == ring_end ? my_ring : wr + St::BYTES;
     }
     cp_async_wait<0>();
 
@@ -808,11 +839,16 @@ bsfa_status bsfa_decode4(const bsfa_cache4* cache, const bsfa_decode4_params* p,
   a.vs = cache->v_scale;
   a.kexp = cache->k_exp;
   a.vexp = cache->v_exp;
+  auto strides = [](const int64_t (&s)[3], uint32_t& page, long long& head, int& token) {
+    page = static_cast<uint32_t>(s[0] >> 2);  // validate_cache4_pointers() bounds both
+    head = s[1];
+    token = static_cast<int>(s[2]);
+  };
+  strides(cache->k_stride, a.kc_sp4, a.kc_sh, a.kc_st);
+  strides(cache->v_stride, a.vc_sp4, a.vc_sh, a.vc_st);
+  strides(cache->k_scale_stride, a.ks_sp4, a.ks_sh, a.ks_st);
+  strides(cache->v_scale_stride, a.vs_sp4, a.vs_sh, a.vs_st);
   for (int i = 0; i < 3; ++i) {
-    a.kc_s[i] = cache->k_stride[i];
-    a.vc_s[i] = cache->v_stride[i];
-    a.ks_s[i] = cache->k_scale_stride[i];
-    a.vs_s[i] = cache->v_scale_stride[i];
     a.q_s[i] = p->q_stride[i];
     a.o_s[i] = p->o_stride[i];
   }

@@ -84,6 +84,8 @@ int main(void) {
                                             check=True).stdout.split()))
     n = _native()
     C, R, P = n.Cache4, n.Cache4Rows, n.Decode4Params
+    assert (n.CACHE4.size, n.CACHE4_ROWS.size, n.DECODE4.size) == tuple(map(ctypes.sizeof,
+                                                                           (C, R, P)))
     assert got == (ctypes.sizeof(C), C.k_scale_stride.offset, C.block_table.offset,
                    C.block_table_width.offset, ctypes.sizeof(R), R.cu_seqlens.offset,
                    R.dtype.offset, ctypes.sizeof(P), P.seqlens.offset, P.lse.offset,
@@ -109,7 +111,9 @@ def test_cache_descriptors_that_are_refused(lib, change, status):
 
 def test_cache_strides_that_are_refused(lib):
     for field, i, bad in (("k_stride", 0, 64 * 64 + 8), ("v_stride", 2, 0), ("k_stride", 1, -64),
-                          ("k_scale_stride", 0, 1020), ("v_scale_stride", 2, 4)):
+                          ("k_scale_stride", 0, 1020), ("v_scale_stride", 2, 4),
+                          ("k_stride", 0, 1 << 34), ("v_scale_stride", 0, 1 << 34),
+                          ("v_stride", 2, 1 << 25), ("k_scale_stride", 2, 1 << 25)):
         c = _cache()
         getattr(c, field)[i] = bad
         p, r = _decode(), _rows()
@@ -194,60 +198,89 @@ def test_binding_checks_what_the_library_cannot_see(monkeypatch):
     cache = b.cache4_empty(4, 2, 32, 128, device="cpu")
     table = torch.zeros(3, 2, dtype=torch.int32)
     dev = torch.device("cpu")
-    c = m._cache_params(cache, table, dev, 3)
+    n = _native()
+
+    def descriptor(*a):
+        return n.Cache4.from_buffer_copy(m._cache_fields(*a)[0])
+
+    def rows(*a):
+        return n.Cache4Rows.from_buffer_copy(m._rows_fields(*a)[0])
+
+    def decode(*a, **kw):
+        return n.Decode4Params.from_buffer_copy(m._decode_fields(*a, **kw)[1](4096, 77))
+
+    c = descriptor(cache, table, dev, 3)
     assert (c.num_pages, c.num_heads_kv, c.page_size, c.head_dim) == (4, 2, 32, 128)
+    assert (c.k, c.v_scale, c.k_exp) == (cache.k.data_ptr(), cache.v_scale.data_ptr(), None)
     assert tuple(c.k_stride) == (2 * 32 * 64, 32 * 64, 64)
+    assert c.block_table == table.data_ptr()
     assert (c.block_table_stride, c.block_table_width) == (2, 2)
     other = b.cache4_empty(4, 2, 32, 128, layout="pthd", device="cpu")
-    assert tuple(m._cache_params(other, table, dev, 3).v_scale_stride) == (32 * 2 * 8, 8, 2 * 8)
+    assert tuple(descriptor(other, table, dev, 3).v_scale_stride) == (32 * 2 * 8, 8, 2 * 8)
     wide = torch.zeros(3, 9, dtype=torch.int32)[:, :2]
-    c = m._cache_params(cache, wide, dev, 3)
+    c = descriptor(cache, wide, dev, 3)
     assert (c.block_table_stride, c.block_table_width) == (9, 2)
+    exps = torch.zeros(2, dtype=torch.int32)
+    c = descriptor(cache._replace(k_exp=exps, v_exp=exps), table, dev, 3)
+    assert c.k_exp == c.v_exp == exps.data_ptr()
     for bad in (cache._replace(v=cache.v[:2]), cache._replace(k_scale=cache.k_scale[..., :4]),
                 cache._replace(k=cache.k.to(torch.int8)),
                 cache._replace(v_scale=cache.v_scale.view(torch.uint8)),
+                cache._replace(k_scale=cache.k_scale[0]), cache._replace(k=cache.k[0]),
                 cache._replace(k_exp=torch.zeros(3, dtype=torch.int32)),
                 cache._replace(v_exp=torch.zeros(2)), cache._replace(layout="thpd"),
                 cache._replace(k=cache.k.transpose(2, 3).contiguous().transpose(2, 3))):
         with pytest.raises(ValueError):
-            m._cache_params(bad, table, dev, 3)
+            descriptor(bad, table, dev, 3)
     for bad in (table.long(), table[0], torch.zeros(2, 3, dtype=torch.int32).t()):
         with pytest.raises(ValueError, match="block_table"):
-            m._cache_params(cache, bad, dev, 3)
+            descriptor(cache, bad, dev, 3)
     with pytest.raises(ValueError, match="fewer rows"):
-        m._cache_params(cache, table, dev, 4)
+        descriptor(cache, table, dev, 4)
     k = torch.zeros(3, 2, 10, 128, dtype=torch.bfloat16)
     ok = (None, None, None, 2, 128)
-    assert m._rows_params(k, k, *ok).batch == 3
+    r = rows(k, k, *ok)
+    assert (r.batch, r.seqlen, r.dtype, r.cu_seqlens, r.start) == (3, 10, 0, None, None)
+    assert tuple(r.v_stride) == (2 * 10 * 128, 10 * 128, 128) and r.v == k.data_ptr()
+    at = torch.zeros(3, dtype=torch.int32)
+    cu = torch.zeros(4, dtype=torch.int32)
+    r = rows(k[0].half(), k[0].half(), "htd", cu, at, 2, 128)
+    assert (r.batch, r.seqlen, r.dtype) == (3, 10, 1)
+    assert (r.cu_seqlens, r.start) == (cu.data_ptr(), at.data_ptr())
     with pytest.raises(ValueError, match="disagree"):
-        m._rows_params(k, k[:, :, :9], *ok)
+        rows(k, k[:, :, :9], *ok)
     with pytest.raises(TypeError):
-        m._rows_params(k, k.half(), *ok)
+        rows(k, k.half(), *ok)
     with pytest.raises(TypeError):
-        m._rows_params(k.float(), k.float(), *ok)
+        rows(k.float(), k.float(), *ok)
     with pytest.raises(ValueError, match="heads"):
-        m._rows_params(k[..., :64], k[..., :64], *ok)
+        rows(k[..., :64], k[..., :64], *ok)
     with pytest.raises(ValueError, match="start"):
-        m._rows_params(k, k, None, None, torch.zeros(2, dtype=torch.int32), 2, 128)
+        rows(k, k, None, None, torch.zeros(2, dtype=torch.int32), 2, 128)
     with pytest.raises(ValueError, match="cu_seqlens"):
-        m._rows_params(k[0], k[0], None, torch.zeros(2), None, 2, 128)
+        rows(k[0], k[0], None, torch.zeros(2), None, 2, 128)
     with pytest.raises(ValueError, match="seqlen"):
         m.cache4_read(cache, table)
     with pytest.raises(ValueError, match="total"):
         m.cache4_read(cache, table, seqlen=3, cu_seqlens=torch.zeros(2, dtype=torch.int32))
     q = torch.zeros(3, 8, 1, 128, dtype=torch.bfloat16)
-    n = torch.zeros(3, dtype=torch.int32)
+    lens = torch.zeros(3, dtype=torch.int32)
     kw = dict(layout=None, max_seqlen=None, softmax_scale=None, causal=True)
-    p, _ = m._decode_params(q, cache, table, n, q, **kw)
+    p = decode(q, cache, table, lens, q, lse=512, **kw)
     assert (p.batch, p.num_heads_q, p.q_len, p.max_seqlen) == (3, 8, 1, 64)
+    assert (p.q, p.o, p.seqlens, p.lse) == (q.data_ptr(), q.data_ptr(), lens.data_ptr(), 512)
+    assert (p.workspace, p.workspace_bytes, p.dtype, p.causal) == (4096, 77, 0, 1)
+    p = decode(q.half(), cache, table, lens, q.half(),
+               **dict(kw, softmax_scale=0.5, causal=False, max_seqlen=9))
+    assert (p.dtype, p.causal, p.max_seqlen, p.softmax_scale) == (1, 0, 9, 0.5)
     with pytest.raises(ValueError, match="heads"):
-        m._decode_params(q[:, :7], cache, table, n, q[:, :7], **kw)
+        decode(q[:, :7], cache, table, lens, q[:, :7], **kw)
     with pytest.raises(ValueError, match="shape and type"):
-        m._decode_params(q, cache, table, n, q.half(), **kw)
+        decode(q, cache, table, lens, q.half(), **kw)
     with pytest.raises(ValueError, match="seqlens"):
-        m._decode_params(q, cache, table, n.long(), q, **kw)
+        decode(q, cache, table, lens.long(), q, **kw)
     with pytest.raises(ValueError, match="pages"):
-        m._decode_params(q, cache, table, n, q, **dict(kw, max_seqlen=65))
+        decode(q, cache, table, lens, q, **dict(kw, max_seqlen=65))
 
 
 def test_cache_allocation_checks():
