@@ -17,12 +17,14 @@
 // one conversion and one product per pair of elements and no transposition:
 // keys pair neighbours of one token, values pair two tokens by merging nibbles.
 //
-// Work split.  A unit is 64 cached tokens of one (sequence, KV head, row tile)
-// segment.  The units of all segments form one line, which is cut into equal
-// pieces, one per CTA, from the lengths on the device: long and short
-// sequences balance without the host knowing them, and a captured call stays
-// right as they grow.  A segment that a cut crosses leaves partial sums in the
-// workspace, which a second kernel joins in a fixed order.
+// Work split.  A segment is one (sequence, KV head, row tile).  Where it is
+// short by the caller's bound, a cluster of up to eight CTAs shares it and joins
+// its sums through distributed shared memory: one launch, no workspace.
+// Longer ones are counted in units of 64 tokens; the units of all segments form
+// one line, which is cut into equal pieces, one per CTA, from the lengths on the
+// device.  Long and short sequences balance without the host knowing them, and a
+// captured call stays right as they grow.  A segment that a cut crosses leaves
+// partial sums in the workspace, which a second kernel joins in a fixed order.
 //
 // Bound.  HBM: 144 bytes per (token, KV head) at d = 128, against about 240
 // issued warp instructions per 16 tokens and head.  Each warp streams its own
@@ -50,6 +52,8 @@ constexpr int UNIT = TOK * WARPS;   // tokens of a work unit
 constexpr float HEADROOM = 5.f;     // log2 a score may pass the reference by
 constexpr float SHIFT = 10.f;       // log2 of the factor that p carries: p < 2^15
 constexpr int MIN_UNITS = 2;        // shortest piece of the line worth a CTA
+constexpr int MAX_CLUSTER = 8;      // CTAs that share a segment, at most
+constexpr int CLUSTER_UNITS = 16;   // units of a segment per CTA of a cluster, at most
 
 // Per row-tile width (NT tiles of 8 query rows): CTAs per SM, ring stages, and
 // the most CTAs a launch has (the workspace holds two partial results each).
@@ -81,7 +85,7 @@ struct DecArgs {
   long long q_s[3], o_s[3];
   const int32_t* seqlens;
   int batch, heads_kv, group, q_len, rows, row_tiles, max_len;
-  int causal, f16, split;
+  int causal, f16, split, cluster;
   float sigma_log2;
   float* lse;
   long long lse_pitch;
@@ -128,7 +132,7 @@ constexpr int MERGE_ROW = D + 12;
 template <int D, int NT>
 constexpr int smem_bytes() {
   constexpr int ring = WARPS * Shape<NT>::STAGES * Stage<D>::BYTES;
-  constexpr int merge = WARPS * 8 * NT * MERGE_ROW<D> * 4;
+  constexpr int merge = (WARPS * MERGE_ROW<D> + D) * 8 * NT * 4;
   return ring > merge ? ring : merge;
 }
 
@@ -187,6 +191,21 @@ __device__ __forceinline__ Piece cut(const DecArgs& a, int* sh) {
   return p;
 }
 
+// Four elements of an output row, and with the first of them its log-sum-exp:
+// `row` is the query row within the KV head's group, y and l are relative to m.
+__device__ __forceinline__ void store_row4(const DecArgs& a, int b, int kvh, int row, int d0,
+                                           float m, float l, float4 y) {
+  const int i = row / a.group, h = kvh * a.group + (row - i * a.group);
+  const float inv = l == 0.f ? 0.f : pow2f(head_exp(a.vexp, kvh)) / l;
+  uint2 w;
+  w.x = f32_to_x2(y.x * inv, y.y * inv, a.f16);
+  w.y = f32_to_x2(y.z * inv, y.w * inv, a.f16);
+  *reinterpret_cast<uint2*>(a.o + b * a.o_s[0] + h * a.o_s[1] + i * a.o_s[2] + d0) = w;
+  if (a.lse != nullptr && d0 == 0)
+    a.lse[h * a.lse_pitch + static_cast<long long>(b) * a.q_len + i] =
+        l == 0.f ? -INFINITY : (m - SHIFT + log2f(l)) * 0.6931471805599453f;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const DecArgs a) {
   constexpr int STAGES = Shape<NT>::STAGES;
@@ -199,6 +218,7 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
   __shared__ uint2 sh_q[NT * KSTEPS * 32];
   __shared__ float sh_sc[ROWS];
   __shared__ float2 sh_ml[WARPS][ROWS];
+  __shared__ float2 sh_cluster[ROWS];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
@@ -207,11 +227,12 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
   if (a.split) {
     if (tid == 0) a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
     piece = cut(a, sh_cut);
-  } else {  // one whole segment per CTA
-    piece.b = static_cast<int>(blockIdx.x) / (a.heads_kv * a.row_tiles);
+  } else {  // one segment per cluster; u walks over it once
+    const int seg = static_cast<int>(blockIdx.x) / a.cluster, per_b = a.heads_kv * a.row_tiles;
+    piece.b = seg / per_b;
     const int n = units_of(clamp_len(a, piece.b));
     piece.base = 0;
-    piece.begin = (static_cast<int>(blockIdx.x) - piece.b * a.heads_kv * a.row_tiles) * n;
+    piece.begin = (seg - piece.b * per_b) * n;
     piece.end = piece.begin + n;
     piece.per_cta = n;
   }
@@ -235,7 +256,12 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
     const int max_lim = a.causal ? max(0, len - a.q_len + last_i + 1) : len;
 
     // ---- this warp's tiles: an equal run of the piece's
-    const int t0 = u0 * WARPS, t1 = min(u1 * WARPS, (max_lim + TOK - 1) / TOK);
+    int t0 = u0 * WARPS, t1 = min(u1 * WARPS, (max_lim + TOK - 1) / TOK);
+    if (a.cluster > 1) {  // this CTA's share of the segment
+      const int share = (t1 + a.cluster - 1) / a.cluster;
+      t0 = min(t1, static_cast<int>(cluster_rank()) * share);
+      t1 = min(t1, t0 + share);
+    }
     const int run = (max(0, t1 - t0) + WARPS - 1) / WARPS;
     const int t_begin = t0 + warp * run, t_end = min(t1, t_begin + run);
     const int n_tiles = max(0, t_end - t_begin);
@@ -597,42 +623,87 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
         }
       }
     __syncthreads();
+    if (a.cluster > 1) {
+      // The CTA's sums to its own shared memory, where the cluster reads them:
+      // each CTA joins an equal part of the outputs, over the CTAs in order.
+      float* sums = merge + WARPS * ROWS * MERGE_ROW<D>;
+      for (int x = tid; x < n_rows * (D / 4); x += THREADS) {
+        const int r = x / (D / 4), d0 = (x % (D / 4)) * 4;
+        const float* src = merge + r * MERGE_ROW<D> + merge_pos<D>(d0);
+        float4 y = make_float4(src[0], src[1], src[2], src[3]);
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w) {
+          src += ROWS * MERGE_ROW<D>;
+          y.x += src[0], y.y += src[1], y.z += src[2], y.w += src[3];
+        }
+        *reinterpret_cast<float4*>(sums + r * D + d0) = y;
+        if (d0 == 0) {
+          float m = sh_ml[0][r].x, l = 0.f;
+#pragma unroll
+          for (int w = 1; w < WARPS; ++w) m = fmaxf(m, sh_ml[w][r].x);
+#pragma unroll
+          for (int w = 0; w < WARPS; ++w) {
+            const float2 ml = sh_ml[w][r];
+            l += m == -INFINITY ? ml.y : ml.y * ex2_approx(ml.x - m);
+          }
+          sh_cluster[r] = make_float2(m, l);
+        }
+      }
+      cluster_sync();
+      for (int x = tid * a.cluster + cluster_rank(); x < n_rows * (D / 4);
+           x += THREADS * a.cluster) {
+        const int r = x / (D / 4), d0 = (x % (D / 4)) * 4;
+        const uint32_t at = smem_u32(sums + r * D + d0), at_ml = smem_u32(sh_cluster + r);
+        float2 ml[MAX_CLUSTER];
+        float4 part[MAX_CLUSTER];
+#pragma unroll
+        for (int k = 0; k < MAX_CLUSTER; ++k) {
+          if (k < a.cluster) {
+            ml[k] = cluster_ld2(at_ml, k);
+            part[k] = cluster_ld4(at, k);
+          }
+        }
+        float m = ml[0].x;
+#pragma unroll
+        for (int k = 1; k < MAX_CLUSTER; ++k)
+          if (k < a.cluster) m = fmaxf(m, ml[k].x);
+        float l = 0.f;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < MAX_CLUSTER; ++k) {
+          if (k < a.cluster) {
+            const float f = m == -INFINITY ? 1.f : ex2_approx(ml[k].x - m);
+            l += ml[k].y * f;
+            y.x += part[k].x * f, y.y += part[k].y * f;
+            y.z += part[k].z * f, y.w += part[k].w * f;
+          }
+        }
+        store_row4(a, b, kvh, r0 + r, d0, m, l, y);
+      }
+      cluster_sync();  // no CTA leaves while another reads its sums
+      return;
+    }
     const bool whole = u0 == 0 && u1 == n_units;
     const int part = 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0);
-    const float v_up = pow2f(head_exp(a.vexp, kvh));
-    for (int x = tid; x < n_rows * (D / 8); x += THREADS) {
-      const int r = x / (D / 8), d0 = (x % (D / 8)) * 8;
+    for (int x = tid; x < n_rows * (D / 4); x += THREADS) {
+      const int r = x / (D / 4), d0 = (x % (D / 4)) * 4;
       float m = sh_ml[0][r].x;
 #pragma unroll
       for (int w = 1; w < WARPS; ++w) m = fmaxf(m, sh_ml[w][r].x);
-      float l = 0.f, y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = 0.f;
+      float l = 0.f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) {
         const float2 ml = sh_ml[w][r];
         l += m == -INFINITY ? ml.y : ml.y * ex2_approx(ml.x - m);
         const float* src = merge + (w * ROWS + r) * MERGE_ROW<D> + merge_pos<D>(d0);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] += src[e];
+        y.x += src[0], y.y += src[1], y.z += src[2], y.w += src[3];
       }
       if (whole) {
-        const int row = r0 + r, i = row / a.group, h = kvh * a.group + (row - i * a.group);
-        const float inv = l == 0.f ? 0.f : v_up / l;
-        uint4 w;
-        w.x = f32_to_x2(y[0] * inv, y[1] * inv, a.f16);
-        w.y = f32_to_x2(y[2] * inv, y[3] * inv, a.f16);
-        w.z = f32_to_x2(y[4] * inv, y[5] * inv, a.f16);
-        w.w = f32_to_x2(y[6] * inv, y[7] * inv, a.f16);
-        *reinterpret_cast<uint4*>(a.o + b * a.o_s[0] + h * a.o_s[1] + i * a.o_s[2] + d0) = w;
-        if (a.lse != nullptr && d0 == 0)
-          a.lse[h * a.lse_pitch + static_cast<long long>(b) * a.q_len + i] =
-              l == 0.f ? -INFINITY : (m - SHIFT + log2f(l)) * 0.6931471805599453f;
+        store_row4(a, b, kvh, r0 + r, d0, m, l, y);
       } else {
-        float4* dst = reinterpret_cast<float4*>(
-            a.part_o + (static_cast<long long>(part) * ROWS + r) * D + d0);
-        dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-        dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+        *reinterpret_cast<float4*>(
+            a.part_o + (static_cast<long long>(part) * ROWS + r) * D + d0) = y;
         if (d0 == 0) a.part_ml[static_cast<long long>(part) * ROWS + r] = make_float2(m, l);
       }
     }
@@ -701,22 +772,14 @@ __global__ void __launch_bounds__(THREADS) decode4_join_kernel(const DecArgs a) 
     y.z += x.z * e;
     y.w += x.w * e;
   }
-  const int i = row / a.group, h = kvh * a.group + (row - i * a.group);
-  const float inv = l == 0.f ? 0.f : pow2f(head_exp(a.vexp, kvh)) / l;
-  uint2 w;
-  w.x = f32_to_x2(y.x * inv, y.y * inv, a.f16);
-  w.y = f32_to_x2(y.z * inv, y.w * inv, a.f16);
-  *reinterpret_cast<uint2*>(a.o + b * a.o_s[0] + h * a.o_s[1] + i * a.o_s[2] + 4 * lane) = w;
-  if (a.lse != nullptr && lane == 0)
-    a.lse[h * a.lse_pitch + static_cast<long long>(b) * a.q_len + i] =
-        l == 0.f ? -INFINITY : (m - SHIFT + log2f(l)) * 0.6931471805599453f;
+  store_row4(a, b, kvh, row, 4 * lane, m, l, y);
 }
 
 // Query row tiles of a call: as few tensor-core columns as hold its rows, up
 // to 32 to a CTA.
 struct Plan {
-  int nt, row_tiles, units, max_grid;
-  long long all_units;
+  int nt, row_tiles, units, max_grid, cluster;
+  long long segments, all_units;
   bool split;
 };
 
@@ -727,11 +790,16 @@ Plan plan_of(const bsfa_cache4* c, const bsfa_decode4_params* p) {
   pl.row_tiles = static_cast<int>((rows + 8 * pl.nt - 1) / (8 * pl.nt));
   pl.units = (p->max_seqlen + UNIT - 1) / UNIT;
   if (pl.units < 1) pl.units = 1;
-  pl.all_units = static_cast<long long>(p->batch) * c->num_heads_kv * pl.row_tiles * pl.units;
+  pl.segments = static_cast<long long>(p->batch) * c->num_heads_kv * pl.row_tiles;
+  pl.all_units = pl.segments * pl.units;
   pl.max_grid = pl.nt == 1 ? Shape<1>::MAX_GRID : pl.nt == 2 ? Shape<2>::MAX_GRID
                                                              : Shape<4>::MAX_GRID;
-  // A segment of so few units is one CTA's work: no parts, no second kernel.
-  pl.split = pl.units > 2 * MIN_UNITS;
+  pl.cluster = 1;
+  while (pl.cluster < MAX_CLUSTER && pl.units >= 2 * pl.cluster &&
+         (pl.segments * pl.cluster < pl.max_grid || pl.units > CLUSTER_UNITS * pl.cluster))
+    pl.cluster *= 2;
+  pl.split = pl.units > CLUSTER_UNITS * pl.cluster;
+  if (pl.split) pl.cluster = 1;
   return pl;
 }
 
@@ -762,7 +830,10 @@ bsfa_status validate_sizes(const bsfa_cache4* c, const bsfa_decode4_params* p) {
   if (p->max_seqlen > static_cast<long long>(c->block_table_width) * c->page_size)
     return BSFA_ERR_INVALID_ARG;
   const long long rows = static_cast<long long>(p->num_heads_q / c->num_heads_kv) * p->q_len;
-  if (rows > (1 << 24) || plan_of(c, p).all_units > 0x7fffffffLL - 4096) return BSFA_ERR_UNSUPPORTED;
+  if (rows > (1 << 24)) return BSFA_ERR_UNSUPPORTED;
+  const Plan pl = plan_of(c, p);
+  if (pl.all_units > 0x7fffffffLL - 4096 || pl.segments * pl.cluster > 0x7fffffffLL)
+    return BSFA_ERR_UNSUPPORTED;
   return BSFA_OK;
 }
 
@@ -778,16 +849,27 @@ bsfa_status launch(const DecArgs& a, const Plan& pl, int sms, int dev, cudaStrea
       return BSFA_ERR_CUDA;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  long long grid = static_cast<long long>(a.batch) * a.heads_kv * a.row_tiles;
-  if (pl.split) {
-    const long long full = static_cast<long long>(sms) * Shape<NT>::CTAS;
-    grid = full < pl.max_grid ? full : pl.max_grid;
-    const long long most = (pl.all_units + MIN_UNITS - 1) / MIN_UNITS;
-    if (most < grid) grid = most;
+  if (!pl.split) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(pl.segments * pl.cluster));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = pl.cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, decode4_kernel<D, NT>, a) == cudaSuccess ? BSFA_OK
+                                                                             : BSFA_ERR_CUDA;
   }
+  const long long full = static_cast<long long>(sms) * Shape<NT>::CTAS;
+  long long grid = full < pl.max_grid ? full : pl.max_grid;
+  const long long most = (pl.all_units + MIN_UNITS - 1) / MIN_UNITS;
+  if (most < grid) grid = most;
   decode4_kernel<D, NT><<<static_cast<unsigned>(grid), THREADS, smem, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return BSFA_ERR_CUDA;
-  if (!pl.split) return BSFA_OK;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), a.rows < 8 * NT ? a.rows : 8 * NT);
   cfg.blockDim = dim3(THREADS);
@@ -869,6 +951,7 @@ bsfa_status bsfa_decode4(const bsfa_cache4* cache, const bsfa_decode4_params* p,
   a.causal = p->causal != 0;
   a.f16 = p->dtype == BSFA_DTYPE_F16;
   a.split = pl.split;
+  a.cluster = pl.cluster;
   const float sigma =
       p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt((float)cache->head_dim);
   a.sigma_log2 = sigma * 1.4426950408889634f;

@@ -35,31 +35,35 @@ HEADS = [(2, 2, 1), (8, 2, 1), (8, 1, 1), (9, 3, 2), (12, 1, 1), (4, 1, 4), (8, 
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("heads", HEADS)
-@pytest.mark.parametrize("short", [True, False])
-def test_against_the_oracle(cuda_device, d, heads, short):
-    """Ragged batches from an empty sequence to several pieces per sequence;
-    rows past each end hold NaN scales."""
+@pytest.mark.parametrize("bound", [256, 1400, 9000])
+def test_against_the_oracle(cuda_device, d, heads, bound):
+    """Ragged batches, an empty sequence among them, shared by clusters of four
+    and eight and cut into pieces; rows past each end hold NaN scales."""
     b = _bsfa()
     Hq, Hkv, n = heads
-    lens = [1, 0, 16, 250, 17] if short else [700, 1, 0, 64, 1301, 129]
+    lens = [1, 0, 16, 250, 17] if bound == 256 else [700, 1, 0, 64, 1301, 129]
     page, layout = (16, "pthd") if (Hq + d) % 3 == 0 else (48, "phtd")
     dtype = BF if n % 2 else HF
     cache, table, rows = cu.random_cache(b, lens, page, Hkv, d, 10 * Hq + n, cuda_device,
                                          layout=layout, exps=Hkv == 2)
     q = _queries(len(lens), Hq, n, d, dtype, Hq, cuda_device, 1.5)
-    res = b.decode4(q, cache, table, _i32(lens, cuda_device), return_lse=True,
-                    max_seqlen=256 if short else None)
+    table = cu.widen(table, page, bound)
+    res = b.decode4(q, cache, table, _i32(lens, cuda_device), return_lse=True, max_seqlen=bound)
     cu.check_decode(res, q, rows, lens, dtype, d)
 
 
 @pytest.mark.parametrize("length", [1, 2, 15, 16, 17, 63, 64, 65, 127, 256, 257, 511, 1000])
 def test_every_kind_of_length(cuda_device, length):
-    """One sequence, whole and cut, at tile, unit and page borders."""
+    """One sequence at tile, unit and page borders: cut into pieces, shared by a
+    cluster, by one CTA."""
     b = _bsfa()
     cache, table, rows = cu.random_cache(b, [length], 32, 2, 128, length, cuda_device)
     q = _queries(1, 8, 1, 128, BF, length, cuda_device, 2.0)
-    for most in (None, length):
-        res = b.decode4(q, cache, table, _i32([length], cuda_device), return_lse=True,
+    wide = cu.widen(table, 32)
+    for most in (9000, 1024, 64, length):
+        if most < length:
+            continue
+        res = b.decode4(q, cache, wide, _i32([length], cuda_device), return_lse=True,
                         max_seqlen=most)
         cu.check_decode(res, q, rows, [length], BF, 128)
 
@@ -73,8 +77,9 @@ def test_queries_longer_than_the_cache(cuda_device, causal, n):
     lens = [2, 90, 0, 40]
     cache, table, rows = cu.random_cache(b, lens, 16, 2, 64, n, cuda_device)
     q = _queries(4, 4, n, 64, HF, n, cuda_device)
-    res = b.decode4(q, cache, table, _i32(lens, cuda_device), causal=causal, return_lse=True)
-    cu.check_decode(res, q, rows, lens, HF, 64, causal=causal)
+    for t in (table, cu.widen(table, 16)):
+        res = b.decode4(q, cache, t, _i32(lens, cuda_device), causal=causal, return_lse=True)
+        cu.check_decode(res, q, rows, lens, HF, 64, causal=causal)
     if causal and n > 2:
         assert not res["out"][0, :, :n - 2].any()
         assert bool(torch.isneginf(res["lse"][:, :n - 2]).all())
@@ -136,6 +141,7 @@ def test_nan_rows_reach_only_the_queries_that_see_them(cuda_device, where, d):
     b = _bsfa()
     L, n = 85, 6
     cache, table, rows = cu.random_cache(b, [L], 32, 1, d, 3, cuda_device)
+    table = cu.widen(table, 32) if d == 64 else table
     q = _queries(1, 2, n, d, BF, 3, cuda_device)
     clean = b.decode4(q, cache, table, _i32([L], cuda_device), return_lse=True)
     t, group = 82, 2  # seen by queries i with 82 <= 85 - 6 + i, that is i >= 3
@@ -189,8 +195,9 @@ def test_sharp_and_flat_rows(cuda_device):
     q[0, 1] = -400.0
     q[0, 2] = 0.0
     q[0, 3] = 3.0
-    res = b.decode4(q, cache, table, _i32([L], cuda_device), return_lse=True)
-    cu.check_decode(res, q, rows, [L], BF, d)
+    for t in (table, cu.widen(table, 16)):
+        res = b.decode4(q, cache, t, _i32([L], cuda_device), return_lse=True)
+        cu.check_decode(res, q, rows, [L], BF, d)
 
 
 def test_runs_repeat_bit_for_bit_whatever_the_workspace_holds(cuda_device):
@@ -198,6 +205,7 @@ def test_runs_repeat_bit_for_bit_whatever_the_workspace_holds(cuda_device):
     from block_sparse_gated_gb300 import cache4
     lens = [3000, 10, 777]
     cache, table, rows = cu.random_cache(b, lens, 64, 2, 128, 4, cuda_device)
+    table = cu.widen(table, 64)
     q = _queries(3, 16, 1, 128, BF, 4, cuda_device)
     n32 = _i32(lens, cuda_device)
     need = cache4.decode4_workspace_bytes(q, cache, table, n32)
@@ -212,13 +220,15 @@ def test_runs_repeat_bit_for_bit_whatever_the_workspace_holds(cuda_device):
         b.decode4(q, cache, table, n32, workspace=ws[:need - 256])
 
 
-def test_graphs_follow_the_lengths_and_streams_do_not_mix(cuda_device):
+@pytest.mark.parametrize("cut", [True, False])
+def test_graphs_follow_the_lengths_and_streams_do_not_mix(cuda_device, cut):
     """A captured call reads the lengths at replay; two graphs with workspaces
     of their own run on two streams at once."""
     b = _bsfa()
     from block_sparse_gated_gb300 import cache4
     lens = [2000, 1500]
     cache, table, rows = cu.random_cache(b, lens, 32, 2, 64, 21, cuda_device)
+    table = cu.widen(table, 32) if cut else table
     q = [_queries(2, 8, 1, 64, HF, s, cuda_device) for s in (1, 2)]
     n32 = [_i32(lens, cuda_device) for _ in range(2)]
     need = cache4.decode4_workspace_bytes(q[0], cache, table, n32[0])
@@ -249,11 +259,13 @@ def test_graphs_follow_the_lengths_and_streams_do_not_mix(cuda_device):
     assert torch.equal(r["out"], outs[0])
 
 
-def test_a_batch_of_many_short_and_one_long(cuda_device):
-    """300 sequences over more than one piece each, and pieces over many."""
+@pytest.mark.parametrize("cut", [True, False])
+def test_a_batch_of_many_short_and_one_long(cuda_device, cut):
+    """300 sequences, many of them in one piece and one over many pieces."""
     b = _bsfa()
     lens = [int(x) for x in np.random.default_rng(1).integers(0, 40, 299)] + [5000]
     cache, table, rows = cu.random_cache(b, lens, 16, 1, 64, 2, cuda_device)
+    table = cu.widen(table, 16) if cut else table
     q = _queries(300, 2, 1, 64, BF, 2, cuda_device)
     res = b.decode4(q, cache, table, _i32(lens, cuda_device), return_lse=True)
     cu.check_decode(res, q, rows, lens, BF, 64)
