@@ -51,7 +51,10 @@ constexpr int TOK = 16;             // tokens of a warp's tile
 constexpr int UNIT = TOK * WARPS;   // tokens of a work unit
 constexpr float HEADROOM = 5.f;     // log2 a score may pass the reference by
 constexpr float SHIFT = 10.f;       // log2 of the factor that p carries: p < 2^15
-constexpr int MIN_UNITS = 2;        // shortest piece of the line worth a CTA
+constexpr int MIN_UNITS = 4;        // shortest piece of the line worth a CTA
+constexpr int SEGMENT_UNITS = 5;    // a segment's fixed cost, in units
+constexpr int JOIN_THREADS = 256;   // of the kernel that joins parts
+constexpr int MAX_PARTS = 768;      // parts of a segment, at most: CTAs of a cut call
 constexpr int MAX_CLUSTER = 8;      // CTAs that share a segment, at most
 constexpr int CLUSTER_UNITS = 16;   // units of a segment per CTA of a cluster, at most
 
@@ -98,7 +101,11 @@ struct DecArgs {
 __device__ __forceinline__ int clamp_len(const DecArgs& a, int b) {
   return max(0, min(__ldg(a.seqlens + b), a.max_len));
 }
-__device__ __forceinline__ int units_of(int len) { return max(1, (len + UNIT - 1) / UNIT); }
+// Units of a segment on the line: its tokens', and what a CTA spends on any
+// segment (queries, the first copies' latency, the join of its warps): without it
+// the CTAs with many short sequences end last (64 ragged sequences to 16K: 136 us
+// at 0, 127 at 3, 124 at 5; eight to 64K: 67, 62, 61).
+__device__ __forceinline__ int units_of(int len) { return SEGMENT_UNITS + (len + UNIT - 1) / UNIT; }
 
 // Byte offset in a warp's stage of row `t` (0..15), 16-byte chunk `c`.  Rows
 // are paired into 128-byte lines and chunks permuted so that both readers --
@@ -256,7 +263,8 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
     const int max_lim = a.causal ? max(0, len - a.q_len + last_i + 1) : len;
 
     // ---- this warp's tiles: an equal run of the piece's
-    int t0 = u0 * WARPS, t1 = min(u1 * WARPS, (max_lim + TOK - 1) / TOK);
+    int t0 = max(0, u0 - SEGMENT_UNITS) * WARPS;
+    int t1 = min(max(0, u1 - SEGMENT_UNITS) * WARPS, (max_lim + TOK - 1) / TOK);
     if (a.cluster > 1) {  // this CTA's share of the segment
       const int share = (t1 + a.cluster - 1) / a.cluster;
       t0 = min(t1, static_cast<int>(cluster_rank()) * share);
@@ -580,17 +588,22 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
 
     uint32_t rd = my_ring, wr = my_ring + (STAGES - 1) * St::BYTES;
     const uint32_t ring_end = my_ring + STAGES * St::BYTES;
-    for (int tok0 = t_begin * TOK; tok0 < t_end * TOK; tok0 += TOK) {
+    auto next_tile = [&]() {
       cp_async_wait<STAGES - 2>();
       __syncwarp();  // every lane's copies of this tile are in, and the last one is read
       copy_tile(wr);
-      if (tok0 + TOK <= min_lim)
-        tile(rd, tok0, std::false_type{});
-      else
-        tile(rd, tok0, std::true_type{});
+      const uint32_t st = rd;
       rd = rd + St::BYTES == ring_end ? my_ring : rd + St::BYTES;
       wr = wr + St::BYTES == ring_end ? my_ring : wr + St::BYTES;
-    }
+      return st;
+    };
+    // Tiles that every row sees in whole come first; the few others take the
+    // masked path in a loop of their own (one loop with a branch would move the
+    // sums between registers at every join of the two).
+    const int t_full = max(t_begin, min(t_end, min_lim / TOK));
+    int t = t_begin;
+    for (; t < t_full; ++t) tile(next_tile(), 0, std::false_type{});
+    for (; t < t_end; ++t) tile(next_tile(), t * TOK, std::true_type{});
     cp_async_wait<0>();
 
     // ---- join the warps: common reference, then one sum of the scaled parts
@@ -721,56 +734,69 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
 
 // Joins the parts of the segments that a cut crossed: block (x, r) takes row r
 // of the segment that CTA x began and did not finish, if there is one.  The
-// parts lie in the CTAs x (its second slot) .. last (their first slots).
+// parts lie in the CTAs x (its second slot) .. last (their first slots).  The
+// references come first, all at once, so that the sums' loads wait for nothing.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(THREADS) decode4_join_kernel(const DecArgs a) {
-  constexpr int LANES = D / 4;              // threads that cover a row, four elements each
-  constexpr int PARTS = THREADS / LANES;    // parts read at once
+__global__ void __launch_bounds__(JOIN_THREADS) decode4_join_kernel(const DecArgs a) {
+  constexpr int LANES = D / 4;                 // threads that cover a row, four elements each
+  constexpr int PARTS = JOIN_THREADS / LANES;  // parts read at once
   __shared__ float4 sh_y[PARTS][LANES];
-  __shared__ float2 sh_ml[PARTS];
+  __shared__ float2 sh_ml[JOIN_THREADS / 32];
+  __shared__ float sh_w[MAX_PARTS];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 job = a.joins[blockIdx.x];
   if (job.x < 0) return;
   const int b = job.x, kvh = job.y / a.row_tiles;
   const int r = blockIdx.y, row = (job.y - kvh * a.row_tiles) * ROWS + r;
   if (row >= a.rows) return;
-  const int first = blockIdx.x, count = job.z - first + 1;
-  const int lane = threadIdx.x % LANES, p0 = threadIdx.x / LANES;
-  float m = -INFINITY, l = 0.f;
+  const int first = blockIdx.x, count = job.z - first + 1;  // count <= gridDim.x <= MAX_PARTS
+  const int tid = threadIdx.x;
+  auto slot = [&](int p) { return 2LL * (first + p) + (p == 0 ? 1 : 0); };
+
+  float2 mine[MAX_PARTS / JOIN_THREADS];
+  float m = -INFINITY;
+#pragma unroll
+  for (int x = 0; x < MAX_PARTS / JOIN_THREADS; ++x) {
+    const int p = tid + x * JOIN_THREADS;
+    mine[x] = p < count ? a.part_ml[slot(p) * ROWS + r] : make_float2(-INFINITY, 0.f);
+    m = fmaxf(m, mine[x].x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((tid & 31) == 0) sh_ml[tid >> 5].x = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < JOIN_THREADS / 32; ++w) m = fmaxf(m, sh_ml[w].x);
+  float l = 0.f;
+#pragma unroll
+  for (int x = 0; x < MAX_PARTS / JOIN_THREADS; ++x) {
+    const float w = m == -INFINITY ? 1.f : ex2_approx(mine[x].x - m);
+    l += mine[x].y * w;
+    sh_w[tid + x * JOIN_THREADS] = w;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if ((tid & 31) == 0) sh_ml[tid >> 5].y = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < JOIN_THREADS / 32; ++w) l += sh_ml[w].y;
+
+  const int lane = tid % LANES, p0 = tid / LANES;
   float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
   for (int p = p0; p < count; p += PARTS) {
-    const long long part = 2LL * (first + p) + (p == 0 ? 1 : 0);
-    const float2 ml = a.part_ml[part * ROWS + r];
-    const float4 x = reinterpret_cast<const float4*>(a.part_o + (part * ROWS + r) * D)[lane];
-    const float m1 = fmaxf(m, ml.x);
-    const float f = m1 == -INFINITY ? 1.f : ex2_approx(m - m1);
-    const float e = m1 == -INFINITY ? 1.f : ex2_approx(ml.x - m1);
-    m = m1;
-    l = l * f + ml.y * e;
-    y.x = y.x * f + x.x * e;
-    y.y = y.y * f + x.y * e;
-    y.z = y.z * f + x.z * e;
-    y.w = y.w * f + x.w * e;
+    const float4 x = reinterpret_cast<const float4*>(a.part_o + (slot(p) * ROWS + r) * D)[lane];
+    const float w = sh_w[p];
+    y.x += x.x * w, y.y += x.y * w, y.z += x.z * w, y.w += x.w * w;
   }
   sh_y[p0][lane] = y;
-  if (lane == 0) sh_ml[p0] = make_float2(m, l);
   __syncthreads();
   if (p0 != 0) return;
 #pragma unroll
-  for (int p = 1; p < PARTS; ++p) m = fmaxf(m, sh_ml[p].x);
-  l = 0.f;
-  y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int p = 0; p < PARTS; ++p) {
-    const float2 ml = sh_ml[p];
-    const float e = m == -INFINITY ? 1.f : ex2_approx(ml.x - m);
+  for (int p = 1; p < PARTS; ++p) {
     const float4 x = sh_y[p][lane];
-    l += ml.y * e;
-    y.x += x.x * e;
-    y.y += x.y * e;
-    y.z += x.z * e;
-    y.w += x.w * e;
+    y.x += x.x, y.y += x.y, y.z += x.z, y.w += x.w;
   }
   store_row4(a, b, kvh, row, 4 * lane, m, l, y);
 }
@@ -791,7 +817,7 @@ Plan plan_of(const bsfa_cache4* c, const bsfa_decode4_params* p) {
   pl.units = (p->max_seqlen + UNIT - 1) / UNIT;
   if (pl.units < 1) pl.units = 1;
   pl.segments = static_cast<long long>(p->batch) * c->num_heads_kv * pl.row_tiles;
-  pl.all_units = pl.segments * pl.units;
+  pl.all_units = pl.segments * (pl.units + SEGMENT_UNITS);
   pl.max_grid = pl.nt == 1 ? Shape<1>::MAX_GRID : pl.nt == 2 ? Shape<2>::MAX_GRID
                                                              : Shape<4>::MAX_GRID;
   pl.cluster = 1;
@@ -840,6 +866,7 @@ bsfa_status validate_sizes(const bsfa_cache4* c, const bsfa_decode4_params* p) {
 template <int D, int NT>
 bsfa_status launch(const DecArgs& a, const Plan& pl, int sms, int dev, cudaStream_t stream) {
   constexpr int smem = smem_bytes<D, NT>();
+  static_assert(Shape<NT>::MAX_GRID <= MAX_PARTS, "the join's weights");
   // The shared-memory size of a kernel is set once per device.
   static std::atomic<uint64_t> ready{0};
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
@@ -872,7 +899,7 @@ bsfa_status launch(const DecArgs& a, const Plan& pl, int sms, int dev, cudaStrea
   if (cudaGetLastError() != cudaSuccess) return BSFA_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), a.rows < 8 * NT ? a.rows : 8 * NT);
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(JOIN_THREADS);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
