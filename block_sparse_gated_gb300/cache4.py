@@ -116,28 +116,36 @@ def _int32_vector(t, n: int, what: str):
     return t.data_ptr()
 
 
-def _rows_fields(k, v, layout, cu_seqlens, start, heads: int, d: int):
+def _rows_fields(k, v, layout, cu_seqlens, start, heads: int, d: int, device):
     """The packed bsfa_cache4_rows of a call, and its number of sequences."""
     varlen = cu_seqlens is not None
     if layout is None:
         layout = "htd" if varlen else "bhld"
-    if k.shape != v.shape:
+    shape = k.shape
+    if v.shape != shape:
         raise ValueError("K and V shapes disagree")
-    if k.dtype != v.dtype:
+    if v.dtype is not k.dtype:
         raise TypeError("K and V must share one element type")
+    if device.type != "cuda" or k.device != device or v.device != device:
+        _on_device(device, k=k, v=v)
     ks, hk, n = _strides_bhtd(k, layout, varlen)
-    vs, _, _ = _strides_bhtd(v, layout, varlen)
-    if hk != heads or k.shape[-1] != d:
+    vs = ks if v.stride() == k.stride() else _strides_bhtd(v, layout, varlen)[0]
+    if hk != heads or shape[-1] != d:
         raise ValueError("K and V must have the cache's heads and head dimension")
-    cu = 0
+    cu = first = 0
     if varlen:
         if cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or \
                 not cu_seqlens.is_contiguous() or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be a contiguous int32 [batch + 1] tensor")
+        if cu_seqlens.device != device:
+            _on_device(device, cu_seqlens=cu_seqlens)
         batch, cu = cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
     else:
-        batch = 1 if k.dim() == 3 else k.shape[0]
-    first = 0 if start is None else _int32_vector(start, batch, "start")
+        batch = 1 if len(shape) == 3 else shape[0]
+    if start is not None:
+        first = _int32_vector(start, batch, "start")
+        if start.device != device:
+            _on_device(device, start=start)
     return _native.CACHE4_ROWS.pack(k.data_ptr(), v.data_ptr(), *ks, *vs, batch, n, cu, first,
                                     _dtype_code(k)), batch
 
@@ -192,8 +200,7 @@ def cache4_write(cache: KVCache4, k, v, block_table, *, start=None, cu_seqlens=N
     at most 448; elements round to the nearest e2m1 value, ties to the even
     code.  A group that holds an infinity or a NaN reads back as NaN."""
     dev = k.device
-    _on_device(dev, v=v, start=start, cu_seqlens=cu_seqlens)
-    r, batch = _rows_fields(k, v, layout, cu_seqlens, start, *_heads_and_dim(cache))
+    r, batch = _rows_fields(k, v, layout, cu_seqlens, start, *_heads_and_dim(cache), dev)
     c, _ = _cache_fields(cache, block_table, dev, batch)
     _call("bsfa_cache4_write", dev, stream, c, r)
 
@@ -214,22 +221,27 @@ def cache4_read(cache: KVCache4, block_table, *, seqlen=None, total=None, start=
         layout = "htd" if varlen else "bhld"
     if out is None:
         n = total if varlen else seqlen
-        if n is None or int(n) < 0:
+        if n is None or n < 0:
             raise ValueError("a varlen read needs total, a batched one seqlen")
+        if layout == "bhld" and not varlen:
+            shape = (block_table.shape[0], heads, n, d)
+        elif layout == "blhd" and not varlen:
+            shape = (block_table.shape[0], n, heads, d)
+        elif layout == "htd" and varlen:
+            shape = (heads, n, d)
+        elif layout == "thd" and varlen:
+            shape = (n, heads, d)
+        else:
+            raise ValueError(layout)
         if dtype not in _DTYPES:
             raise TypeError("expected bfloat16 or float16")
-        shapes = {"bhld": (block_table.shape[0], heads, int(n), d),
-                  "blhd": (block_table.shape[0], int(n), heads, d),
-                  "htd": (heads, int(n), d), "thd": (int(n), heads, d)}
-        if layout not in (("htd", "thd") if varlen else ("bhld", "blhd")):
-            raise ValueError(layout)
-        k, v = (torch.empty(shapes[layout], dtype=dtype, device=dev) for _ in range(2))
+        k = torch.empty(shape, dtype=dtype, device=dev)
+        v = torch.empty(shape, dtype=dtype, device=dev)
         if stream is not None:
             _made_here(stream, dev, k, v)
     else:
         k, v = out
-    _on_device(dev, k=k, v=v, start=start, cu_seqlens=cu_seqlens)
-    r, batch = _rows_fields(k, v, layout, cu_seqlens, start, heads, d)
+    r, batch = _rows_fields(k, v, layout, cu_seqlens, start, heads, d, dev)
     c, _ = _cache_fields(cache, block_table, dev, batch)
     _call("bsfa_cache4_read", dev, stream, c, r)
     return k, v
@@ -276,14 +288,17 @@ def decode4(q, cache: KVCache4, block_table, seqlens, *, max_seqlen=None, softma
     ``max_seqlen`` bounds the lengths (default: what the block table can hold;
     longer entries of seqlens are cut to it); the call reads lengths on the
     device only, so a captured graph stays right as they grow within it.
-    ``workspace``: at least ``decode4_workspace_bytes`` of device memory, not
-    shared by calls that may overlap (default: allocated for the call)."""
+    ``workspace``: at least ``decode4_workspace_bytes`` of device memory (0 for
+    bounds up to 8192), not shared by calls that may overlap (default: allocated
+    for the call)."""
     made = []
     if out is None:
         out = torch.empty_like(q)
         made.append(out)
     dev = q.device
-    _on_device(dev, out=out, seqlens=seqlens, workspace=workspace)
+    if dev.type != "cuda" or out.device != dev or seqlens.device != dev or \
+            workspace is not None and workspace.device != dev:
+        _on_device(dev, out=out, seqlens=seqlens, workspace=workspace)
     res = {"out": out}
     lse = 0
     if return_lse:
@@ -297,13 +312,15 @@ def decode4(q, cache: KVCache4, block_table, seqlens, *, max_seqlen=None, softma
                                lse=lse)
     if workspace is None:
         need = _native.lib().bsfa_decode4_workspace_size(c, fields(0, 0))
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        made.append(workspace)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            made.append(workspace)
     elif not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous")
     if stream is not None:
         _made_here(stream, dev, *made)
-    _call("bsfa_decode4", dev, stream, c, fields(workspace.data_ptr(), _nbytes(workspace)))
+    _call("bsfa_decode4", dev, stream, c,
+          fields(0, 0) if workspace is None else fields(workspace.data_ptr(), _nbytes(workspace)))
     return res
 
 

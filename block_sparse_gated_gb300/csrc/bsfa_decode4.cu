@@ -841,7 +841,6 @@ Carve carve(const Plan& pl, int d) {
   c.part_ml = up(c.part_o + grid * 2 * rows * d * sizeof(float));
   c.joins = up(c.part_ml + grid * 2 * rows * sizeof(float2));
   c.bytes = up(c.joins + grid * sizeof(int4));
-  if (c.bytes == 0) c.bytes = 256;
   return c;
 }
 
@@ -937,8 +936,8 @@ bsfa_status bsfa_decode4(const bsfa_cache4* cache, const bsfa_decode4_params* p,
     return BSFA_ERR_UNSUPPORTED;
   const Plan pl = plan_of(cache, p);
   const Carve cv = carve(pl, cache->head_dim);
-  if (p->workspace == nullptr || (reinterpret_cast<uintptr_t>(p->workspace) & 255u) ||
-      p->workspace_bytes < cv.bytes)
+  if (pl.split && (p->workspace == nullptr || (reinterpret_cast<uintptr_t>(p->workspace) & 255u) ||
+                   p->workspace_bytes < cv.bytes))
     return BSFA_ERR_WORKSPACE;
 
   DecArgs a{};

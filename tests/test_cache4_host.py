@@ -152,23 +152,26 @@ def test_decode_parameters_that_are_refused(lib):
         p = _decode(**change)
         assert lib.bsfa_decode4(c, ctypes.byref(p), None) == status, change
         assert size(c, ctypes.byref(p)) == 0, change
+    long = _cache(block_table_width=200, block_table_stride=200)
+    c2 = ctypes.byref(long)  # a bound beyond 8192 needs a workspace
+    need = size(c2, ctypes.byref(_decode(max_seqlen=8193)))
+    assert need > 0 and size(c2, ctypes.byref(_decode(max_seqlen=8192))) == 0
     for change, status in ((dict(q=0), INVALID), (dict(seqlens=0), INVALID),
                            (dict(o=(1 << 20) + 8), UNSUPPORTED), (dict(), WORKSPACE),
                            (dict(workspace=128, workspace_bytes=1 << 30), WORKSPACE),
-                           (dict(workspace=1 << 20, workspace_bytes=0), WORKSPACE)):
-        p = _decode(**change)
-        assert lib.bsfa_decode4(c, ctypes.byref(p), None) == status, change
-    p = _decode()
+                           (dict(workspace=1 << 20, workspace_bytes=0), WORKSPACE),
+                           (dict(workspace=1 << 20, workspace_bytes=need - 1), WORKSPACE)):
+        p = _decode(max_seqlen=8193, **change)
+        assert lib.bsfa_decode4(c2, ctypes.byref(p), None) == status, change
+    p = _decode(max_seqlen=8193)
     p.q_stride[1] = 4
-    assert lib.bsfa_decode4(c, ctypes.byref(p), None) == UNSUPPORTED
-    p = _decode()
+    assert lib.bsfa_decode4(c2, ctypes.byref(p), None) == UNSUPPORTED
+    p = _decode(max_seqlen=8193)
     p.q_stride[2] = 3  # the only token's stride says nothing
-    assert lib.bsfa_decode4(c, ctypes.byref(p), None) == WORKSPACE
+    assert lib.bsfa_decode4(c2, ctypes.byref(p), None) == WORKSPACE
     for empty in (dict(batch=0), dict(q_len=0)):
         p = _decode(q=0, o=0, **empty)
         assert lib.bsfa_decode4(c, ctypes.byref(p), None) == OK
-    p = _decode(workspace=1 << 20, workspace_bytes=size(c, ctypes.byref(_decode())) - 1)
-    assert lib.bsfa_decode4(c, ctypes.byref(p), None) == WORKSPACE
 
 
 def _bsfa():
@@ -203,8 +206,14 @@ def test_binding_checks_what_the_library_cannot_see(monkeypatch):
     def descriptor(*a):
         return n.Cache4.from_buffer_copy(m._cache_fields(*a)[0])
 
+    class Cuda:  # stands for the host tensors' device
+        type = "cuda"
+
+        def __ne__(self, other):
+            return False
+
     def rows(*a):
-        return n.Cache4Rows.from_buffer_copy(m._rows_fields(*a)[0])
+        return n.Cache4Rows.from_buffer_copy(m._rows_fields(*a, Cuda())[0])
 
     def decode(*a, **kw):
         return n.Decode4Params.from_buffer_copy(m._decode_fields(*a, **kw)[1](4096, 77))

@@ -232,6 +232,7 @@ def test_graphs_follow_the_lengths_and_streams_do_not_mix(cuda_device, cut):
     q = [_queries(2, 8, 1, 64, HF, s, cuda_device) for s in (1, 2)]
     n32 = [_i32(lens, cuda_device) for _ in range(2)]
     need = cache4.decode4_workspace_bytes(q[0], cache, table, n32[0])
+    assert (need > 0) == cut
     ws = [torch.empty(need, dtype=torch.uint8, device=cuda_device) for _ in range(2)]
     outs = [torch.empty_like(x) for x in q]
     graphs = []
