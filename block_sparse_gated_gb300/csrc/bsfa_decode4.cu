@@ -58,21 +58,32 @@ constexpr int MAX_PARTS = 768;      // parts of a segment, at most: CTAs of a cu
 constexpr int MAX_CLUSTER = 8;      // CTAs that share a segment, at most
 constexpr int CLUSTER_UNITS = 16;   // units of a segment per CTA of a cluster, at most
 
-// Per row-tile width (NT tiles of 8 query rows): CTAs per SM, ring stages, and
-// the most CTAs a launch has (the workspace holds two partial results each).
+// Per row-tile width (NT tiles of 8 query rows): CTAs per SM, ring stages,
+// whether the main loop goes around the ring in one piece (64 ragged sequences
+// to 16K, NT = 1: 121 us by single tiles, 118 unrolled with 5 stages, 115 with 4;
+// five tokens over 16 to 32K, NT = 3: 133 and 141), and the most CTAs a launch
+// has (the workspace holds two partial results each).
 template <int NT>
 struct Shape;
 template <>
 struct Shape<1> {
-  static constexpr int CTAS = 4, STAGES = 5, MAX_GRID = 640;
+  static constexpr int CTAS = 4, STAGES = 4, MAX_GRID = 640;
+  static constexpr bool UNROLL = true;
 };
 template <>
 struct Shape<2> {
-  static constexpr int CTAS = 3, STAGES = 6, MAX_GRID = 480;
+  static constexpr int CTAS = 3, STAGES = 4, MAX_GRID = 480;
+  static constexpr bool UNROLL = true;
+};
+template <>
+struct Shape<3> {
+  static constexpr int CTAS = 2, STAGES = 4, MAX_GRID = 320;
+  static constexpr bool UNROLL = false;
 };
 template <>
 struct Shape<4> {
-  static constexpr int CTAS = 2, STAGES = 8, MAX_GRID = 320;
+  static constexpr int CTAS = 2, STAGES = 4, MAX_GRID = 320;
+  static constexpr bool UNROLL = false;
 };
 
 struct DecArgs {
@@ -213,7 +224,9 @@ __device__ __forceinline__ void store_row4(const DecArgs& a, int b, int kvh, int
         l == 0.f ? -INFINITY : (m - SHIFT + log2f(l)) * 0.6931471805599453f;
 }
 
-template <int D, int NT>
+// DENSE: the tokens of a page lie together in each pool, so that the strides of
+// the copies are constants.
+template <int D, int NT, bool DENSE>
 __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const DecArgs a) {
   constexpr int STAGES = Shape<NT>::STAGES;
   constexpr int KSTEPS = D / 16;  // 16-element steps of K Q^T
@@ -282,9 +295,10 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
     const int cp_tok = lane / CHUNKS, cp_chunk = lane % CHUNKS;
     const bool cp_val = lane >= 16;
     const int32_t* table = a.table + static_cast<long long>(b) * a.table_stride;
-    const uint8_t* k_base = a.kc + kvh * a.kc_sh + (cp_tok * a.kc_st + cp_chunk * 16);
-    const uint8_t* v_base = a.vc + kvh * a.vc_sh + (cp_tok * a.vc_st + cp_chunk * 16);
-    const int z_st = cp_val ? a.vs_st : a.ks_st;
+    const int kc_st = DENSE ? D / 2 : a.kc_st, vc_st = DENSE ? D / 2 : a.vc_st;
+    const int z_st = DENSE ? D / FP4_GROUP : cp_val ? a.vs_st : a.ks_st;
+    const uint8_t* k_base = a.kc + kvh * a.kc_sh + (cp_tok * kc_st + cp_chunk * 16);
+    const uint8_t* v_base = a.vc + kvh * a.vc_sh + (cp_tok * vc_st + cp_chunk * 16);
     const uint32_t z_sp4 = cp_val ? a.vs_sp4 : a.ks_sp4;
     const uint8_t* z_base =
         (cp_val ? a.vs + kvh * a.vs_sh : a.ks + kvh * a.ks_sh) + (lane & 15) * z_st;
@@ -300,8 +314,8 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
       const uint32_t page = ok ? cp_entry : 0;
       const int row = off * TOK;
       cp_ok = ok;
-      k_src = k_base + (static_cast<uint64_t>(page) * a.kc_sp4 << 2) + row * a.kc_st;
-      v_src = v_base + (static_cast<uint64_t>(page) * a.vc_sp4 << 2) + row * a.vc_st;
+      k_src = k_base + (static_cast<uint64_t>(page) * a.kc_sp4 << 2) + row * kc_st;
+      v_src = v_base + (static_cast<uint64_t>(page) * a.vc_sp4 << 2) + row * vc_st;
       z_src = z_base + (static_cast<uint64_t>(page) * z_sp4 << 2) + row * z_st;
       cp_run = min(cp_left, a.tiles_per_page - off);
       cp_left -= cp_run;
@@ -311,16 +325,15 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
     auto copy_tile = [&](uint32_t dst) {
       if (cp_run > 0) {
         const uint32_t at = dst + cp_dst;
-        cp_async16(at, k_src, cp_ok);
-        cp_async16(at + St::CODES, v_src, cp_ok);
-        if constexpr (D == 128) {  // rows 8 .. 15: swizzle(t + 8) = swizzle(t) + 512
-          cp_async16(at + 512, k_src + 8 * a.kc_st, cp_ok);
-          cp_async16(at + St::CODES + 512, v_src + 8 * a.vc_st, cp_ok);
-        }
-        cp_async_small<D / FP4_GROUP>(dst + 2 * St::CODES + lane * (D / FP4_GROUP), z_src,
-                                      cp_ok);
-        k_src += TOK * a.kc_st;
-        v_src += TOK * a.vc_st;
+        if constexpr (D == 128)  // rows 8 .. 15: swizzle(t + 8) = swizzle(t) + 512
+          cp_async_tile<St::CODES, D / FP4_GROUP>(at, dst + 2 * St::CODES + lane * (D / FP4_GROUP),
+                                                  k_src, k_src + 8 * kc_st, v_src,
+                                                  v_src + 8 * vc_st, z_src, cp_ok);
+        else
+          cp_async_tile<St::CODES, D / FP4_GROUP>(at, dst + 2 * St::CODES + lane * (D / FP4_GROUP),
+                                                  k_src, v_src, z_src, cp_ok);
+        k_src += TOK * kc_st;
+        v_src += TOK * vc_st;
         z_src += TOK * z_st;
         if (--cp_run == 0 && cp_left > 0) open_page(0);
       }
@@ -565,10 +578,10 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
 #pragma unroll
         for (int w = 0; w < D / 64; ++w) {
           // f16x2 fragments want {token 4j', token 4j' + 4} of one element.
-          const uint32_t even01 = (v[0][w] & 0x0f0f0f0fu) | ((v[1][w] << 4) & 0xf0f0f0f0u);
-          const uint32_t odd01 = ((v[0][w] >> 4) & 0x0f0f0f0fu) | (v[1][w] & 0xf0f0f0f0u);
-          const uint32_t even23 = (v[2][w] & 0x0f0f0f0fu) | ((v[3][w] << 4) & 0xf0f0f0f0u);
-          const uint32_t odd23 = ((v[2][w] >> 4) & 0x0f0f0f0fu) | (v[3][w] & 0xf0f0f0f0u);
+          const uint32_t even01 = select_low_nibbles(v[0][w], v[1][w] << 4);
+          const uint32_t odd01 = select_low_nibbles(v[0][w] >> 4, v[1][w]);
+          const uint32_t even23 = select_low_nibbles(v[2][w], v[3][w] << 4);
+          const uint32_t odd23 = select_low_nibbles(v[2][w] >> 4, v[3][w]);
           uint32_t a0[4], a1[4], a2[4], a3[4];
           e2m1x8_to_f16(even01, a0);
           e2m1x8_to_f16(odd01, a1);
@@ -602,6 +615,17 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
     // sums between registers at every join of the two).
     const int t_full = max(t_begin, min(t_end, min_lim / TOK));
     int t = t_begin;
+    if constexpr (Shape<NT>::UNROLL) {  // the ring once around, its places constants
+      for (; t + STAGES <= t_full; t += STAGES) {
+#pragma unroll
+        for (int x = 0; x < STAGES; ++x) {
+          cp_async_wait<STAGES - 2>();
+          __syncwarp();
+          copy_tile(my_ring + (x + STAGES - 1) % STAGES * St::BYTES);
+          tile(my_ring + x * St::BYTES, 0, std::false_type{});
+        }
+      }
+    }
     for (; t < t_full; ++t) tile(next_tile(), 0, std::false_type{});
     for (; t < t_end; ++t) tile(next_tile(), t * TOK, std::true_type{});
     cp_async_wait<0>();
@@ -802,7 +826,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) decode4_join_kernel(const DecArg
 }
 
 // Query row tiles of a call: as few tensor-core columns as hold its rows, up
-// to 32 to a CTA.
+// to 32 to a CTA, and equal shares where one CTA does not hold them.
 struct Plan {
   int nt, row_tiles, units, max_grid, cluster;
   long long segments, all_units;
@@ -812,14 +836,16 @@ struct Plan {
 Plan plan_of(const bsfa_cache4* c, const bsfa_decode4_params* p) {
   Plan pl;
   const long long rows = static_cast<long long>(p->num_heads_q / c->num_heads_kv) * p->q_len;
-  pl.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-  pl.row_tiles = static_cast<int>((rows + 8 * pl.nt - 1) / (8 * pl.nt));
+  const long long eights = rows > 0 ? (rows + 7) / 8 : 1;
+  pl.row_tiles = static_cast<int>((eights + 3) / 4);
+  pl.nt = static_cast<int>((eights + pl.row_tiles - 1) / pl.row_tiles);
   pl.units = (p->max_seqlen + UNIT - 1) / UNIT;
   if (pl.units < 1) pl.units = 1;
   pl.segments = static_cast<long long>(p->batch) * c->num_heads_kv * pl.row_tiles;
   pl.all_units = pl.segments * (pl.units + SEGMENT_UNITS);
-  pl.max_grid = pl.nt == 1 ? Shape<1>::MAX_GRID : pl.nt == 2 ? Shape<2>::MAX_GRID
-                                                             : Shape<4>::MAX_GRID;
+  constexpr int grids[4] = {Shape<1>::MAX_GRID, Shape<2>::MAX_GRID, Shape<3>::MAX_GRID,
+                            Shape<4>::MAX_GRID};
+  pl.max_grid = grids[pl.nt - 1];
   pl.cluster = 1;
   while (pl.cluster < MAX_CLUSTER && pl.units >= 2 * pl.cluster &&
          (pl.segments * pl.cluster < pl.max_grid || pl.units > CLUSTER_UNITS * pl.cluster))
@@ -862,7 +888,7 @@ bsfa_status validate_sizes(const bsfa_cache4* c, const bsfa_decode4_params* p) {
   return BSFA_OK;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool DENSE>
 bsfa_status launch(const DecArgs& a, const Plan& pl, int sms, int dev, cudaStream_t stream) {
   constexpr int smem = smem_bytes<D, NT>();
   static_assert(Shape<NT>::MAX_GRID <= MAX_PARTS, "the join's weights");
@@ -870,7 +896,7 @@ bsfa_status launch(const DecArgs& a, const Plan& pl, int sms, int dev, cudaStrea
   static std::atomic<uint64_t> ready{0};
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    if (cudaFuncSetAttribute(decode4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(decode4_kernel<D, NT, DENSE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem) != cudaSuccess)
       return BSFA_ERR_CUDA;
     ready.fetch_or(bit, std::memory_order_relaxed);
@@ -887,14 +913,14 @@ bsfa_status launch(const DecArgs& a, const Plan& pl, int sms, int dev, cudaStrea
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode4_kernel<D, NT>, a) == cudaSuccess ? BSFA_OK
+    return cudaLaunchKernelEx(&cfg, decode4_kernel<D, NT, DENSE>, a) == cudaSuccess ? BSFA_OK
                                                                              : BSFA_ERR_CUDA;
   }
   const long long full = static_cast<long long>(sms) * Shape<NT>::CTAS;
   long long grid = full < pl.max_grid ? full : pl.max_grid;
   const long long most = (pl.all_units + MIN_UNITS - 1) / MIN_UNITS;
   if (most < grid) grid = most;
-  decode4_kernel<D, NT><<<static_cast<unsigned>(grid), THREADS, smem, stream>>>(a);
+  decode4_kernel<D, NT, DENSE><<<static_cast<unsigned>(grid), THREADS, smem, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return BSFA_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), a.rows < 8 * NT ? a.rows : 8 * NT);
@@ -993,13 +1019,17 @@ bsfa_status bsfa_decode4(const bsfa_cache4* cache, const bsfa_decode4_params* p,
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
     return BSFA_ERR_CUDA;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  if (cache->head_dim == 128)
-    return pl.nt == 1   ? launch<128, 1>(a, pl, sms, dev, stream)
-           : pl.nt == 2 ? launch<128, 2>(a, pl, sms, dev, stream)
-                        : launch<128, 4>(a, pl, sms, dev, stream);
-  return pl.nt == 1   ? launch<64, 1>(a, pl, sms, dev, stream)
-         : pl.nt == 2 ? launch<64, 2>(a, pl, sms, dev, stream)
-                      : launch<64, 4>(a, pl, sms, dev, stream);
+  const int row = cache->head_dim / 2, z = cache->head_dim / FP4_GROUP;
+  const bool dense = cache->k_stride[2] == row && cache->v_stride[2] == row &&
+                     cache->k_scale_stride[2] == z && cache->v_scale_stride[2] == z;
+  using Launch = bsfa_status (*)(const DecArgs&, const Plan&, int, int, cudaStream_t);
+  static const Launch launches[2][2][4] = {  // [d = 128][dense][tiles of 8 query rows - 1]
+      {{launch<64, 1, false>, launch<64, 2, false>, launch<64, 3, false>, launch<64, 4, false>},
+       {launch<64, 1, true>, launch<64, 2, true>, launch<64, 3, true>, launch<64, 4, true>}},
+      {{launch<128, 1, false>, launch<128, 2, false>, launch<128, 3, false>,
+        launch<128, 4, false>},
+       {launch<128, 1, true>, launch<128, 2, true>, launch<128, 3, true>, launch<128, 4, true>}}};
+  return launches[cache->head_dim == 128][dense][pl.nt - 1](a, pl, sms, dev, stream);
 }
 
 }  // extern "C"

@@ -56,6 +56,13 @@ __device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
   return r & 0xffu;
 }
 
+// The low nibble of each byte from `low`, the high one from `high`.
+__device__ __forceinline__ uint32_t select_low_nibbles(uint32_t low, uint32_t high) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xe4;" : "=r"(r) : "r"(low), "r"(high), "r"(0x0f0f0f0fu));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -145,23 +152,35 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   return r;
 }
 
-// Asynchronous copies global -> shared; `ok` false reads nothing and writes
-// zeros (the predicate form: a byte count in a register costs about eight
-// instructions more per copy).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+// One lane's share of a tile, global -> shared, asynchronously: 16 bytes of keys
+// (k1: also of the tile's second half, 512 bytes on), of values `V` bytes on, and
+// `Z` bytes of scales.  `ok` false reads nothing and writes zeros.  (One block with
+// one predicate: a byte count in a register costs about eight instructions more
+// per copy, a predicate of its own one.)
+template <int V, int Z>
+__device__ __forceinline__ void cp_async_tile(uint32_t dst, uint32_t dst_z, const void* k0,
+                                              const void* k1, const void* v0, const void* v1,
+                                              const void* z, bool ok) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %2, 0;\n\t"
-      "cp.async.cg.shared.global [%0], [%1], 16, p;\n\t}" ::"r"(dst),
-      "l"(src), "r"(static_cast<uint32_t>(ok))
+      "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %7, 0;\n\t"
+      "cp.async.cg.shared.global [%0], [%2], 16, p;\n\t"
+      "cp.async.cg.shared.global [%0+512], [%3], 16, p;\n\t"
+      "cp.async.cg.shared.global [%0+%8], [%4], 16, p;\n\t"
+      "cp.async.cg.shared.global [%0+%9], [%5], 16, p;\n\t"
+      "cp.async.ca.shared.global [%1], [%6], %10, p;\n\t}" ::"r"(dst),
+      "r"(dst_z), "l"(k0), "l"(k1), "l"(v0), "l"(v1), "l"(z), "r"(static_cast<uint32_t>(ok)),
+      "n"(V), "n"(V + 512), "n"(Z)
       : "memory");
 }
-template <int BYTES>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool ok) {
-  static_assert(BYTES == 4 || BYTES == 8, "copies of 4 or 8 bytes");
+template <int V, int Z>
+__device__ __forceinline__ void cp_async_tile(uint32_t dst, uint32_t dst_z, const void* k0,
+                                              const void* v0, const void* z, bool ok) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %3, 0;\n\t"
-      "cp.async.ca.shared.global [%0], [%1], %2, p;\n\t}" ::"r"(dst),
-      "l"(src), "n"(BYTES), "r"(static_cast<uint32_t>(ok))
+      "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %5, 0;\n\t"
+      "cp.async.cg.shared.global [%0], [%2], 16, p;\n\t"
+      "cp.async.cg.shared.global [%0+%6], [%3], 16, p;\n\t"
+      "cp.async.ca.shared.global [%1], [%4], %7, p;\n\t}" ::"r"(dst),
+      "r"(dst_z), "l"(k0), "l"(v0), "l"(z), "r"(static_cast<uint32_t>(ok)), "n"(V), "n"(Z)
       : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
