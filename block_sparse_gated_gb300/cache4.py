@@ -288,9 +288,9 @@ def decode4(q, cache: KVCache4, block_table, seqlens, *, max_seqlen=None, softma
     ``max_seqlen`` bounds the lengths (default: what the block table can hold;
     longer entries of seqlens are cut to it); the call reads lengths on the
     device only, so a captured graph stays right as they grow within it.
-    ``workspace``: at least ``decode4_workspace_bytes`` of device memory (0 for
-    bounds up to 8192), not shared by calls that may overlap (default: allocated
-    for the call)."""
+    ``workspace``: at least ``decode4_workspace_bytes`` of device memory (0 where
+    the lengths' bound and the batch are small), not shared by calls that may
+    overlap (default: allocated for the call)."""
     made = []
     if out is None:
         out = torch.empty_like(q)

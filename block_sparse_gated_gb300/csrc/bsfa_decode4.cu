@@ -99,13 +99,13 @@ struct DecArgs {
   long long q_s[3], o_s[3];
   const int32_t* seqlens;
   int batch, heads_kv, group, q_len, rows, row_tiles, max_len;
-  int causal, f16, split, cluster;
+  int causal, f16, split, cluster, join_by_segment;
   float sigma_log2;
   float* lse;
   long long lse_pitch;
   float* part_o;    // [grid][2][8 * NT][d]
   float2* part_ml;  // [grid][2][8 * NT]
-  int4* joins;      // [grid]: {sequence, kvh * row_tiles + row tile, last CTA, 0}, or x < 0
+  int4* joins;      // [jobs]: {sequence, kvh * row_tiles + row tile, first, last CTA}, or x < 0
 };
 
 // The sequence length that the call sees.
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
 
   Piece piece;
   if (a.split) {
-    if (tid == 0) a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (tid == 0 && !a.join_by_segment) a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
     piece = cut(a, sh_cut);
   } else {  // one segment per cluster; u walks over it once
     const int seg = static_cast<int>(blockIdx.x) / a.cluster, per_b = a.heads_kv * a.row_tiles;
@@ -744,8 +744,14 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
         if (d0 == 0) a.part_ml[static_cast<long long>(part) * ROWS + r] = make_float2(m, l);
       }
     }
-    if (!whole && u0 == 0 && tid == 0)
-      a.joins[blockIdx.x] = make_int4(b, seg, (u + n_units - 1) / piece.per_cta, 0);
+    if (u0 == 0 && tid == 0) {
+      const int4 job =
+          make_int4(whole ? -1 : b, seg, blockIdx.x, (u + n_units - 1) / piece.per_cta);
+      if (a.join_by_segment)
+        a.joins[b * a.heads_kv * a.row_tiles + seg] = job;
+      else if (!whole)
+        a.joins[blockIdx.x] = job;
+    }
     __syncthreads();  // the ring and sh_ml are free again
 
     u += u1 - u0;
@@ -757,9 +763,10 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
 }
 
 // Joins the parts of the segments that a cut crossed: block (x, r) takes row r
-// of the segment that CTA x began and did not finish, if there is one.  The
-// parts lie in the CTAs x (its second slot) .. last (their first slots).  The
-// references come first, all at once, so that the sums' loads wait for nothing.
+// of job x, which is segment x, or where there are more segments than CTAs the
+// one that CTA x began and did not finish -- if that was cut.  The parts lie in
+// the CTAs first (its second slot) .. last (their first slots).  The references
+// come first, all at once, so that the sums' loads wait for nothing.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(JOIN_THREADS) decode4_join_kernel(const DecArgs a) {
   constexpr int LANES = D / 4;                 // threads that cover a row, four elements each
@@ -773,7 +780,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) decode4_join_kernel(const DecArg
   const int b = job.x, kvh = job.y / a.row_tiles;
   const int r = blockIdx.y, row = (job.y - kvh * a.row_tiles) * ROWS + r;
   if (row >= a.rows) return;
-  const int first = blockIdx.x, count = job.z - first + 1;  // count <= gridDim.x <= MAX_PARTS
+  const int first = job.z, count = job.w - first + 1;  // at most the CTAs, so MAX_PARTS
   const int tid = threadIdx.x;
   auto slot = [&](int p) { return 2LL * (first + p) + (p == 0 ? 1 : 0); };
 
@@ -846,9 +853,10 @@ Plan plan_of(const bsfa_cache4* c, const bsfa_decode4_params* p) {
   constexpr int grids[4] = {Shape<1>::MAX_GRID, Shape<2>::MAX_GRID, Shape<3>::MAX_GRID,
                             Shape<4>::MAX_GRID};
   pl.max_grid = grids[pl.nt - 1];
+  // As many CTAs to a segment as keep them all resident at once.
   pl.cluster = 1;
   while (pl.cluster < MAX_CLUSTER && pl.units >= 2 * pl.cluster &&
-         (pl.segments * pl.cluster < pl.max_grid || pl.units > CLUSTER_UNITS * pl.cluster))
+         2 * pl.segments * pl.cluster <= pl.max_grid)
     pl.cluster *= 2;
   pl.split = pl.units > CLUSTER_UNITS * pl.cluster;
   if (pl.split) pl.cluster = 1;
@@ -889,7 +897,7 @@ bsfa_status validate_sizes(const bsfa_cache4* c, const bsfa_decode4_params* p) {
 }
 
 template <int D, int NT, bool DENSE>
-bsfa_status launch(const DecArgs& a, const Plan& pl, int sms, int dev, cudaStream_t stream) {
+bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaStream_t stream) {
   constexpr int smem = smem_bytes<D, NT>();
   static_assert(Shape<NT>::MAX_GRID <= MAX_PARTS, "the join's weights");
   // The shared-memory size of a kernel is set once per device.
@@ -913,17 +921,20 @@ bsfa_status launch(const DecArgs& a, const Plan& pl, int sms, int dev, cudaStrea
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode4_kernel<D, NT, DENSE>, a) == cudaSuccess ? BSFA_OK
+    return cudaLaunchKernelEx(&cfg, decode4_kernel<D, NT, DENSE>, args) == cudaSuccess ? BSFA_OK
                                                                              : BSFA_ERR_CUDA;
   }
   const long long full = static_cast<long long>(sms) * Shape<NT>::CTAS;
   long long grid = full < pl.max_grid ? full : pl.max_grid;
   const long long most = (pl.all_units + MIN_UNITS - 1) / MIN_UNITS;
   if (most < grid) grid = most;
+  DecArgs a = args;
+  a.join_by_segment = pl.segments <= grid;
   decode4_kernel<D, NT, DENSE><<<static_cast<unsigned>(grid), THREADS, smem, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return BSFA_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), a.rows < 8 * NT ? a.rows : 8 * NT);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.join_by_segment ? pl.segments : grid),
+                     a.rows < 8 * NT ? a.rows : 8 * NT);
   cfg.blockDim = dim3(JOIN_THREADS);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};

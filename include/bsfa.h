@@ -402,8 +402,8 @@ typedef struct {
 } bsfa_decode4_params;
 
 /* Bytes of workspace bsfa_decode4 needs (reads shape fields only).  0 for a
- * call that needs none, as those with a max_seqlen of at most 8192 do -- its
- * workspace may be NULL --, and for invalid parameters. */
+ * call that needs none (short or few sequences by max_seqlen and batch): its
+ * workspace may be NULL.  0 for invalid parameters, too. */
 size_t bsfa_decode4_workspace_size(const bsfa_cache4* cache, const bsfa_decode4_params* p);
 
 /* Limits (BSFA_ERR_UNSUPPORTED beyond them): 4096 sequences, and
