@@ -15,6 +15,8 @@ from . import _native
 from .api import _DTYPES, _check, _dtype_code, _nbytes, _on_device, _strides_bhtd
 
 GROUP = 16  # elements that share a scale
+_U8, _E4M3, _I32 = torch.uint8, torch.float8_e4m3fn, torch.int32
+_BAD_TABLE = "block_table must be an int32 [batch, pages_per_sequence] tensor"
 
 
 class KVCache4(NamedTuple):
@@ -77,41 +79,51 @@ def _cache_fields(cache: KVCache4, block_table: torch.Tensor, device, batch: int
     and the tokens that a row of the block table can hold."""
     k, v, ks, vs, ke, ve, layout = cache
     heads, d = _heads_and_dim(cache)
+    index = device.index
     shape = k.shape
-    n, _, _, row = shape
-    scales = (n, shape[1], shape[2], row // 8)
+    n, x, y, row = shape
+    scales = (n, x, y, row // 8)
     a, b, e, f = k.stride(), v.stride(), ks.stride(), vs.stride()
-    u8, f8 = torch.uint8, torch.float8_e4m3fn
-    if not (k.dtype is u8 and v.dtype is u8 and ks.dtype is f8 and vs.dtype is f8 and
-            v.shape == shape and ks.shape == scales and vs.shape == scales and
-            len(b) == len(e) == len(f) == 4 and a[3] == b[3] == e[3] == f[3] == 1 and
-            k.device == device and v.device == device and ks.device == device and
-            vs.device == device):
+    if not (k.dtype is v.dtype is _U8 and ks.dtype is vs.dtype is _E4M3 and v.shape == shape and
+            ks.shape == scales and vs.shape == scales and a[3] == b[3] == e[3] == f[3] == 1 and
+            k.get_device() == v.get_device() == ks.get_device() == vs.get_device() == index):
         _bad_pool(cache, device)
-    for x in (ke, ve):
-        if x is not None and not (x.dtype is torch.int32 and x.shape == (heads,) and
-                                  x.is_contiguous() and x.device == device):
-            _bad_pool(cache, device)
-    if block_table.device != device:
+    ke_ptr = ve_ptr = 0
+    if ke is not None:
+        ke_ptr = _exponents(ke, heads, cache, device)
+    if ve is not None:
+        ve_ptr = _exponents(ve, heads, cache, device)
+    if block_table.get_device() != index:
         _on_device(device, block_table=block_table)
-    if block_table.dtype is not torch.int32 or block_table.dim() != 2 or \
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be an int32 [batch, pages_per_sequence] tensor")
+    if block_table.dtype is not _I32 or block_table.dim() != 2:
+        raise ValueError(_BAD_TABLE)
     rows, width = block_table.shape
+    pitch, unit = block_table.stride()
+    if unit != 1 and width > 1:
+        raise ValueError(_BAD_TABLE)
     if rows < batch:
         raise ValueError("block_table has fewer rows than sequences")
-    i, j = (1, 2) if layout == "phtd" else (2, 1)
-    page = shape[j]
+    if layout == "phtd":
+        return _native.CACHE4.pack(
+            k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), ke_ptr, ve_ptr,
+            a[0], a[1], a[2], b[0], b[1], b[2], e[0], e[1], e[2], f[0], f[1], f[2],
+            n, y, heads, d, block_table.data_ptr(), pitch if rows > 1 else width,
+            width), width * y
     return _native.CACHE4.pack(
-        k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(),
-        0 if ke is None else ke.data_ptr(), 0 if ve is None else ve.data_ptr(),
-        a[0], a[i], a[j], b[0], b[i], b[j], e[0], e[i], e[j], f[0], f[i], f[j],
-        n, page, heads, d, block_table.data_ptr(),
-        block_table.stride(0) if rows > 1 else width, width), width * page
+        k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), ke_ptr, ve_ptr,
+        a[0], a[2], a[1], b[0], b[2], b[1], e[0], e[2], e[1], f[0], f[2], f[1],
+        n, x, heads, d, block_table.data_ptr(), pitch if rows > 1 else width, width), width * x
+
+
+def _exponents(t, heads: int, cache, device):
+    if not (t.dtype is _I32 and t.shape == (heads,) and t.is_contiguous() and
+            t.get_device() == device.index):
+        _bad_pool(cache, device)
+    return t.data_ptr()
 
 
 def _int32_vector(t, n: int, what: str):
-    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
+    if t.dtype is not _I32 or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 [{n}] tensor")
     return t.data_ptr()
 
@@ -124,9 +136,12 @@ def _rows_fields(k, v, layout, cu_seqlens, start, heads: int, d: int, device):
     shape = k.shape
     if v.shape != shape:
         raise ValueError("K and V shapes disagree")
+    code = _DTYPES.get(k.dtype)
+    if code is None:
+        raise TypeError("expected a bfloat16 or float16 tensor")
     if v.dtype is not k.dtype:
         raise TypeError("K and V must share one element type")
-    if device.type != "cuda" or k.device != device or v.device != device:
+    if device.type != "cuda" or not k.get_device() == v.get_device() == device.index:
         _on_device(device, k=k, v=v)
     ks, hk, n = _strides_bhtd(k, layout, varlen)
     vs = ks if v.stride() == k.stride() else _strides_bhtd(v, layout, varlen)[0]
@@ -134,20 +149,20 @@ def _rows_fields(k, v, layout, cu_seqlens, start, heads: int, d: int, device):
         raise ValueError("K and V must have the cache's heads and head dimension")
     cu = first = 0
     if varlen:
-        if cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or \
+        if cu_seqlens.dtype is not _I32 or cu_seqlens.dim() != 1 or \
                 not cu_seqlens.is_contiguous() or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be a contiguous int32 [batch + 1] tensor")
-        if cu_seqlens.device != device:
+        if cu_seqlens.get_device() != device.index:
             _on_device(device, cu_seqlens=cu_seqlens)
         batch, cu = cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
     else:
         batch = 1 if len(shape) == 3 else shape[0]
     if start is not None:
         first = _int32_vector(start, batch, "start")
-        if start.device != device:
+        if start.get_device() != device.index:
             _on_device(device, start=start)
     return _native.CACHE4_ROWS.pack(k.data_ptr(), v.data_ptr(), *ks, *vs, batch, n, cu, first,
-                                    _dtype_code(k)), batch
+                                    code), batch
 
 
 def _heads_and_dim(cache: KVCache4):
@@ -162,19 +177,18 @@ def _heads_and_dim(cache: KVCache4):
     raise ValueError(layout)
 
 
-def _call(name, device, stream, *args):
+def _call(fn, device, stream, *args):
     """One library call on ``stream`` (default: the device's current one), with
     the tensors' device current."""
-    fn = getattr(_native.lib(), name)
-    raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else \
-        stream.cuda_stream
-    if torch._C._cuda_getDevice() == device.index:
+    index = device.index
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
         status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
             status = fn(*args, raw)
     if status:
-        _check(status, name)
+        _check(status, fn.__name__)
 
 
 def _made_here(stream, device, *tensors):
@@ -202,7 +216,7 @@ def cache4_write(cache: KVCache4, k, v, block_table, *, start=None, cu_seqlens=N
     dev = k.device
     r, batch = _rows_fields(k, v, layout, cu_seqlens, start, *_heads_and_dim(cache), dev)
     c, _ = _cache_fields(cache, block_table, dev, batch)
-    _call("bsfa_cache4_write", dev, stream, c, r)
+    _call(_native.lib().bsfa_cache4_write, dev, stream, c, r)
 
 
 def cache4_read(cache: KVCache4, block_table, *, seqlen=None, total=None, start=None,
@@ -243,26 +257,26 @@ def cache4_read(cache: KVCache4, block_table, *, seqlen=None, total=None, start=
         k, v = out
     r, batch = _rows_fields(k, v, layout, cu_seqlens, start, heads, d, dev)
     c, _ = _cache_fields(cache, block_table, dev, batch)
-    _call("bsfa_cache4_read", dev, stream, c, r)
+    _call(_native.lib().bsfa_cache4_read, dev, stream, c, r)
     return k, v
 
 
-def _decode_fields(q, cache, block_table, seqlens, out, *, layout, max_seqlen, softmax_scale,
+def _decode_fields(q, cache, block_table, seqlens, out, device, *, layout, max_seqlen, softmax_scale,
                    causal, lse=0):
     """The packed bsfa_cache4 of a decode call, and a function of a workspace's
     address and size that gives its packed bsfa_decode4_params."""
     if layout is None:
         layout = "bhld"
-    if q.shape != out.shape or q.dtype != out.dtype:
+    shape = q.shape
+    if out.shape != shape or q.dtype is not out.dtype:
         raise ValueError("q and out must have one shape and type")
     qs, hq, n = _strides_bhtd(q, layout, False)
-    os_ = qs if out is q else _strides_bhtd(out, layout, False)[0]
+    os_ = qs if out.stride() == q.stride() else _strides_bhtd(out, layout, False)[0]
     heads, d = _heads_and_dim(cache)
-    shape = q.shape
     if shape[-1] != d or heads == 0 or hq % heads:
         raise ValueError("q must have the cache's head dimension and a multiple of its heads")
     batch = 1 if len(shape) == 3 else shape[0]
-    c, most = _cache_fields(cache, block_table, q.device, batch)
+    c, most = _cache_fields(cache, block_table, device, batch)
     if max_seqlen is None:
         max_seqlen = most
     elif max_seqlen > most:
@@ -296,7 +310,7 @@ def decode4(q, cache: KVCache4, block_table, seqlens, *, max_seqlen=None, softma
         out = torch.empty_like(q)
         made.append(out)
     dev = q.device
-    if dev.type != "cuda" or out.device != dev or seqlens.device != dev or \
+    if dev.type != "cuda" or not out.get_device() == seqlens.get_device() == dev.index or \
             workspace is not None and workspace.device != dev:
         _on_device(dev, out=out, seqlens=seqlens, workspace=workspace)
     res = {"out": out}
@@ -307,7 +321,7 @@ def decode4(q, cache: KVCache4, block_table, seqlens, *, max_seqlen=None, softma
         res["lse"] = torch.empty((hq, rows), dtype=torch.float32, device=dev)
         made.append(res["lse"])
         lse = res["lse"].data_ptr()
-    c, fields = _decode_fields(q, cache, block_table, seqlens, out, layout=layout,
+    c, fields = _decode_fields(q, cache, block_table, seqlens, out, dev, layout=layout,
                                max_seqlen=max_seqlen, softmax_scale=softmax_scale, causal=causal,
                                lse=lse)
     if workspace is None:
@@ -319,7 +333,7 @@ def decode4(q, cache: KVCache4, block_table, seqlens, *, max_seqlen=None, softma
         raise ValueError("the workspace must be contiguous")
     if stream is not None:
         _made_here(stream, dev, *made)
-    _call("bsfa_decode4", dev, stream, c,
+    _call(_native.lib().bsfa_decode4, dev, stream, c,
           fields(0, 0) if workspace is None else fields(workspace.data_ptr(), _nbytes(workspace)))
     return res
 
@@ -327,6 +341,6 @@ def decode4(q, cache: KVCache4, block_table, seqlens, *, max_seqlen=None, softma
 def decode4_workspace_bytes(q, cache: KVCache4, block_table, seqlens, *, max_seqlen=None,
                             layout=None) -> int:
     """Workspace bytes that decode4 needs for this call's shapes."""
-    c, fields = _decode_fields(q, cache, block_table, seqlens, q, layout=layout,
+    c, fields = _decode_fields(q, cache, block_table, seqlens, q, q.device, layout=layout,
                                max_seqlen=max_seqlen, softmax_scale=None, causal=True)
     return int(_native.lib().bsfa_decode4_workspace_size(c, fields(0, 0)))

@@ -200,23 +200,21 @@ def test_binding_checks_what_the_library_cannot_see(monkeypatch):
     monkeypatch.setattr(m, "_on_device", lambda *a, **k: None)
     cache = b.cache4_empty(4, 2, 32, 128, device="cpu")
     table = torch.zeros(3, 2, dtype=torch.int32)
-    dev = torch.device("cpu")
     n = _native()
 
     def descriptor(*a):
         return n.Cache4.from_buffer_copy(m._cache_fields(*a)[0])
 
     class Cuda:  # stands for the host tensors' device
-        type = "cuda"
+        type, index = "cuda", -1  # get_device() of a host tensor
 
-        def __ne__(self, other):
-            return False
+    dev = Cuda()
 
     def rows(*a):
         return n.Cache4Rows.from_buffer_copy(m._rows_fields(*a, Cuda())[0])
 
     def decode(*a, **kw):
-        return n.Decode4Params.from_buffer_copy(m._decode_fields(*a, **kw)[1](4096, 77))
+        return n.Decode4Params.from_buffer_copy(m._decode_fields(*a, dev, **kw)[1](4096, 77))
 
     c = descriptor(cache, table, dev, 3)
     assert (c.num_pages, c.num_heads_kv, c.page_size, c.head_dim) == (4, 2, 32, 128)
