@@ -54,6 +54,7 @@ constexpr float SHIFT = 10.f;       // log2 of the factor that p carries: p < 2^
 constexpr int MIN_UNITS = 4;        // shortest piece of the line worth a CTA
 constexpr int SEGMENT_UNITS = 5;    // a segment's fixed cost, in units
 constexpr int JOIN_THREADS = 256;   // of the kernel that joins parts
+constexpr int JOIN_ROWS_PARTS = 8;  // a warp to a row below, a block above
 constexpr int MAX_PARTS = 768;      // parts of a segment, at most: CTAs of a cut call
 constexpr int MAX_CLUSTER = 8;      // CTAs that share a segment, at most
 constexpr int CLUSTER_UNITS = 16;   // units of a segment per CTA of a cluster, at most
@@ -147,11 +148,17 @@ __device__ __forceinline__ int merge_pos(int d) {
 template <int D>
 constexpr int MERGE_ROW = D + 12;
 
+// Dynamic shared memory: the rings, whose place the warps' sums take later, and
+// behind them what the CTAs of a cluster send each other.
 template <int D, int NT>
-constexpr int smem_bytes() {
+constexpr int ring_bytes() {
   constexpr int ring = WARPS * Shape<NT>::STAGES * Stage<D>::BYTES;
-  constexpr int merge = (WARPS * MERGE_ROW<D> + D) * 8 * NT * 4;
+  constexpr int merge = WARPS * MERGE_ROW<D> * 8 * NT * 4;
   return ring > merge ? ring : merge;
+}
+template <int D, int NT>
+constexpr int smem_bytes(bool cluster) {
+  return ring_bytes<D, NT>() + (cluster ? 8 * NT * D * 4 : 0);
 }
 
 // Where a CTA's piece of the line begins.
@@ -238,11 +245,12 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
   __shared__ uint2 sh_q[NT * KSTEPS * 32];
   __shared__ float sh_sc[ROWS];
   __shared__ float2 sh_ml[WARPS][ROWS];
-  __shared__ float2 sh_cluster[ROWS];
+  __shared__ float2 sh_cluster[MAX_CLUSTER][ROWS];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
 
+  if (a.cluster > 1) cluster_arrive();
   Piece piece;
   if (a.split) {
     if (tid == 0 && !a.join_by_segment) a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -661,9 +669,14 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
       }
     __syncthreads();
     if (a.cluster > 1) {
-      // The CTA's sums to its own shared memory, where the cluster reads them:
-      // each CTA joins an equal part of the outputs, over the CTAs in order.
-      float* sums = merge + WARPS * ROWS * MERGE_ROW<D>;
+      // Output x of the segment (four elements) is joined by CTA x % cluster: each
+      // CTA stores its sums, and the references, straight into the joining CTAs'
+      // shared memory, and after one barrier every CTA adds what it got, over the
+      // CTAs in order.  (Sums left in place and read remotely need a second
+      // barrier and wait for the loads: 1 x 4097 tokens 9.6 us, pushed @@ us.)
+      const int items = ROWS * (D / 4) / a.cluster;  // the cluster is a power of two
+      const uint32_t rank = cluster_rank(), got = smem_u32(ring) + ring_bytes<D, NT>();
+      cluster_wait();  // the one of the kernel's beginning: every CTA runs
       for (int x = tid; x < n_rows * (D / 4); x += THREADS) {
         const int r = x / (D / 4), d0 = (x % (D / 4)) * 4;
         const float* src = merge + r * MERGE_ROW<D> + merge_pos<D>(d0);
@@ -673,51 +686,39 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
           src += ROWS * MERGE_ROW<D>;
           y.x += src[0], y.y += src[1], y.z += src[2], y.w += src[3];
         }
-        *reinterpret_cast<float4*>(sums + r * D + d0) = y;
-        if (d0 == 0) {
-          float m = sh_ml[0][r].x, l = 0.f;
-#pragma unroll
-          for (int w = 1; w < WARPS; ++w) m = fmaxf(m, sh_ml[w][r].x);
-#pragma unroll
-          for (int w = 0; w < WARPS; ++w) {
-            const float2 ml = sh_ml[w][r];
-            l += m == -INFINITY ? ml.y : ml.y * ex2_approx(ml.x - m);
-          }
-          sh_cluster[r] = make_float2(m, l);
-        }
+        cluster_st4(got + (rank * items + x / a.cluster) * 16, x % a.cluster, y);
       }
-      cluster_sync();
-      for (int x = tid * a.cluster + cluster_rank(); x < n_rows * (D / 4);
-           x += THREADS * a.cluster) {
-        const int r = x / (D / 4), d0 = (x % (D / 4)) * 4;
-        const uint32_t at = smem_u32(sums + r * D + d0), at_ml = smem_u32(sh_cluster + r);
-        float2 ml[MAX_CLUSTER];
-        float4 part[MAX_CLUSTER];
+      for (int x = tid; x < n_rows * a.cluster; x += THREADS) {
+        const int r = x / a.cluster;
+        float m = sh_ml[0][r].x, l = 0.f;
 #pragma unroll
-        for (int k = 0; k < MAX_CLUSTER; ++k) {
-          if (k < a.cluster) {
-            ml[k] = cluster_ld2(at_ml, k);
-            part[k] = cluster_ld4(at, k);
-          }
+        for (int w = 1; w < WARPS; ++w) m = fmaxf(m, sh_ml[w][r].x);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+          const float2 ml = sh_ml[w][r];
+          l += m == -INFINITY ? ml.y : ml.y * ex2_approx(ml.x - m);
         }
-        float m = ml[0].x;
-#pragma unroll
-        for (int k = 1; k < MAX_CLUSTER; ++k)
-          if (k < a.cluster) m = fmaxf(m, ml[k].x);
+        cluster_st2(smem_u32(&sh_cluster[rank][r]), x % a.cluster, make_float2(m, l));
+      }
+      cluster_arrive();
+      cluster_wait();
+      const float4* parts =
+          reinterpret_cast<const float4*>(ring + ring_bytes<D, NT>());
+      for (int k = tid; k * a.cluster + rank < n_rows * (D / 4); k += THREADS) {
+        const int x = k * a.cluster + rank, r = x / (D / 4), d0 = (x % (D / 4)) * 4;
+        float m = sh_cluster[0][r].x;
+        for (int c1 = 1; c1 < a.cluster; ++c1) m = fmaxf(m, sh_cluster[c1][r].x);
         float l = 0.f;
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < MAX_CLUSTER; ++k) {
-          if (k < a.cluster) {
-            const float f = m == -INFINITY ? 1.f : ex2_approx(ml[k].x - m);
-            l += ml[k].y * f;
-            y.x += part[k].x * f, y.y += part[k].y * f;
-            y.z += part[k].z * f, y.w += part[k].w * f;
-          }
+        for (int c1 = 0; c1 < a.cluster; ++c1) {
+          const float2 ml = sh_cluster[c1][r];
+          const float4 p = parts[c1 * items + k];
+          const float f = m == -INFINITY ? 1.f : ex2_approx(ml.x - m);
+          l += ml.y * f;
+          y.x += p.x * f, y.y += p.y * f, y.z += p.z * f, y.w += p.w * f;
         }
         store_row4(a, b, kvh, r0 + r, d0, m, l, y);
       }
-      cluster_sync();  // no CTA leaves while another reads its sums
       return;
     }
     const bool whole = u0 == 0 && u1 == n_units;
@@ -832,6 +833,64 @@ __global__ void __launch_bounds__(JOIN_THREADS) decode4_join_kernel(const DecArg
   store_row4(a, b, kvh, row, 4 * lane, m, l, y);
 }
 
+// The same where a segment has few parts: a warp takes a row of job x by itself,
+// 32 parts' references at a time (five tokens over 16 sequences to 32K, about
+// four parts to each of 2560 rows: 125.5 us, and 128.8 with a block to a row; 1 x
+// 128K, 76 parts: 46.1 and 36.4).
+template <int D, int ROWS>
+__global__ void __launch_bounds__(JOIN_THREADS) decode4_join_rows_kernel(const DecArgs a) {
+  constexpr int E = D / 32;  // elements of a lane
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 job = a.joins[blockIdx.x];
+  if (job.x < 0) return;
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.y * (JOIN_THREADS / 32) + (threadIdx.x >> 5);
+  const int b = job.x, kvh = job.y / a.row_tiles;
+  const int row = (job.y - kvh * a.row_tiles) * ROWS + r;
+  if (r >= ROWS || row >= a.rows) return;
+  const int first = job.z, count = job.w - first + 1;
+  auto slot = [&](int p) { return 2LL * (first + p) + (p == 0 ? 1 : 0); };
+  float m = -INFINITY, l = 0.f, y[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) y[e] = 0.f;
+  for (int p0 = 0; p0 < count; p0 += 32) {
+    const float2 ml = p0 + lane < count ? a.part_ml[slot(p0 + lane) * ROWS + r]
+                                        : make_float2(-INFINITY, 0.f);
+    float m1 = fmaxf(m, ml.x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+    const float f = m1 == -INFINITY ? 1.f : ex2_approx(m - m1);
+    const float w = m1 == -INFINITY ? 1.f : ex2_approx(ml.x - m1);
+    float sum = ml.y * w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    m = m1;
+    l = l * f + sum;
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] *= f;
+#pragma unroll 4
+    for (int p = p0; p < min(count, p0 + 32); ++p) {
+      const float wp = __shfl_sync(0xffffffffu, w, p - p0);
+      const float* x = a.part_o + (slot(p) * ROWS + r) * D + lane * E;
+      if constexpr (E == 4) {
+        const float4 z = *reinterpret_cast<const float4*>(x);
+        y[0] += z.x * wp, y[1] += z.y * wp, y[2] += z.z * wp, y[3] += z.w * wp;
+      } else {
+        const float2 z = *reinterpret_cast<const float2*>(x);
+        y[0] += z.x * wp, y[1] += z.y * wp;
+      }
+    }
+  }
+  if constexpr (E == 4) {
+    store_row4(a, b, kvh, row, 4 * lane, m, l, make_float4(y[0], y[1], y[2], y[3]));
+  } else {  // two lanes' elements to one store
+    const float z0 = __shfl_down_sync(0xffffffffu, y[0], 1);
+    const float z1 = __shfl_down_sync(0xffffffffu, y[1], 1);
+    if ((lane & 1) == 0)
+      store_row4(a, b, kvh, row, 2 * lane, m, l, make_float4(y[0], y[1], z0, z1));
+  }
+}
+
 // Query row tiles of a call: as few tensor-core columns as hold its rows, up
 // to 32 to a CTA, and equal shares where one CTA does not hold them.
 struct Plan {
@@ -898,7 +957,7 @@ bsfa_status validate_sizes(const bsfa_cache4* c, const bsfa_decode4_params* p) {
 
 template <int D, int NT, bool DENSE>
 bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaStream_t stream) {
-  constexpr int smem = smem_bytes<D, NT>();
+  constexpr int smem = smem_bytes<D, NT>(true);
   static_assert(Shape<NT>::MAX_GRID <= MAX_PARTS, "the join's weights");
   // The shared-memory size of a kernel is set once per device.
   static std::atomic<uint64_t> ready{0};
@@ -913,7 +972,7 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(pl.segments * pl.cluster));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = smem_bytes<D, NT>(pl.cluster > 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -930,11 +989,15 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
   if (most < grid) grid = most;
   DecArgs a = args;
   a.join_by_segment = pl.segments <= grid;
-  decode4_kernel<D, NT, DENSE><<<static_cast<unsigned>(grid), THREADS, smem, stream>>>(a);
+  decode4_kernel<D, NT, DENSE>
+      <<<static_cast<unsigned>(grid), THREADS, smem_bytes<D, NT>(false), stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return BSFA_ERR_CUDA;
+  // About grid / segments parts to a segment.
+  const bool by_rows = grid < JOIN_ROWS_PARTS * pl.segments;
+  const int rows = a.rows < 8 * NT ? a.rows : 8 * NT, per_block = by_rows ? JOIN_THREADS / 32 : 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(a.join_by_segment ? pl.segments : grid),
-                     a.rows < 8 * NT ? a.rows : 8 * NT);
+                     (rows + per_block - 1) / per_block);
   cfg.blockDim = dim3(JOIN_THREADS);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
@@ -942,9 +1005,10 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode4_join_kernel<D, 8 * NT>, a) == cudaSuccess
-             ? BSFA_OK
-             : BSFA_ERR_CUDA;
+  const cudaError_t e =
+      by_rows ? cudaLaunchKernelEx(&cfg, decode4_join_rows_kernel<D, 8 * NT>, a)
+              : cudaLaunchKernelEx(&cfg, decode4_join_kernel<D, 8 * NT>, a);
+  return e == cudaSuccess ? BSFA_OK : BSFA_ERR_CUDA;
 }
 
 }  // namespace

@@ -191,36 +191,33 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Thread-block clusters: this CTA's rank, a barrier over all threads (release
-// and acquire), and loads from the CTA of rank k at a local address's offset.
+// Thread-block clusters: this CTA's rank, the two halves of a barrier over all
+// threads (release and acquire), and stores into the CTA of rank k at a local
+// address's offset.
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float4 cluster_ld4(uint32_t addr, uint32_t k) {
-  float4 r;
-  asm volatile(
-      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
-      "ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [a];\n\t}"
-      : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
-      : "r"(addr), "r"(k)
-      : "memory");
-  return r;
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float2 cluster_ld2(uint32_t addr, uint32_t k) {
-  float2 r;
+__device__ __forceinline__ void cluster_st4(uint32_t addr, uint32_t k, float4 x) {
   asm volatile(
-      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\t"
-      "ld.shared::cluster.v2.f32 {%0,%1}, [a];\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "r"(addr), "r"(k)
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+      "st.shared::cluster.v4.f32 [a], {%2,%3,%4,%5};\n\t}" ::"r"(addr),
+      "r"(k), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w)
       : "memory");
-  return r;
+}
+__device__ __forceinline__ void cluster_st2(uint32_t addr, uint32_t k, float2 x) {
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+      "st.shared::cluster.v2.f32 [a], {%2,%3};\n\t}" ::"r"(addr),
+      "r"(k), "f"(x.x), "f"(x.y)
+      : "memory");
 }
 
 }  // namespace bsfa
