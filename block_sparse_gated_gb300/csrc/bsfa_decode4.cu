@@ -57,6 +57,11 @@ constexpr int JOIN_THREADS = 256;   // of the kernel that joins parts
 constexpr int JOIN_ROWS_PARTS = 8;  // a warp to a row below, a block above
 constexpr int MAX_PARTS = 768;      // parts of a segment, at most: CTAs of a cut call
 constexpr int MAX_CLUSTER = 8;      // CTAs that share a segment, at most
+constexpr int WIDE_WARPS = 16;       // warps of a CTA where there are few segments
+constexpr int WIDE_GRID = 152;       // CTAs of that size: the GPU's SMs
+constexpr int WIDE_GRID_OF_8 = 64;   // ... in clusters of eight
+constexpr int WIDE_LEAST = 8;        // units of a segment worth one
+constexpr int WIDE_UNITS = 32;       // units of a segment per CTA of that size, at most
 constexpr int CLUSTER_UNITS = 16;   // units of a segment per CTA of a cluster, at most
 
 // Per row-tile width (NT tiles of 8 query rows): CTAs per SM, ring stages,
@@ -150,15 +155,15 @@ constexpr int MERGE_ROW = D + 12;
 
 // Dynamic shared memory: the rings, whose place the warps' sums take later, and
 // behind them what the CTAs of a cluster send each other.
-template <int D, int NT>
+template <int D, int NT, int W>
 constexpr int ring_bytes() {
-  constexpr int ring = WARPS * Shape<NT>::STAGES * Stage<D>::BYTES;
-  constexpr int merge = WARPS * MERGE_ROW<D> * 8 * NT * 4;
+  constexpr int ring = W * Shape<NT>::STAGES * Stage<D>::BYTES;
+  constexpr int merge = W * MERGE_ROW<D> * 8 * NT * 4;
   return ring > merge ? ring : merge;
 }
-template <int D, int NT>
+template <int D, int NT, int W>
 constexpr int smem_bytes(bool cluster) {
-  return ring_bytes<D, NT>() + (cluster ? 8 * NT * D * 4 : 0);
+  return ring_bytes<D, NT, W>() + (cluster ? 8 * NT * D * 4 : 0);
 }
 
 // Where a CTA's piece of the line begins.
@@ -233,8 +238,11 @@ __device__ __forceinline__ void store_row4(const DecArgs& a, int b, int kvh, int
 
 // DENSE: the tokens of a page lie together in each pool, so that the strides of
 // the copies are constants.
-template <int D, int NT, bool DENSE>
-__global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const DecArgs a) {
+template <int D, int NT, bool DENSE, int W>
+__global__ void __launch_bounds__(32 * W, W == WARPS ? Shape<NT>::CTAS : 1)
+    decode4_kernel(const DecArgs a) {
+  constexpr int WARPS = W, THREADS = 32 * W;  // of this CTA
+  constexpr int UNIT_TILES = UNIT / TOK;
   constexpr int STAGES = Shape<NT>::STAGES;
   constexpr int KSTEPS = D / 16;  // 16-element steps of K Q^T
   constexpr int MT = D / 16;      // 16-element row tiles of V^T P^T
@@ -252,7 +260,7 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
 
   if (a.cluster > 1) cluster_arrive();
   Piece piece;
-  if (a.split) {
+  if (W == bsfa::WARPS && a.split) {
     if (tid == 0 && !a.join_by_segment) a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
     piece = cut(a, sh_cut);
   } else {  // one segment per cluster; u walks over it once
@@ -284,8 +292,8 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
     const int max_lim = a.causal ? max(0, len - a.q_len + last_i + 1) : len;
 
     // ---- this warp's tiles: an equal run of the piece's
-    int t0 = max(0, u0 - SEGMENT_UNITS) * WARPS;
-    int t1 = min(max(0, u1 - SEGMENT_UNITS) * WARPS, (max_lim + TOK - 1) / TOK);
+    int t0 = max(0, u0 - SEGMENT_UNITS) * UNIT_TILES;
+    int t1 = min(max(0, u1 - SEGMENT_UNITS) * UNIT_TILES, (max_lim + TOK - 1) / TOK);
     if (a.cluster > 1) {  // this CTA's share of the segment
       const int share = (t1 + a.cluster - 1) / a.cluster;
       t0 = min(t1, static_cast<int>(cluster_rank()) * share);
@@ -675,7 +683,7 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
       // CTAs in order.  (Sums left in place and read remotely need a second
       // barrier and wait for the loads: 1 x 4097 tokens 9.6 us, pushed @@ us.)
       const int items = ROWS * (D / 4) / a.cluster;  // the cluster is a power of two
-      const uint32_t rank = cluster_rank(), got = smem_u32(ring) + ring_bytes<D, NT>();
+      const uint32_t rank = cluster_rank(), got = smem_u32(ring) + ring_bytes<D, NT, W>();
       cluster_wait();  // the one of the kernel's beginning: every CTA runs
       for (int x = tid; x < n_rows * (D / 4); x += THREADS) {
         const int r = x / (D / 4), d0 = (x % (D / 4)) * 4;
@@ -703,7 +711,7 @@ __global__ void __launch_bounds__(THREADS, Shape<NT>::CTAS) decode4_kernel(const
       cluster_arrive();
       cluster_wait();
       const float4* parts =
-          reinterpret_cast<const float4*>(ring + ring_bytes<D, NT>());
+          reinterpret_cast<const float4*>(ring + ring_bytes<D, NT, W>());
       for (int k = tid; k * a.cluster + rank < n_rows * (D / 4); k += THREADS) {
         const int x = k * a.cluster + rank, r = x / (D / 4), d0 = (x % (D / 4)) * 4;
         float m = sh_cluster[0][r].x;
@@ -896,7 +904,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) decode4_join_rows_kernel(const D
 struct Plan {
   int nt, row_tiles, units, max_grid, cluster;
   long long segments, all_units;
-  bool split;
+  bool split, wide;
 };
 
 Plan plan_of(const bsfa_cache4* c, const bsfa_decode4_params* p) {
@@ -912,12 +920,26 @@ Plan plan_of(const bsfa_cache4* c, const bsfa_decode4_params* p) {
   constexpr int grids[4] = {Shape<1>::MAX_GRID, Shape<2>::MAX_GRID, Shape<3>::MAX_GRID,
                             Shape<4>::MAX_GRID};
   pl.max_grid = grids[pl.nt - 1];
-  // As many CTAs to a segment as keep them all resident at once.
+  // Few segments, of half a thousand tokens or more: a CTA of 16 warps to an SM
+  // (19 ragged sequences to 1024: 13.8 -> 9.5 us; 1 x 4097: 9.4 -> 8.8; 1 x 300
+  // would go from 6.6 to 7.1).  Otherwise CTAs of four.  As many CTAs to a segment
+  // as keep them all resident at once, eight wide ones only up to 64 in all (2 x
+  // 16K, 128 of them: 27 us, cut 19): a cluster lies within one GPC.
+  pl.wide = pl.nt == 1 && pl.segments <= WIDE_GRID && pl.units >= WIDE_LEAST;
   pl.cluster = 1;
-  while (pl.cluster < MAX_CLUSTER && pl.units >= 2 * pl.cluster &&
-         2 * pl.segments * pl.cluster <= pl.max_grid)
-    pl.cluster *= 2;
-  pl.split = pl.units > CLUSTER_UNITS * pl.cluster;
+  while (pl.cluster < MAX_CLUSTER && pl.units >= 2 * pl.cluster) {
+    const int next = 2 * pl.cluster;
+    const int resident = !pl.wide ? pl.max_grid : next == MAX_CLUSTER ? WIDE_GRID_OF_8 : WIDE_GRID;
+    if (pl.segments * next > resident) break;
+    pl.cluster = next;
+  }
+  // Longer segments are cut.  Wide CTAs stay ahead of the cut for twice as long
+  // where they fill more than half of the GPU (4 x 16K: 21.8 and 24.4 us, 1 x 32K:
+  // 20.5 and 18.8).
+  const int most = !pl.wide                                        ? CLUSTER_UNITS
+                   : 2 * pl.segments * pl.cluster > WIDE_GRID ? 2 * WIDE_UNITS
+                                                                   : WIDE_UNITS;
+  pl.split = pl.units > most * pl.cluster;
   if (pl.split) pl.cluster = 1;
   return pl;
 }
@@ -955,15 +977,15 @@ bsfa_status validate_sizes(const bsfa_cache4* c, const bsfa_decode4_params* p) {
   return BSFA_OK;
 }
 
-template <int D, int NT, bool DENSE>
+template <int D, int NT, bool DENSE, int W = WARPS>
 bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaStream_t stream) {
-  constexpr int smem = smem_bytes<D, NT>(true);
+  constexpr int smem = smem_bytes<D, NT, W>(true);
   static_assert(Shape<NT>::MAX_GRID <= MAX_PARTS, "the join's weights");
   // The shared-memory size of a kernel is set once per device.
   static std::atomic<uint64_t> ready{0};
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    if (cudaFuncSetAttribute(decode4_kernel<D, NT, DENSE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(decode4_kernel<D, NT, DENSE, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem) != cudaSuccess)
       return BSFA_ERR_CUDA;
     ready.fetch_or(bit, std::memory_order_relaxed);
@@ -971,8 +993,8 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
   if (!pl.split) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(pl.segments * pl.cluster));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem_bytes<D, NT>(pl.cluster > 1);
+    cfg.blockDim = dim3(32 * W);
+    cfg.dynamicSmemBytes = smem_bytes<D, NT, W>(pl.cluster > 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -980,35 +1002,38 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode4_kernel<D, NT, DENSE>, args) == cudaSuccess ? BSFA_OK
+    return cudaLaunchKernelEx(&cfg, decode4_kernel<D, NT, DENSE, W>, args) == cudaSuccess ? BSFA_OK
                                                                              : BSFA_ERR_CUDA;
   }
-  const long long full = static_cast<long long>(sms) * Shape<NT>::CTAS;
-  long long grid = full < pl.max_grid ? full : pl.max_grid;
-  const long long most = (pl.all_units + MIN_UNITS - 1) / MIN_UNITS;
-  if (most < grid) grid = most;
-  DecArgs a = args;
-  a.join_by_segment = pl.segments <= grid;
-  decode4_kernel<D, NT, DENSE>
-      <<<static_cast<unsigned>(grid), THREADS, smem_bytes<D, NT>(false), stream>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return BSFA_ERR_CUDA;
-  // About grid / segments parts to a segment.
-  const bool by_rows = grid < JOIN_ROWS_PARTS * pl.segments;
-  const int rows = a.rows < 8 * NT ? a.rows : 8 * NT, per_block = by_rows ? JOIN_THREADS / 32 : 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.join_by_segment ? pl.segments : grid),
-                     (rows + per_block - 1) / per_block);
-  cfg.blockDim = dim3(JOIN_THREADS);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e =
-      by_rows ? cudaLaunchKernelEx(&cfg, decode4_join_rows_kernel<D, 8 * NT>, a)
-              : cudaLaunchKernelEx(&cfg, decode4_join_kernel<D, 8 * NT>, a);
-  return e == cudaSuccess ? BSFA_OK : BSFA_ERR_CUDA;
+  if constexpr (W == WARPS) {  // CTAs of WIDE_WARPS never cut
+    const long long full = static_cast<long long>(sms) * Shape<NT>::CTAS;
+    long long grid = full < pl.max_grid ? full : pl.max_grid;
+    const long long most = (pl.all_units + MIN_UNITS - 1) / MIN_UNITS;
+    if (most < grid) grid = most;
+    DecArgs a = args;
+    a.join_by_segment = pl.segments <= grid;
+    decode4_kernel<D, NT, DENSE, W>
+        <<<static_cast<unsigned>(grid), THREADS, smem_bytes<D, NT, W>(false), stream>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return BSFA_ERR_CUDA;
+    // About grid / segments parts to a segment.
+    const bool by_rows = grid < JOIN_ROWS_PARTS * pl.segments;
+    const int rows = a.rows < 8 * NT ? a.rows : 8 * NT, per_block = by_rows ? JOIN_THREADS / 32 : 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.join_by_segment ? pl.segments : grid),
+                       (rows + per_block - 1) / per_block);
+    cfg.blockDim = dim3(JOIN_THREADS);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e =
+        by_rows ? cudaLaunchKernelEx(&cfg, decode4_join_rows_kernel<D, 8 * NT>, a)
+                : cudaLaunchKernelEx(&cfg, decode4_join_kernel<D, 8 * NT>, a);
+    return e == cudaSuccess ? BSFA_OK : BSFA_ERR_CUDA;
+  }
+  return BSFA_ERR_CUDA;
 }
 
 }  // namespace
@@ -1098,13 +1123,18 @@ bsfa_status bsfa_decode4(const bsfa_cache4* cache, const bsfa_decode4_params* p,
   const bool dense = cache->k_stride[2] == row && cache->v_stride[2] == row &&
                      cache->k_scale_stride[2] == z && cache->v_scale_stride[2] == z;
   using Launch = bsfa_status (*)(const DecArgs&, const Plan&, int, int, cudaStream_t);
-  static const Launch launches[2][2][4] = {  // [d = 128][dense][tiles of 8 query rows - 1]
-      {{launch<64, 1, false>, launch<64, 2, false>, launch<64, 3, false>, launch<64, 4, false>},
-       {launch<64, 1, true>, launch<64, 2, true>, launch<64, 3, true>, launch<64, 4, true>}},
+  static const Launch launches[2][2][5] = {
+      // [d = 128][dense][tiles of 8 query rows - 1, or one tile and wide CTAs]
+      {{launch<64, 1, false>, launch<64, 2, false>, launch<64, 3, false>, launch<64, 4, false>,
+        launch<64, 1, false, WIDE_WARPS>},
+       {launch<64, 1, true>, launch<64, 2, true>, launch<64, 3, true>, launch<64, 4, true>,
+        launch<64, 1, true, WIDE_WARPS>}},
       {{launch<128, 1, false>, launch<128, 2, false>, launch<128, 3, false>,
-        launch<128, 4, false>},
-       {launch<128, 1, true>, launch<128, 2, true>, launch<128, 3, true>, launch<128, 4, true>}}};
-  return launches[cache->head_dim == 128][dense][pl.nt - 1](a, pl, sms, dev, stream);
+        launch<128, 4, false>, launch<128, 1, false, WIDE_WARPS>},
+       {launch<128, 1, true>, launch<128, 2, true>, launch<128, 3, true>, launch<128, 4, true>,
+        launch<128, 1, true, WIDE_WARPS>}}};
+  const int which = pl.wide && !pl.split ? 4 : pl.nt - 1;
+  return launches[cache->head_dim == 128][dense][which](a, pl, sms, dev, stream);
 }
 
 }  // extern "C"

@@ -62,9 +62,9 @@ def random_cache(bsfa, lens, page, heads, d, seed, device, *, layout="phtd", exp
     return bsfa.KVCache4(*t, *e, layout), torch.from_numpy(table).to(device), rows
 
 
-def widen(table, page, tokens=9000):
+def widen(table, page, tokens=70000):
     """The same table with unused columns up to a capacity of ``tokens``: the
-    bound that a call works with when it is given none.  Beyond 8192 a call
+    bound that a call works with when it is given none.  With the default a call
     cuts the batch into equal pieces instead of giving each sequence a cluster."""
     more = -(-tokens // page) - table.shape[1]
     pad = torch.full((table.shape[0], max(0, more)), 1 << 30, dtype=torch.int32,

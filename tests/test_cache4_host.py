@@ -152,21 +152,21 @@ def test_decode_parameters_that_are_refused(lib):
         p = _decode(**change)
         assert lib.bsfa_decode4(c, ctypes.byref(p), None) == status, change
         assert size(c, ctypes.byref(p)) == 0, change
-    long = _cache(block_table_width=200, block_table_stride=200)
-    c2 = ctypes.byref(long)  # a bound beyond 8192 needs a workspace
-    need = size(c2, ctypes.byref(_decode(max_seqlen=8193)))
-    assert need > 0 and size(c2, ctypes.byref(_decode(max_seqlen=8192))) == 0
+    long = _cache(block_table_width=2000, block_table_stride=2000)
+    c2 = ctypes.byref(long)  # a bound this long needs a workspace
+    need = size(c2, ctypes.byref(_decode(max_seqlen=100000)))
+    assert need > 0 and size(c2, ctypes.byref(_decode(max_seqlen=4096))) == 0
     for change, status in ((dict(q=0), INVALID), (dict(seqlens=0), INVALID),
                            (dict(o=(1 << 20) + 8), UNSUPPORTED), (dict(), WORKSPACE),
                            (dict(workspace=128, workspace_bytes=1 << 30), WORKSPACE),
                            (dict(workspace=1 << 20, workspace_bytes=0), WORKSPACE),
                            (dict(workspace=1 << 20, workspace_bytes=need - 1), WORKSPACE)):
-        p = _decode(max_seqlen=8193, **change)
+        p = _decode(max_seqlen=100000, **change)
         assert lib.bsfa_decode4(c2, ctypes.byref(p), None) == status, change
-    p = _decode(max_seqlen=8193)
+    p = _decode(max_seqlen=100000)
     p.q_stride[1] = 4
     assert lib.bsfa_decode4(c2, ctypes.byref(p), None) == UNSUPPORTED
-    p = _decode(max_seqlen=8193)
+    p = _decode(max_seqlen=100000)
     p.q_stride[2] = 3  # the only token's stride says nothing
     assert lib.bsfa_decode4(c2, ctypes.byref(p), None) == WORKSPACE
     for empty in (dict(batch=0), dict(q_len=0)):
