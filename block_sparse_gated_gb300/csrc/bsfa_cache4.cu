@@ -345,7 +345,7 @@ bsfa_status validate_cache4(const bsfa_cache4* c) {
     return BSFA_ERR_INVALID_ARG;
   if (c->head_dim != 64 && c->head_dim != 128) return BSFA_ERR_UNSUPPORTED;
   if (c->page_size % 16) return BSFA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(c->block_table_width) * c->page_size > 0x7fffffffLL)
+  if (static_cast<long long>(c->block_table_width) * c->page_size > (1LL << 30))
     return BSFA_ERR_UNSUPPORTED;
   if (c->num_heads_kv > CACHE4_MAX_HEADS) return BSFA_ERR_UNSUPPORTED;
   return BSFA_OK;

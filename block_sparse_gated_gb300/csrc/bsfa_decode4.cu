@@ -18,18 +18,22 @@
 // keys pair neighbours of one token, values pair two tokens by merging nibbles.
 //
 // Work split.  A segment is one (sequence, KV head, row tile).  Where it is
-// short by the caller's bound, a cluster of up to eight CTAs shares it and joins
-// its sums through distributed shared memory: one launch, no workspace.
+// short by the caller's bound, a cluster of up to eight CTAs (of four warps, or
+// sixteen where segments are few) shares it and joins its sums through
+// distributed shared memory: one launch, no workspace.
 // Longer ones are counted in units of 64 tokens; the units of all segments form
 // one line, which is cut into equal pieces, one per CTA, from the lengths on the
 // device.  Long and short sequences balance without the host knowing them, and a
 // captured call stays right as they grow.  A segment that a cut crosses leaves
 // partial sums in the workspace, which a second kernel joins in a fixed order.
 //
-// Bound.  HBM: 144 bytes per (token, KV head) at d = 128, against about 240
-// issued warp instructions per 16 tokens and head.  Each warp streams its own
-// 16-token tiles through a private ring of asynchronous copies; no barrier is
-// met inside a segment.
+// Bound.  144 bytes per (token, KV head) at d = 128 set the floor: 100 cycles of
+// an SM per 16 tokens and head at a copy's rate.  They take 269 issued warp
+// instructions (64 conversions, 64 fp16x2 products and 16 tensor products among
+// them), 67 cycles at best and 110 as measured: 64 ragged sequences to 16K (633 MB)
+// take 111 us, 5.7 TB/s or 84% of a copy's 6.77.  Each warp streams its own
+// 16-token tiles through a private ring of asynchronous copies; no barrier is met
+// inside a segment.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -57,12 +61,12 @@ constexpr int JOIN_THREADS = 256;   // of the kernel that joins parts
 constexpr int JOIN_ROWS_PARTS = 8;  // a warp to a row below, a block above
 constexpr int MAX_PARTS = 768;      // parts of a segment, at most: CTAs of a cut call
 constexpr int MAX_CLUSTER = 8;      // CTAs that share a segment, at most
-constexpr int WIDE_WARPS = 16;       // warps of a CTA where there are few segments
-constexpr int WIDE_GRID = 152;       // CTAs of that size: the GPU's SMs
-constexpr int WIDE_GRID_OF_8 = 64;   // ... in clusters of eight
-constexpr int WIDE_LEAST = 8;        // units of a segment worth one
-constexpr int WIDE_UNITS = 32;       // units of a segment per CTA of that size, at most
 constexpr int CLUSTER_UNITS = 16;   // units of a segment per CTA of a cluster, at most
+constexpr int WIDE_WARPS = 16;      // warps of a CTA where there are few segments
+constexpr int WIDE_GRID = 152;      // CTAs of that size: the GPU's SMs
+constexpr int WIDE_GRID_OF_8 = 64;  // ... in clusters of eight
+constexpr int WIDE_LEAST = 8;       // units of a segment worth one
+constexpr int WIDE_UNITS = 32;      // units of a segment per CTA of that size, at most
 
 // Per row-tile width (NT tiles of 8 query rows): CTAs per SM, ring stages,
 // whether the main loop goes around the ring in one piece (64 ragged sequences
@@ -681,7 +685,7 @@ __global__ void __launch_bounds__(32 * W, W == WARPS ? Shape<NT>::CTAS : 1)
       // CTA stores its sums, and the references, straight into the joining CTAs'
       // shared memory, and after one barrier every CTA adds what it got, over the
       // CTAs in order.  (Sums left in place and read remotely need a second
-      // barrier and wait for the loads: 1 x 4097 tokens 9.6 us, pushed @@ us.)
+      // barrier and wait for the loads: 8 x 2K tokens 10.8 us, pushed 10.3.)
       const int items = ROWS * (D / 4) / a.cluster;  // the cluster is a power of two
       const uint32_t rank = cluster_rank(), got = smem_u32(ring) + ring_bytes<D, NT, W>();
       cluster_wait();  // the one of the kernel's beginning: every CTA runs

@@ -336,7 +336,8 @@ typedef struct {
    * sees a zero key and a zero value (a prefill's page table does the same). */
   const int32_t* block_table; /* device int32 [batch][block_table_stride] */
   int block_table_stride;     /* elements between two sequences' rows, >= width */
-  int block_table_width;      /* entries of each row that may be read */
+  int block_table_width;      /* entries of each row that may be read;
+                                 block_table_width * page_size <= 2^30 */
 } bsfa_cache4;
 
 /* 16-bit rows that bsfa_cache4_write takes or bsfa_cache4_read gives.

@@ -97,7 +97,7 @@ int main(void) {
     (dict(page_size=0), INVALID), (dict(num_pages=0), INVALID), (dict(num_heads_kv=0), INVALID),
     (dict(num_heads_kv=4097), UNSUPPORTED), (dict(block_table_width=5), INVALID),
     (dict(block_table_width=-1), INVALID),
-    (dict(block_table_width=1 << 26, block_table_stride=1 << 26), UNSUPPORTED),
+    (dict(block_table_width=(1 << 24) + 1, block_table_stride=1 << 25), UNSUPPORTED),
     (dict(k=0), INVALID), (dict(v_scale=0), INVALID), (dict(block_table=0), INVALID),
     (dict(k=(1 << 20) + 8), UNSUPPORTED), (dict(k_scale=(1 << 20) + 4), UNSUPPORTED),
 ])

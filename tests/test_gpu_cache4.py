@@ -261,6 +261,33 @@ def test_exponent_range_and_rounding_to_the_output_type(cuda_device):
         assert torch.equal(k, (base * f).float().to(dtype))
 
 
+def test_the_largest_batch(cuda_device):
+    """One token of each of 4096 sequences, batched and packed."""
+    b = _bsfa()
+    g = torch.Generator().manual_seed(12)
+    x = torch.randn(2, 4096, 1, 1, 64, generator=g).to(HF)
+    k, v = x.to(cuda_device)
+    start = torch.randint(0, 32, (4096,), generator=g, dtype=torch.int32).to(cuda_device)
+    table = torch.randperm(8192, generator=g).to(torch.int32).view(4096, 2).to(cuda_device)
+    got = []
+    for packed in (False, True):
+        cache = b.cache4_empty(8192, 1, 16, 64, device=cuda_device)
+        kw = {"start": start}
+        if packed:
+            kw["cu_seqlens"] = torch.arange(4097, dtype=torch.int32, device=cuda_device)
+            b.cache4_write(cache, k.view(1, 4096, 64), v.view(1, 4096, 64), table, **kw)
+            got.append(b.cache4_read(cache, table, total=4096, dtype=HF, **kw)[0].view(4096, 64))
+        else:
+            b.cache4_write(cache, k, v, table, **kw)
+            got.append(b.cache4_read(cache, table, seqlen=1, dtype=HF, **kw)[0].view(4096, 64))
+        page, row = table.long().gather(1, start.long()[:, None] // 16)[:, 0], start.long() % 16
+        codes, scale = cache.k[page, 0, row].cpu().numpy(), _as_u8(cache.k_scale)
+        want, byte = co.quantise(x[0].view(4096, 64).double().numpy())
+        assert _same_codes(codes, co.pack(want), None)
+        assert np.array_equal(scale[page.cpu().numpy(), 0, row.cpu().numpy()], byte)
+    assert torch.equal(got[0], got[1])
+
+
 def test_streams_and_graphs(cuda_device):
     """A side stream, and a captured write-and-read replayed on new data."""
     b = _bsfa()

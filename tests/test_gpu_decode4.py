@@ -27,10 +27,10 @@ def _i32(x, device):
     return torch.tensor(x, dtype=torch.int32, device=device)
 
 
-# (heads q, heads kv, query tokens): rows of one KV head 1 .. 40, so that every
+# (heads q, heads kv, query tokens): rows of one KV head 1 .. 70, so that every
 # width of the query row tile and more than one tile of them occur.
 HEADS = [(2, 2, 1), (8, 2, 1), (8, 1, 1), (9, 3, 2), (12, 1, 1), (4, 1, 4), (8, 2, 5), (6, 2, 8),
-         (8, 1, 5)]
+         (32, 1, 1), (10, 1, 3), (8, 1, 5), (14, 1, 5)]
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -117,6 +117,48 @@ def test_lengths_beyond_the_bound_are_cut(cuda_device):
     given = _i32([400, 1 << 30, -5, -(1 << 31)], cuda_device)
     res = b.decode4(q, cache, table[:, :25], given, max_seqlen=390, return_lse=True)
     cu.check_decode(res, q, rows, [390, 390, 0, 0], BF, 64)
+
+
+def test_no_length_at_all(cuda_device):
+    """A bound of 0: every query sees nothing, whatever seqlens says."""
+    b = _bsfa()
+    cache, table, _ = cu.random_cache(b, [40, 40], 16, 2, 128, 8, cuda_device)
+    q = _queries(2, 8, 3, 128, HF, 8, cuda_device)
+    res = b.decode4(q, cache, table, _i32([40, 7], cuda_device), max_seqlen=0, return_lse=True)
+    assert not res["out"].any() and bool(torch.isneginf(res["lse"]).all())
+    none = b.decode4(q[:, :, :0], cache, table, _i32([40, 7], cuda_device), return_lse=True)
+    assert none["out"].shape == (2, 8, 0, 128) and none["lse"].shape == (8, 0)
+
+
+@pytest.mark.parametrize("cut", [True, False])
+def test_the_largest_batch(cuda_device, cut):
+    """4096 sequences of 0 to 3 tokens and one of 500; one more is refused."""
+    b = _bsfa()
+    lens = [int(x) for x in np.random.default_rng(5).integers(0, 4, 4096)]
+    lens[2222] = 500
+    cache, table, rows = cu.random_cache(b, lens, 16, 1, 64, 2, cuda_device)
+    table = cu.widen(table, 16) if cut else table
+    q = _queries(4097, 2, 1, 64, BF, 2, cuda_device)
+    n32 = _i32(lens + [1], cuda_device)
+    res = b.decode4(q[:4096], cache, table, n32[:4096], return_lse=True)
+    cu.check_decode(res, q[:4096], rows, lens, BF, 64)
+    with pytest.raises(b.BsfaError, match="unsupported"):
+        b.decode4(q, cache, torch.cat([table, table[:1]]), n32)
+
+
+@pytest.mark.parametrize("batch,length,d", [(1, 4097, 128), (2, 3000, 64), (19, 600, 128),
+                                            (40, 550, 64), (75, 513, 128), (3, 16000, 64)])
+def test_few_sequences_of_some_length(cuda_device, batch, length, d):
+    """Wide CTAs in clusters of 8 down to 1, and the lengths' bounds between
+    them and the cut."""
+    b = _bsfa()
+    rng = np.random.default_rng(batch)
+    lens = [length] + [int(x) for x in rng.integers(0, length + 1, batch - 1)]
+    lens = [x if i < 4 else x % 100 for i, x in enumerate(lens)]
+    cache, table, rows = cu.random_cache(b, lens, 32, 2, d, 6, cuda_device)
+    q = _queries(batch, 8, 1, d, HF, 6, cuda_device, 1.5)
+    res = b.decode4(q, cache, table, _i32(lens, cuda_device), max_seqlen=length, return_lse=True)
+    cu.check_decode(res, q, rows, lens, HF, d)
 
 
 def test_entries_outside_the_pool_read_as_zero_rows(cuda_device):
