@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(32 * W, W == WARPS ? Shape<NT>::CTAS : 1)
   __shared__ int sh_cut[WARPS + 2];
   __shared__ uint2 sh_q[NT * KSTEPS * 32];
   __shared__ float sh_sc[ROWS];
+  __shared__ int sh_lim[ROWS];  // positions below it are visible to the row
   __shared__ float2 sh_ml[WARPS][ROWS];
   __shared__ float2 sh_cluster[MAX_CLUSTER][ROWS];
 
@@ -394,8 +395,11 @@ __global__ void __launch_bounds__(32 * W, W == WARPS ? Shape<NT>::CTAS : 1)
       const int ex = (__float_as_int(amax) >> 23) - 127;
       const int up = amax == 0.f || ex > 127 ? 0 : min(14 - ex, 100);
       const float mul = pow2f(up);
-      if (c == 0)
+      if (c == 0) {
         sh_sc[nt * 8 + g] = a.sigma_log2 * pow2f(-up) * pow2f(head_exp(a.kexp, kvh));
+        // Rows past the last are computed along with the rest and not stored.
+        sh_lim[nt * 8 + g] = !a.causal || r >= a.rows ? len : len - a.q_len + r / a.group + 1;
+      }
 #pragma unroll
       for (int j = 0; j < KSTEPS; ++j)
         sh_q[(nt * KSTEPS + j) * 32 + lane] =
@@ -406,9 +410,8 @@ __global__ void __launch_bounds__(32 * W, W == WARPS ? Shape<NT>::CTAS : 1)
 
     // ---- per-lane columns: 2c and 2c + 1 of each row tile
     float acc[NT][MT][4];
-    float ref[NT][2], sum[NT][2], sc[NT][2];
-    float zn[NT][2];  // SHIFT - ref: a weight is 2^(sc * product + zn)
-    int lim[NT][2];
+    float sum[NT][2], sc[NT][2];
+    float zn[NT][2];  // SHIFT - reference: a weight is 2^(sc * product + zn)
     uint2 qf[NT == 1 ? KSTEPS : 1];  // one row tile's queries stay in registers
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -418,13 +421,9 @@ __global__ void __launch_bounds__(32 * W, W == WARPS ? Shape<NT>::CTAS : 1)
         for (int e = 0; e < 4; ++e) acc[nt][mt][e] = 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = r0 + nt * 8 + 2 * c + e;
-        ref[nt][e] = -INFINITY;
         zn[nt][e] = INFINITY;
         sum[nt][e] = 0.f;
         sc[nt][e] = sh_sc[nt * 8 + 2 * c + e];
-        // Rows past the last are computed along with the rest and not stored.
-        lim[nt][e] = !a.causal || r >= a.rows ? len : len - a.q_len + r / a.group + 1;
       }
     }
     if constexpr (NT == 1) {
@@ -498,6 +497,7 @@ __global__ void __launch_bounds__(32 * W, W == WARPS ? Shape<NT>::CTAS : 1)
 
       // ---- weights; the reference moves where one would pass 2^(SHIFT + HEADROOM)
       float y[NT][4];
+      auto lim = [&](int nt, int e) { return sh_lim[nt * 8 + 2 * c + e]; };
       auto weigh = [&]() {
         bool over = false;
 #pragma unroll
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(32 * W, W == WARPS ? Shape<NT>::CTAS : 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             y[nt][e] = fmaf(s[nt][e], sc[nt][e & 1], zn[nt][e & 1]);
-            if (MASKED && tok0 + my_tok + (e & 2) * 4 >= lim[nt][e & 1]) y[nt][e] = -INFINITY;
+            if (MASKED && tok0 + my_tok + (e & 2) * 4 >= lim(nt, e & 1)) y[nt][e] = -INFINITY;
             over |= y[nt][e] > SHIFT + HEADROOM;
           }
         return over;
@@ -517,15 +517,15 @@ __global__ void __launch_bounds__(32 * W, W == WARPS ? Shape<NT>::CTAS : 1)
           for (int e = 0; e < 2; ++e) {
             float lo = s[nt][e] * sc[nt][e], hi = s[nt][e + 2] * sc[nt][e];
             if (MASKED) {
-              if (tok0 + my_tok >= lim[nt][e]) lo = -INFINITY;
-              if (tok0 + my_tok + 8 >= lim[nt][e]) hi = -INFINITY;
+              if (tok0 + my_tok >= lim(nt, e)) lo = -INFINITY;
+              if (tok0 + my_tok + 8 >= lim(nt, e)) hi = -INFINITY;
             }
-            float m1 = fmaxf(ref[nt][e], fmaxf(lo, hi));
+            const float m0 = SHIFT - zn[nt][e];
+            float m1 = fmaxf(m0, fmaxf(lo, hi));
             m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 4));
             m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 8));
             m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, 16));
-            const float f = m1 == -INFINITY ? 1.f : ex2_approx(ref[nt][e] - m1);
-            ref[nt][e] = m1;
+            const float f = m1 == -INFINITY ? 1.f : ex2_approx(m0 - m1);
             zn[nt][e] = SHIFT - m1;
             sum[nt][e] *= f;
 #pragma unroll
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(32 * W, W == WARPS ? Shape<NT>::CTAS : 1)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int seen = min(max(lim[nt][e] - tok0, 0), TOK);
+                const int seen = min(max(lim(nt, e) - tok0, 0), TOK);
                 if (nans & ((1u << seen) - 1u)) {
 #pragma unroll
                   for (int mt = 0; mt < MT; ++mt)
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(32 * W, W == WARPS ? Shape<NT>::CTAS : 1)
         l += __shfl_xor_sync(0xffffffffu, l, 4);
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (g == 0) sh_ml[warp][nt * 8 + 2 * c + e] = make_float2(ref[nt][e], l);
+        if (g == 0) sh_ml[warp][nt * 8 + 2 * c + e] = make_float2(SHIFT - zn[nt][e], l);
       }
     __syncthreads();  // also: every warp is done with its ring, which the sums reuse
     float* merge = reinterpret_cast<float*>(ring);
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(32 * W, W == WARPS ? Shape<NT>::CTAS : 1)
         float m = sh_ml[0][r].x;
 #pragma unroll
         for (int w = 1; w < WARPS; ++w) m = fmaxf(m, sh_ml[w][r].x);
-        const float f = m == -INFINITY ? 1.f : ex2_approx(ref[nt][e] - m);
+        const float f = m == -INFINITY ? 1.f : ex2_approx(SHIFT - zn[nt][e] - m);
         float* dst = merge + (warp * ROWS + r) * MERGE_ROW<D>;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
