@@ -18,9 +18,9 @@
 // keys pair neighbours of one token, values pair two tokens by merging nibbles.
 //
 // Work split.  A segment is one (sequence, KV head, row tile).  Where it is
-// short by the caller's bound, a cluster of up to eight CTAs (of four warps, or
-// sixteen where segments are few) shares it and joins its sums through
-// distributed shared memory: one launch, no workspace.
+// short by the caller's bound, a CTA (of two, four or sixteen warps, the fewer the
+// more segments there are) takes it, or a cluster of up to eight, which joins its
+// sums through distributed shared memory: one launch, no workspace.
 // Longer ones are counted in units of 64 tokens; the units of all segments form
 // one line, which is cut into equal pieces, one per CTA, from the lengths on the
 // device.  Long and short sequences balance without the host knowing them, and a
@@ -62,6 +62,8 @@ constexpr int JOIN_ROWS_PARTS = 8;  // a warp to a row below, a block above
 constexpr int MAX_PARTS = 768;      // parts of a segment, at most: CTAs of a cut call
 constexpr int MAX_CLUSTER = 8;      // CTAs that share a segment, at most
 constexpr int CLUSTER_UNITS = 16;   // units of a segment per CTA of a cluster, at most
+constexpr int SMALL_WARPS = 2;      // warps of a CTA where there are many segments
+constexpr int SMALL_UNITS = 32;     // units of a segment per CTA of that size, at most
 constexpr int WIDE_WARPS = 16;      // warps of a CTA where there are few segments
 constexpr int WIDE_GRID = 152;      // CTAs of that size: the GPU's SMs
 constexpr int WIDE_GRID_OF_8 = 64;  // ... in clusters of eight
@@ -243,7 +245,7 @@ __device__ __forceinline__ void store_row4(const DecArgs& a, int b, int kvh, int
 // DENSE: the tokens of a page lie together in each pool, so that the strides of
 // the copies are constants.
 template <int D, int NT, bool DENSE, int W>
-__global__ void __launch_bounds__(32 * W, W == WARPS ? Shape<NT>::CTAS : 1)
+__global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NT>::CTAS * WARPS / W : 1)
     decode4_kernel(const DecArgs a) {
   constexpr int WARPS = W, THREADS = 32 * W;  // of this CTA
   constexpr int UNIT_TILES = UNIT / TOK;
@@ -906,9 +908,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) decode4_join_rows_kernel(const D
 // Query row tiles of a call: as few tensor-core columns as hold its rows, up
 // to 32 to a CTA, and equal shares where one CTA does not hold them.
 struct Plan {
-  int nt, row_tiles, units, max_grid, cluster;
+  int nt, row_tiles, units, max_grid, warps, cluster;
   long long segments, all_units;
-  bool split, wide;
+  bool split;
 };
 
 Plan plan_of(const bsfa_cache4* c, const bsfa_decode4_params* p) {
@@ -926,25 +928,35 @@ Plan plan_of(const bsfa_cache4* c, const bsfa_decode4_params* p) {
   pl.max_grid = grids[pl.nt - 1];
   // Few segments, of half a thousand tokens or more: a CTA of 16 warps to an SM
   // (19 ragged sequences to 1024: 13.8 -> 9.5 us; 1 x 4097: 9.4 -> 8.8; 1 x 300
-  // would go from 6.6 to 7.1).  Otherwise CTAs of four.  As many CTAs to a segment
-  // as keep them all resident at once, eight wide ones only up to 64 in all (2 x
+  // would go from 6.6 to 7.1).  Otherwise CTAs of four, or where those would not
+  // all be resident at once of two (256 ragged sequences to 128, 8 heads: 21.3 ->
+  // 16.0 us; 128 to 512: 21.6 -> 17.9; of one: 17.9, 18.1).  As many CTAs of four or
+  // more to a segment as keep them all resident at once, eight wide ones only up to 64 in all (2 x
   // 16K, 128 of them: 27 us, cut 19): a cluster lies within one GPC.
-  pl.wide = pl.nt == 1 && pl.segments <= WIDE_GRID && pl.units >= WIDE_LEAST;
+  pl.warps = WARPS;
+  if (pl.nt == 1) {
+    if (pl.segments <= WIDE_GRID && pl.units >= WIDE_LEAST)
+      pl.warps = WIDE_WARPS;
+    else if (pl.segments > pl.max_grid)
+      pl.warps = SMALL_WARPS;
+  }
   pl.cluster = 1;
-  while (pl.cluster < MAX_CLUSTER && pl.units >= 2 * pl.cluster) {
+  while (pl.warps >= WARPS && pl.cluster < MAX_CLUSTER && pl.units >= 2 * pl.cluster) {
     const int next = 2 * pl.cluster;
-    const int resident = !pl.wide ? pl.max_grid : next == MAX_CLUSTER ? WIDE_GRID_OF_8 : WIDE_GRID;
+    const int resident = pl.warps == WARPS       ? pl.max_grid
+                         : next == MAX_CLUSTER ? WIDE_GRID_OF_8
+                                                 : WIDE_GRID;
     if (pl.segments * next > resident) break;
     pl.cluster = next;
   }
   // Longer segments are cut.  Wide CTAs stay ahead of the cut for twice as long
   // where they fill more than half of the GPU (4 x 16K: 21.8 and 24.4 us, 1 x 32K:
   // 20.5 and 18.8).
-  const int most = !pl.wide                                        ? CLUSTER_UNITS
-                   : 2 * pl.segments * pl.cluster > WIDE_GRID ? 2 * WIDE_UNITS
-                                                                   : WIDE_UNITS;
+  int most = pl.warps == SMALL_WARPS ? SMALL_UNITS : CLUSTER_UNITS;
+  if (pl.warps == WIDE_WARPS)
+    most = 2 * pl.segments * pl.cluster > WIDE_GRID ? 2 * WIDE_UNITS : WIDE_UNITS;
   pl.split = pl.units > most * pl.cluster;
-  if (pl.split) pl.cluster = 1;
+  if (pl.split) pl.cluster = 1, pl.warps = WARPS;
   return pl;
 }
 
@@ -1009,7 +1021,7 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
     return cudaLaunchKernelEx(&cfg, decode4_kernel<D, NT, DENSE, W>, args) == cudaSuccess ? BSFA_OK
                                                                              : BSFA_ERR_CUDA;
   }
-  if constexpr (W == WARPS) {  // CTAs of WIDE_WARPS never cut
+  if constexpr (W == WARPS) {  // other CTAs never cut
     const long long full = static_cast<long long>(sms) * Shape<NT>::CTAS;
     long long grid = full < pl.max_grid ? full : pl.max_grid;
     const long long most = (pl.all_units + MIN_UNITS - 1) / MIN_UNITS;
@@ -1127,17 +1139,15 @@ bsfa_status bsfa_decode4(const bsfa_cache4* cache, const bsfa_decode4_params* p,
   const bool dense = cache->k_stride[2] == row && cache->v_stride[2] == row &&
                      cache->k_scale_stride[2] == z && cache->v_scale_stride[2] == z;
   using Launch = bsfa_status (*)(const DecArgs&, const Plan&, int, int, cudaStream_t);
-  static const Launch launches[2][2][5] = {
-      // [d = 128][dense][tiles of 8 query rows - 1, or one tile and wide CTAs]
-      {{launch<64, 1, false>, launch<64, 2, false>, launch<64, 3, false>, launch<64, 4, false>,
-        launch<64, 1, false, WIDE_WARPS>},
-       {launch<64, 1, true>, launch<64, 2, true>, launch<64, 3, true>, launch<64, 4, true>,
-        launch<64, 1, true, WIDE_WARPS>}},
-      {{launch<128, 1, false>, launch<128, 2, false>, launch<128, 3, false>,
-        launch<128, 4, false>, launch<128, 1, false, WIDE_WARPS>},
-       {launch<128, 1, true>, launch<128, 2, true>, launch<128, 3, true>, launch<128, 4, true>,
-        launch<128, 1, true, WIDE_WARPS>}}};
-  const int which = pl.wide && !pl.split ? 4 : pl.nt - 1;
+#define BSFA_LAUNCHES(D, DENSE)                                                          \
+  {launch<D, 1, DENSE>, launch<D, 2, DENSE>, launch<D, 3, DENSE>, launch<D, 4, DENSE>,   \
+   launch<D, 1, DENSE, SMALL_WARPS>, launch<D, 1, DENSE, WIDE_WARPS>}
+  static const Launch launches[2][2][6] = {
+      // [d = 128][dense][tiles of 8 query rows - 1, or one tile and small or wide CTAs]
+      {BSFA_LAUNCHES(64, false), BSFA_LAUNCHES(64, true)},
+      {BSFA_LAUNCHES(128, false), BSFA_LAUNCHES(128, true)}};
+#undef BSFA_LAUNCHES
+  const int which = pl.warps == WARPS ? pl.nt - 1 : pl.warps == SMALL_WARPS ? 4 : 5;
   return launches[cache->head_dim == 128][dense][which](a, pl, sms, dev, stream);
 }
 
