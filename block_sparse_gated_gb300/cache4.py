@@ -191,12 +191,15 @@ def _call(fn, device, stream, *args):
         _check(status, fn.__name__)
 
 
-def _made_here(stream, device, *tensors):
-    """Tensors allocated by a call that runs on ``stream``: their memory must
-    not be handed out again before that stream is done with it."""
-    if stream != torch.cuda.current_stream(device):
-        for t in tensors:
-            t.record_stream(stream)
+def _empty(stream, device, shape, dtype):
+    """A tensor for a call on ``stream``: memory that this stream may write at
+    once, and that is not handed out again while the caller's stream reads it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def cache4_write(cache: KVCache4, k, v, block_table, *, start=None, cu_seqlens=None, layout=None,
@@ -249,10 +252,8 @@ def cache4_read(cache: KVCache4, block_table, *, seqlen=None, total=None, start=
             raise ValueError(layout)
         if dtype not in _DTYPES:
             raise TypeError("expected bfloat16 or float16")
-        k = torch.empty(shape, dtype=dtype, device=dev)
-        v = torch.empty(shape, dtype=dtype, device=dev)
-        if stream is not None:
-            _made_here(stream, dev, k, v)
+        k = _empty(stream, dev, shape, dtype)
+        v = _empty(stream, dev, shape, dtype)
     else:
         k, v = out
     r, batch = _rows_fields(k, v, layout, cu_seqlens, start, heads, d, dev)
@@ -261,8 +262,8 @@ def cache4_read(cache: KVCache4, block_table, *, seqlen=None, total=None, start=
     return k, v
 
 
-def _decode_fields(q, cache, block_table, seqlens, out, device, *, layout, max_seqlen, softmax_scale,
-                   causal, lse=0):
+def _decode_fields(q, cache, block_table, seqlens, out, device, *, layout, max_seqlen,
+                   softmax_scale, causal, lse=0):
     """The packed bsfa_cache4 of a decode call, and a function of a workspace's
     address and size that gives its packed bsfa_decode4_params."""
     if layout is None:
@@ -305,21 +306,19 @@ def decode4(q, cache: KVCache4, block_table, seqlens, *, max_seqlen=None, softma
     ``workspace``: at least ``decode4_workspace_bytes`` of device memory (0 where
     the lengths' bound and the batch are small), not shared by calls that may
     overlap (default: allocated for the call)."""
-    made = []
-    if out is None:
-        out = torch.empty_like(q)
-        made.append(out)
     dev = q.device
-    if dev.type != "cuda" or not out.get_device() == seqlens.get_device() == dev.index or \
+    if dev.type != "cuda" or not seqlens.get_device() == dev.index or \
+            out is not None and out.device != dev or \
             workspace is not None and workspace.device != dev:
         _on_device(dev, out=out, seqlens=seqlens, workspace=workspace)
+    if out is None:
+        out = torch.empty_like(q) if stream is None else _empty(stream, dev, q.shape, q.dtype)
     res = {"out": out}
     lse = 0
     if return_lse:
         _, hq, n = _strides_bhtd(q, layout or "bhld", False)
         rows = n if q.dim() == 3 else q.shape[0] * n
-        res["lse"] = torch.empty((hq, rows), dtype=torch.float32, device=dev)
-        made.append(res["lse"])
+        res["lse"] = _empty(stream, dev, (hq, rows), torch.float32)
         lse = res["lse"].data_ptr()
     c, fields = _decode_fields(q, cache, block_table, seqlens, out, dev, layout=layout,
                                max_seqlen=max_seqlen, softmax_scale=softmax_scale, causal=causal,
@@ -327,12 +326,9 @@ def decode4(q, cache: KVCache4, block_table, seqlens, *, max_seqlen=None, softma
     if workspace is None:
         need = _native.lib().bsfa_decode4_workspace_size(c, fields(0, 0))
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            made.append(workspace)
+            workspace = _empty(stream, dev, (need,), torch.uint8)
     elif not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous")
-    if stream is not None:
-        _made_here(stream, dev, *made)
     _call(_native.lib().bsfa_decode4, dev, stream, c,
           fields(0, 0) if workspace is None else fields(workspace.data_ptr(), _nbytes(workspace)))
     return res

@@ -20,8 +20,9 @@ namespace bsfa {
 namespace {
 
 constexpr int THREADS = 128;
-constexpr int AHEAD = 4;  // heads whose loads a thread issues at once (128K tokens written and read: 207.7,
-                          // 211.0, 205.7 us at 1, 2, 4)
+// Heads whose loads a thread issues at once (128K tokens written and read: 207.7,
+// 211.0, 205.7 us at 1, 2, 4).
+constexpr int AHEAD = 4;
 
 struct RowsArgs {
   const uint8_t *kc, *vc, *ks, *vs;  // written by the write, read by the read
@@ -365,7 +366,9 @@ bsfa_status validate_cache4_pointers(const bsfa_cache4* c) {
       return BSFA_ERR_UNSUPPORTED;
     // The attention kernel's address arithmetic: page strides below 2^34 bytes,
     // offsets within a page below 2^31.
-    const int64_t most = i == 0 ? (1LL << 34) - 1 : i == 2 ? 0x7fffffffLL / c->page_size : INT64_MAX;
+    const int64_t most = i == 0   ? (1LL << 34) - 1
+                         : i == 2 ? 0x7fffffffLL / c->page_size
+                                  : INT64_MAX;
     if (c->k_stride[i] > most || c->v_stride[i] > most || c->k_scale_stride[i] > most ||
         c->v_scale_stride[i] > most)
       return BSFA_ERR_UNSUPPORTED;

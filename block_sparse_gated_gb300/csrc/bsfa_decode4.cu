@@ -930,9 +930,10 @@ Plan plan_of(const bsfa_cache4* c, const bsfa_decode4_params* p) {
   // (19 ragged sequences to 1024: 13.8 -> 9.5 us; 1 x 4097: 9.4 -> 8.8; 1 x 300
   // would go from 6.6 to 7.1).  Otherwise CTAs of four, or where those would not
   // all be resident at once of two (256 ragged sequences to 128, 8 heads: 21.3 ->
-  // 16.0 us; 128 to 512: 21.6 -> 17.9; of one: 17.9, 18.1).  As many CTAs of four or
-  // more to a segment as keep them all resident at once, eight wide ones only up to 64 in all (2 x
-  // 16K, 128 of them: 27 us, cut 19): a cluster lies within one GPC.
+  // 16.0 us; 128 to 512: 21.6 -> 17.9; of one: 17.9, 18.1).
+  // Of CTAs of four and sixteen a segment gets as many as keep them all resident
+  // at once; eight of sixteen only up to 64 CTAs in all (2 x 16K, 128 of them: 27
+  // us, cut 19), since a cluster lies within one GPC.
   pl.warps = WARPS;
   if (pl.nt == 1) {
     if (pl.segments <= WIDE_GRID && pl.units >= WIDE_LEAST)
@@ -1001,8 +1002,8 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
   static std::atomic<uint64_t> ready{0};
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    if (cudaFuncSetAttribute(decode4_kernel<D, NT, DENSE, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smem) != cudaSuccess)
+    if (cudaFuncSetAttribute(decode4_kernel<D, NT, DENSE, W>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
       return BSFA_ERR_CUDA;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
@@ -1018,8 +1019,8 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode4_kernel<D, NT, DENSE, W>, args) == cudaSuccess ? BSFA_OK
-                                                                             : BSFA_ERR_CUDA;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, decode4_kernel<D, NT, DENSE, W>, args);
+    return e == cudaSuccess ? BSFA_OK : BSFA_ERR_CUDA;
   }
   if constexpr (W == WARPS) {  // other CTAs never cut
     const long long full = static_cast<long long>(sms) * Shape<NT>::CTAS;

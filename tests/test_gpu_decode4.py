@@ -302,6 +302,30 @@ def test_graphs_follow_the_lengths_and_streams_do_not_mix(cuda_device, cut):
     assert torch.equal(r["out"], outs[0])
 
 
+def test_results_on_another_stream_have_memory_of_their_own(cuda_device):
+    """Memory that the current stream has given back but still writes is not what
+    a call on another stream returns its results in."""
+    b = _bsfa()
+    cache, table, rows = cu.random_cache(b, [500], 32, 2, 128, 9, cuda_device)
+    q = _queries(1, 8, 1, 128, BF, 9, cuda_device)
+    n32 = _i32([500], cuda_device)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        old = [torch.empty_like(q), torch.empty(1, 2, 500, 128, dtype=BF, device=cuda_device),
+               torch.empty(1, 2, 500, 128, dtype=BF, device=cuda_device)]
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+        for t in old:
+            t.fill_(7.0)
+        del old, t
+        r = b.decode4(q, cache, table, n32, stream=side, return_lse=True)
+        k, v = b.cache4_read(cache, table, seqlen=500, stream=side)
+        torch.cuda.synchronize()
+        cu.check_decode(r, q, rows, [500], BF, 128)
+        assert np.array_equal(k[0].cpu().double().numpy(), rows[0][0])
+        assert np.array_equal(v[0].cpu().double().numpy(), rows[0][1])
+
+
 @pytest.mark.parametrize("cut", [True, False])
 def test_a_batch_of_many_short_and_one_long(cuda_device, cut):
     """300 sequences, many of them in one piece and one over many pieces."""
