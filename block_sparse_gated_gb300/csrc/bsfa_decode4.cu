@@ -70,13 +70,22 @@ constexpr int WIDE_GRID_OF_8 = 64;  // ... in clusters of eight
 constexpr int WIDE_LEAST = 8;       // units of a segment worth one
 constexpr int WIDE_UNITS = 32;      // units of a segment per CTA of that size, at most
 
-// Per row-tile width (NT tiles of 8 query rows): CTAs per SM, ring stages,
+// Query rows of a CTA: NT tiles of 8, or four (NT = 0, "half": see the values'
+// product).
+constexpr int rows_of(int nt) { return nt == 0 ? 4 : 8 * nt; }
+
+// Per row-tile width: CTAs per SM, ring stages,
 // whether the main loop goes around the ring in one piece (64 ragged sequences
 // to 16K, NT = 1: 121 us by single tiles, 118 unrolled with 5 stages, 115 with 4;
 // five tokens over 16 to 32K, NT = 3: 133 and 141), and the most CTAs a launch
 // has (the workspace holds two partial results each).
 template <int NT>
 struct Shape;
+template <>
+struct Shape<0> {
+  static constexpr int CTAS = 4, STAGES = 4, MAX_GRID = 640;
+  static constexpr bool UNROLL = true;
+};
 template <>
 struct Shape<1> {
   static constexpr int CTAS = 4, STAGES = 4, MAX_GRID = 640;
@@ -115,8 +124,8 @@ struct DecArgs {
   float sigma_log2;
   float* lse;
   long long lse_pitch;
-  float* part_o;    // [grid][2][8 * NT][d]
-  float2* part_ml;  // [grid][2][8 * NT]
+  float* part_o;    // [grid][2][rows of a CTA][d]
+  float2* part_ml;  // [grid][2][rows of a CTA]
   int4* joins;      // [jobs]: {sequence, kvh * row_tiles + row tile, first, last CTA}, or x < 0
 };
 
@@ -164,12 +173,12 @@ constexpr int MERGE_ROW = D + 12;
 template <int D, int NT, int W>
 constexpr int ring_bytes() {
   constexpr int ring = W * Shape<NT>::STAGES * Stage<D>::BYTES;
-  constexpr int merge = W * MERGE_ROW<D> * 8 * NT * 4;
+  constexpr int merge = W * MERGE_ROW<D> * rows_of(NT) * 4;
   return ring > merge ? ring : merge;
 }
 template <int D, int NT, int W>
 constexpr int smem_bytes(bool cluster) {
-  return ring_bytes<D, NT, W>() + (cluster ? 8 * NT * D * 4 : 0);
+  return ring_bytes<D, NT, W>() + (cluster ? rows_of(NT) * D * 4 : 0);
 }
 
 // Where a CTA's piece of the line begins.
@@ -244,15 +253,18 @@ __device__ __forceinline__ void store_row4(const DecArgs& a, int b, int kvh, int
 
 // DENSE: the tokens of a page lie together in each pool, so that the strides of
 // the copies are constants.
-template <int D, int NT, bool DENSE, int W>
-__global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NT>::CTAS * WARPS / W : 1)
+template <int D, int NTILES, bool DENSE, int W>
+__global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WARPS / W : 1)
     decode4_kernel(const DecArgs a) {
+  constexpr bool HALF = NTILES == 0;
+  constexpr int NT = HALF ? 1 : NTILES;       // tiles of 8 product columns
+  constexpr int COLS = HALF ? 1 : 2;          // query rows of a lane in each
   constexpr int WARPS = W, THREADS = 32 * W;  // of this CTA
   constexpr int UNIT_TILES = UNIT / TOK;
-  constexpr int STAGES = Shape<NT>::STAGES;
-  constexpr int KSTEPS = D / 16;  // 16-element steps of K Q^T
-  constexpr int MT = D / 16;      // 16-element row tiles of V^T P^T
-  constexpr int ROWS = 8 * NT;
+  constexpr int STAGES = Shape<NTILES>::STAGES;
+  constexpr int KSTEPS = D / 16;              // 16-element steps of K Q^T
+  constexpr int MT = HALF ? D / 32 : D / 16;  // 16-row tiles of V^T P^T
+  constexpr int ROWS = rows_of(NTILES);
   using St = Stage<D>;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ int sh_cut[WARPS + 2];
@@ -264,6 +276,9 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NT>::CTAS * WARPS /
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
+  // The query row (of the CTA's) of this lane's column e of tile nt, 2c + e of the
+  // tile's 8; where the rows are four, each takes two columns.
+  auto col_row = [&](int nt, int e) { return HALF ? c : nt * 8 + 2 * c + e; };
 
   if (a.cluster > 1) cluster_arrive();
   Piece piece;
@@ -368,7 +383,7 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NT>::CTAS * WARPS /
     // ---- queries: fragments of Q^T (fp16, row scaled to [2^14, 2^15)) and the
     // factor that turns a product into a score in log2 units
     for (int nt = warp; nt < NT; nt += WARPS) {
-      const int r = r0 + nt * 8 + g;
+      const int q_row = HALF ? g >> 1 : nt * 8 + g, r = r0 + q_row;
       float f[D / 4];
       float amax = 0.f;
 #pragma unroll
@@ -398,9 +413,9 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NT>::CTAS * WARPS /
       const int up = amax == 0.f || ex > 127 ? 0 : min(14 - ex, 100);
       const float mul = pow2f(up);
       if (c == 0) {
-        sh_sc[nt * 8 + g] = a.sigma_log2 * pow2f(-up) * pow2f(head_exp(a.kexp, kvh));
+        sh_sc[q_row] = a.sigma_log2 * pow2f(-up) * pow2f(head_exp(a.kexp, kvh));
         // Rows past the last are computed along with the rest and not stored.
-        sh_lim[nt * 8 + g] = !a.causal || r >= a.rows ? len : len - a.q_len + r / a.group + 1;
+        sh_lim[q_row] = !a.causal || r >= a.rows ? len : len - a.q_len + r / a.group + 1;
       }
 #pragma unroll
       for (int j = 0; j < KSTEPS; ++j)
@@ -412,8 +427,8 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NT>::CTAS * WARPS /
 
     // ---- per-lane columns: 2c and 2c + 1 of each row tile
     float acc[NT][MT][4];
-    float sum[NT][2], sc[NT][2];
-    float zn[NT][2];  // SHIFT - reference: a weight is 2^(sc * product + zn)
+    float sum[NT][COLS], sc[NT][COLS];
+    float zn[NT][COLS];  // SHIFT - reference: a weight is 2^(sc * product + zn)
     uint2 qf[NT == 1 ? KSTEPS : 1];  // one row tile's queries stay in registers
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -422,10 +437,10 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NT>::CTAS * WARPS /
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[nt][mt][e] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < COLS; ++e) {
         zn[nt][e] = INFINITY;
         sum[nt][e] = 0.f;
-        sc[nt][e] = sh_sc[nt * 8 + 2 * c + e];
+        sc[nt][e] = sh_sc[col_row(nt, e)];
       }
     }
     if constexpr (NT == 1) {
@@ -512,15 +527,16 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NT>::CTAS * WARPS /
 
       // ---- weights; the reference moves where one would pass 2^(SHIFT + HEADROOM)
       float y[NT][4];
-      auto lim = [&](int nt, int e) { return sh_lim[nt * 8 + 2 * c + e]; };
+      auto lim = [&](int nt, int e) { return sh_lim[col_row(nt, e)]; };
       auto weigh = [&]() {
         bool over = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            y[nt][e] = fmaf(s[nt][e], sc[nt][e & 1], zn[nt][e & 1]);
-            if (MASKED && tok0 + my_tok + (e & 2) * 4 >= lim(nt, e & 1)) y[nt][e] = -INFINITY;
+          for (int e = 0; e < 4; e += 3 - COLS) {  // a half tile's odd columns repeat the even
+            const int col = HALF ? 0 : e & 1;
+            y[nt][e] = fmaf(s[nt][e], sc[nt][col], zn[nt][col]);
+            if (MASKED && tok0 + my_tok + (e & 2) * 4 >= lim(nt, col)) y[nt][e] = -INFINITY;
             over |= y[nt][e] > SHIFT + HEADROOM;
           }
         return over;
@@ -529,7 +545,7 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NT>::CTAS * WARPS /
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int e = 0; e < COLS; ++e) {
             float lo = s[nt][e] * sc[nt][e], hi = s[nt][e + 2] * sc[nt][e];
             if (MASKED) {
               if (tok0 + my_tok >= lim(nt, e)) lo = -INFINITY;
@@ -547,6 +563,10 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NT>::CTAS * WARPS /
             for (int mt = 0; mt < MT; ++mt) {
               acc[nt][mt][e] *= f;
               acc[nt][mt][e + 2] *= f;
+              if constexpr (HALF) {
+                acc[nt][mt][1] *= f;
+                acc[nt][mt][3] *= f;
+              }
             }
           }
         weigh();
@@ -555,12 +575,12 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NT>::CTAS * WARPS /
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 4; e += 3 - COLS) {
           y[nt][e] = ex2_approx(y[nt][e]);
-          sum[nt][e & 1] += y[nt][e];
+          sum[nt][HALF ? 0 : e & 1] += y[nt][e];
         }
-        pb[nt][0] = movmatrix_trans(pack_f16x2(y[nt][0], y[nt][1]));
-        pb[nt][1] = movmatrix_trans(pack_f16x2(y[nt][2], y[nt][3]));
+        pb[nt][0] = movmatrix_trans(pack_f16x2(y[nt][0], y[nt][HALF ? 0 : 1]));
+        pb[nt][1] = movmatrix_trans(pack_f16x2(y[nt][2], y[nt][HALF ? 2 : 3]));
       }
 
       // ---- O^T += V^T P^T; this lane: elements [g d/8, (g + 1) d/8) of tokens c + 4j
@@ -608,27 +628,58 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NT>::CTAS * WARPS /
               }
           }
         }
-        const uint32_t z01 = e4m3x2_to_f16(z[0] | z[1] << 8);
-        const uint32_t z23 = e4m3x2_to_f16(z[2] | z[3] << 8);
+        if constexpr (HALF) {
+          // Neighbouring elements of a value stay paired: the rows of a product are
+          // such pairs, its inner index is (token, which of the two), and column
+          // 2r + p weighs query row r for the elements p of the pairs, with zeros at
+          // the others.  No nibbles are merged, the columns that four rows leave
+          // idle carry the second elements, and the products are as many.
+          // After the transposition a lane of column g holds the weights of tokens
+          // val_tok(0), val_tok(1) (and 2, 3) for row g / 2.
+          const uint32_t first = g & 1 ? 0x1044u : 0x4410u, second = g & 1 ? 0x3244u : 0x4432u;
+          uint32_t zz[4];
 #pragma unroll
-        for (int w = 0; w < D / 64; ++w) {
-          // f16x2 fragments want {token 4j', token 4j' + 4} of one element.
-          const uint32_t even01 = select_low_nibbles(v[0][w], v[1][w] << 4);
-          const uint32_t odd01 = select_low_nibbles(v[0][w] >> 4, v[1][w]);
-          const uint32_t even23 = select_low_nibbles(v[2][w], v[3][w] << 4);
-          const uint32_t odd23 = select_low_nibbles(v[2][w] >> 4, v[3][w]);
-          uint32_t a0[4], a1[4], a2[4], a3[4];
-          e2m1x8_to_f16(even01, a0);
-          e2m1x8_to_f16(odd01, a1);
-          e2m1x8_to_f16(even23, a2);
-          e2m1x8_to_f16(odd23, a3);
+          for (int j = 0; j < 4; ++j) zz[j] = e4m3x2_to_f16(z[j] * 0x101u);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t x0 = mul_f16x2(a0[j], z01), x1 = mul_f16x2(a1[j], z01);
-            const uint32_t x2 = mul_f16x2(a2[j], z23), x3 = mul_f16x2(a3[j], z23);
+          for (int step = 0; step < 2; ++step) {
+            const uint32_t b0 = __byte_perm(pb[0][step], 0, first);
+            const uint32_t b1 = __byte_perm(pb[0][step], 0, second);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_f16_16816(acc[nt][4 * w + j], x0, x1, x2, x3, pb[nt][0], pb[nt][1]);
+            for (int w = 0; w < D / 64; ++w) {
+              uint32_t lo[4], hi[4];
+              e2m1x8_to_f16(v[2 * step][w], lo);
+              e2m1x8_to_f16(v[2 * step + 1][w], hi);
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                mma_f16_16816(acc[0][2 * w + j], mul_f16x2(lo[2 * j], zz[2 * step]),
+                              mul_f16x2(lo[2 * j + 1], zz[2 * step]),
+                              mul_f16x2(hi[2 * j], zz[2 * step + 1]),
+                              mul_f16x2(hi[2 * j + 1], zz[2 * step + 1]), b0, b1);
+            }
+          }
+        } else {
+          const uint32_t z01 = e4m3x2_to_f16(z[0] | z[1] << 8);
+          const uint32_t z23 = e4m3x2_to_f16(z[2] | z[3] << 8);
+#pragma unroll
+          for (int w = 0; w < D / 64; ++w) {
+            // f16x2 fragments want {token 4j', token 4j' + 4} of one element.
+            const uint32_t even01 = select_low_nibbles(v[0][w], v[1][w] << 4);
+            const uint32_t odd01 = select_low_nibbles(v[0][w] >> 4, v[1][w]);
+            const uint32_t even23 = select_low_nibbles(v[2][w], v[3][w] << 4);
+            const uint32_t odd23 = select_low_nibbles(v[2][w] >> 4, v[3][w]);
+            uint32_t a0[4], a1[4], a2[4], a3[4];
+            e2m1x8_to_f16(even01, a0);
+            e2m1x8_to_f16(odd01, a1);
+            e2m1x8_to_f16(even23, a2);
+            e2m1x8_to_f16(odd23, a3);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t x0 = mul_f16x2(a0[j], z01), x1 = mul_f16x2(a1[j], z01);
+              const uint32_t x2 = mul_f16x2(a2[j], z23), x3 = mul_f16x2(a3[j], z23);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16_16816(acc[nt][4 * w + j], x0, x1, x2, x3, pb[nt][0], pb[nt][1]);
+            }
           }
         }
       }
@@ -650,7 +701,7 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NT>::CTAS * WARPS /
     // sums between registers at every join of the two).
     const int t_full = max(t_begin, min(t_end, min_lim / TOK));
     int t = t_begin;
-    if constexpr (Shape<NT>::UNROLL) {  // the ring once around, its places constants
+    if constexpr (Shape<NTILES>::UNROLL) {  // the ring once around, its places constants
       for (; t + STAGES <= t_full; t += STAGES) {
 #pragma unroll
         for (int x = 0; x < STAGES; ++x) {
@@ -669,20 +720,20 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NT>::CTAS * WARPS /
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < COLS; ++e) {
         float l = sum[nt][e];
         l += __shfl_xor_sync(0xffffffffu, l, 4);
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (g == 0) sh_ml[warp][nt * 8 + 2 * c + e] = make_float2(SHIFT - zn[nt][e], l);
+        if (g == 0) sh_ml[warp][col_row(nt, e)] = make_float2(SHIFT - zn[nt][e], l);
       }
     __syncthreads();  // also: every warp is done with its ring, which the sums reuse
     float* merge = reinterpret_cast<float*>(ring);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = nt * 8 + 2 * c + e;
+      for (int e = 0; e < COLS; ++e) {
+        const int r = col_row(nt, e);
         float m = sh_ml[0][r].x;
 #pragma unroll
         for (int w = 1; w < WARPS; ++w) m = fmaxf(m, sh_ml[w][r].x);
@@ -690,8 +741,14 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NT>::CTAS * WARPS /
         float* dst = merge + (warp * ROWS + r) * MERGE_ROW<D>;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          dst[merge_pos<D>(g * (D / 8) + 2 * mt)] = acc[nt][mt][e] * f;
-          dst[merge_pos<D>(g * (D / 8) + 2 * mt + 1)] = acc[nt][mt][e + 2] * f;
+          if constexpr (HALF) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              dst[merge_pos<D>(g * (D / 8) + 4 * mt + x)] = acc[nt][mt][x] * f;
+          } else {
+            dst[merge_pos<D>(g * (D / 8) + 2 * mt)] = acc[nt][mt][e] * f;
+            dst[merge_pos<D>(g * (D / 8) + 2 * mt + 1)] = acc[nt][mt][e + 2] * f;
+          }
         }
       }
     __syncthreads();
@@ -702,7 +759,7 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NT>::CTAS * WARPS /
       // CTAs in order.  (Sums left in place and read remotely need a second
       // barrier and wait for the loads: 8 x 2K tokens 10.8 us, pushed 10.3.)
       const int items = ROWS * (D / 4) / a.cluster;  // the cluster is a power of two
-      const uint32_t rank = cluster_rank(), got = smem_u32(ring) + ring_bytes<D, NT, W>();
+      const uint32_t rank = cluster_rank(), got = smem_u32(ring) + ring_bytes<D, NTILES, W>();
       cluster_wait();  // the one of the kernel's beginning: every CTA runs
       for (int x = tid; x < n_rows * (D / 4); x += THREADS) {
         const int r = x / (D / 4), d0 = (x % (D / 4)) * 4;
@@ -730,7 +787,7 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NT>::CTAS * WARPS /
       cluster_arrive();
       cluster_wait();
       const float4* parts =
-          reinterpret_cast<const float4*>(ring + ring_bytes<D, NT, W>());
+          reinterpret_cast<const float4*>(ring + ring_bytes<D, NTILES, W>());
       for (int k = tid; k * a.cluster + rank < n_rows * (D / 4); k += THREADS) {
         const int x = k * a.cluster + rank, r = x / (D / 4), d0 = (x % (D / 4)) * 4;
         float m = sh_cluster[0][r].x;
@@ -936,9 +993,10 @@ Plan plan_of(const bsfa_cache4* c, const bsfa_decode4_params* p) {
   if (pl.units < 1) pl.units = 1;
   pl.segments = static_cast<long long>(p->batch) * c->num_heads_kv * pl.row_tiles;
   pl.all_units = pl.segments * (pl.units + SEGMENT_UNITS);
-  constexpr int grids[4] = {Shape<1>::MAX_GRID, Shape<2>::MAX_GRID, Shape<3>::MAX_GRID,
-                            Shape<4>::MAX_GRID};
-  pl.max_grid = grids[pl.nt - 1];
+  if (rows <= 4) pl.nt = 0;
+  constexpr int grids[5] = {Shape<0>::MAX_GRID, Shape<1>::MAX_GRID, Shape<2>::MAX_GRID,
+                            Shape<3>::MAX_GRID, Shape<4>::MAX_GRID};
+  pl.max_grid = grids[pl.nt];
   // Few segments, of half a thousand tokens or more: a CTA of 16 warps to an SM
   // (19 ragged sequences to 1024: 13.8 -> 9.5 us; 1 x 4097: 9.4 -> 8.8; 1 x 300
   // would go from 6.6 to 7.1).  Otherwise CTAs of four, or where those would not
@@ -948,7 +1006,7 @@ Plan plan_of(const bsfa_cache4* c, const bsfa_decode4_params* p) {
   // at once; eight of sixteen only up to 64 CTAs in all (2 x 16K, 128 of them: 27
   // us, cut 19), since a cluster lies within one GPC.
   pl.warps = WARPS;
-  if (pl.nt == 1) {
+  if (pl.nt <= 1) {
     if (pl.segments <= WIDE_GRID && pl.units >= WIDE_LEAST)
       pl.warps = WIDE_WARPS;
     else if (pl.segments > pl.max_grid)
@@ -981,7 +1039,7 @@ struct Carve {
 Carve carve(const Plan& pl, int d) {
   Carve c{};
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t grid = pl.split ? static_cast<size_t>(pl.max_grid) : 0, rows = 8u * pl.nt;
+  const size_t grid = pl.split ? static_cast<size_t>(pl.max_grid) : 0, rows = rows_of(pl.nt);
   c.part_o = 0;
   c.part_ml = up(c.part_o + grid * 2 * rows * d * sizeof(float));
   c.joins = up(c.part_ml + grid * 2 * rows * sizeof(float2));
@@ -1047,7 +1105,8 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
     if (cudaGetLastError() != cudaSuccess) return BSFA_ERR_CUDA;
     // About grid / segments parts to a segment.
     const bool by_rows = grid < JOIN_ROWS_PARTS * pl.segments;
-    const int rows = a.rows < 8 * NT ? a.rows : 8 * NT, per_block = by_rows ? JOIN_THREADS / 32 : 1;
+    constexpr int ROWS = rows_of(NT);
+    const int rows = a.rows < ROWS ? a.rows : ROWS, per_block = by_rows ? JOIN_THREADS / 32 : 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(a.join_by_segment ? pl.segments : grid),
                        (rows + per_block - 1) / per_block);
@@ -1059,8 +1118,8 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     const cudaError_t e =
-        by_rows ? cudaLaunchKernelEx(&cfg, decode4_join_rows_kernel<D, 8 * NT>, a)
-                : cudaLaunchKernelEx(&cfg, decode4_join_kernel<D, 8 * NT>, a);
+        by_rows ? cudaLaunchKernelEx(&cfg, decode4_join_rows_kernel<D, ROWS>, a)
+                : cudaLaunchKernelEx(&cfg, decode4_join_kernel<D, ROWS>, a);
     return e == cudaSuccess ? BSFA_OK : BSFA_ERR_CUDA;
   }
   return BSFA_ERR_CUDA;
@@ -1154,14 +1213,16 @@ bsfa_status bsfa_decode4(const bsfa_cache4* cache, const bsfa_decode4_params* p,
                      cache->k_scale_stride[2] == z && cache->v_scale_stride[2] == z;
   using Launch = bsfa_status (*)(const DecArgs&, const Plan&, int, int, cudaStream_t);
 #define BSFA_LAUNCHES(D, DENSE)                                                          \
-  {launch<D, 1, DENSE>, launch<D, 2, DENSE>, launch<D, 3, DENSE>, launch<D, 4, DENSE>,   \
-   launch<D, 1, DENSE, SMALL_WARPS>, launch<D, 1, DENSE, WIDE_WARPS>}
-  static const Launch launches[2][2][6] = {
-      // [d = 128][dense][tiles of 8 query rows - 1, or one tile and small or wide CTAs]
+  {launch<D, 0, DENSE>,    launch<D, 1, DENSE>, launch<D, 2, DENSE>, launch<D, 3, DENSE>, \
+   launch<D, 4, DENSE>,    launch<D, 0, DENSE, SMALL_WARPS>,                              \
+   launch<D, 1, DENSE, SMALL_WARPS>, launch<D, 0, DENSE, WIDE_WARPS>,                     \
+   launch<D, 1, DENSE, WIDE_WARPS>}
+  static const Launch launches[2][2][9] = {
+      // [d = 128][dense][tiles of 8 query rows (0: half a one), or small or wide CTAs]
       {BSFA_LAUNCHES(64, false), BSFA_LAUNCHES(64, true)},
       {BSFA_LAUNCHES(128, false), BSFA_LAUNCHES(128, true)}};
 #undef BSFA_LAUNCHES
-  const int which = pl.warps == WARPS ? pl.nt - 1 : pl.warps == SMALL_WARPS ? 4 : 5;
+  const int which = pl.nt + (pl.warps == WARPS ? 0 : pl.warps == SMALL_WARPS ? 5 : 7);
   return launches[cache->head_dim == 128][dense][which](a, pl, sms, dev, stream);
 }
 
