@@ -28,12 +28,11 @@
 // partial sums in the workspace, which a second kernel joins in a fixed order.
 //
 // Bound.  144 bytes per (token, KV head) at d = 128 set the floor: 100 cycles of
-// an SM per 16 tokens and head at a copy's rate.  They take 269 issued warp
+// an SM per 16 tokens and head at a copy's rate.  They take about 250 issued warp
 // instructions (64 conversions, 64 fp16x2 products and 16 tensor products among
-// them), 67 cycles at best and 110 as measured: 64 ragged sequences to 16K (633 MB)
-// take 111 us, 5.7 TB/s or 84% of a copy's 6.77.  Each warp streams its own
-// 16-token tiles through a private ring of asynchronous copies; no barrier is met
-// inside a segment.
+// them): 64 ragged sequences to 16K (633 MB) take 104 us, 6.1 TB/s or 90% of a
+// copy's 6.77.  Each warp streams its own 16-token tiles through a private ring of
+// asynchronous copies; no barrier is met inside a segment.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -56,7 +55,7 @@ constexpr int UNIT = TOK * WARPS;   // tokens of a work unit
 constexpr float HEADROOM = 5.f;     // log2 a score may pass the reference by
 constexpr float SHIFT = 10.f;       // log2 of the factor that p carries: p < 2^15
 constexpr int MIN_UNITS = 4;        // shortest piece of the line worth a CTA
-constexpr int SEGMENT_UNITS = 5;    // a segment's fixed cost, in units
+constexpr int SEGMENT_UNITS = 8;    // a segment's fixed cost, in units
 constexpr int JOIN_THREADS = 256;   // of the kernel that joins parts
 constexpr int JOIN_ROWS_PARTS = 8;  // a warp to a row below, a block above
 constexpr int MAX_PARTS = 768;      // parts of a segment, at most: CTAs of a cut call
@@ -135,8 +134,8 @@ __device__ __forceinline__ int clamp_len(const DecArgs& a, int b) {
 }
 // Units of a segment on the line: its tokens', and what a CTA spends on any
 // segment (queries, the first copies' latency, the join of its warps): without it
-// the CTAs with many short sequences end last (64 ragged sequences to 16K: 136 us
-// at 0, 127 at 3, 124 at 5; eight to 64K: 67, 62, 61).
+// the CTAs with many short sequences end last (64 ragged sequences to 16K: 106.2 us
+// at 5, 103.6 at 8, 105.0 at 11; an earlier kernel 136 at 0, 124 at 5).
 __device__ __forceinline__ int units_of(int len) { return SEGMENT_UNITS + (len + UNIT - 1) / UNIT; }
 
 // Byte offset in a warp's stage of row `t` (0..15), 16-byte chunk `c`.  Rows
