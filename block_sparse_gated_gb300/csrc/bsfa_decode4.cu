@@ -15,7 +15,8 @@
 // that a lane owns whole scale groups: of a key it needs d/4 consecutive
 // elements, of a value d/8.  The codes go from shared memory to fragments with
 // one conversion and one product per pair of elements and no transposition:
-// keys pair neighbours of one token, values pair two tokens by merging nibbles.
+// keys pair neighbours of one token, values pair two tokens by merging nibbles
+// (or, where query rows are four at most, neighbours as well: see there).
 //
 // Work split.  A segment is one (sequence, KV head, row tile).  Where it is
 // short by the caller's bound, a CTA (of two, four or sixteen warps, the fewer the
@@ -28,7 +29,7 @@
 // partial sums in the workspace, which a second kernel joins in a fixed order.
 //
 // Bound.  144 bytes per (token, KV head) at d = 128 set the floor: 100 cycles of
-// an SM per 16 tokens and head at a copy's rate.  They take about 250 issued warp
+// an SM per 16 tokens and head at a copy's rate.  They take 242 issued warp
 // instructions (64 conversions, 64 fp16x2 products and 16 tensor products among
 // them): 64 ragged sequences to 16K (633 MB) take 104 us, 6.1 TB/s or 90% of a
 // copy's 6.77.  Each warp streams its own 16-token tiles through a private ring of
@@ -73,11 +74,11 @@ constexpr int WIDE_UNITS = 32;      // units of a segment per CTA of that size, 
 // product).
 constexpr int rows_of(int nt) { return nt == 0 ? 4 : 8 * nt; }
 
-// Per row-tile width: CTAs per SM, ring stages,
-// whether the main loop goes around the ring in one piece (64 ragged sequences
-// to 16K, NT = 1: 121 us by single tiles, 118 unrolled with 5 stages, 115 with 4;
-// five tokens over 16 to 32K, NT = 3: 133 and 141), and the most CTAs a launch
-// has (the workspace holds two partial results each).
+// Per row-tile width: CTAs per SM, ring stages, whether the main loop goes around
+// the ring in one piece (64 ragged sequences to 16K, NT = 1: 121 us by single
+// tiles, 118 unrolled with 5 stages, 115 with 4; five tokens over 16 to 32K, NT =
+// 3: 133 and 141), and the most CTAs a launch has (the workspace holds two partial
+// results each).
 template <int NT>
 struct Shape;
 template <>
