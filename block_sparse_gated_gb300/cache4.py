@@ -122,6 +122,18 @@ def _exponents(t, heads: int, cache, device):
     return t.data_ptr()
 
 
+def _strides(t, shape, s, layout: str, varlen: bool):
+    """Element strides {batch, head, token}, heads and tokens of a tensor of
+    this shape and stride: _strides_bhtd for the layouts met most, without
+    reading the tensor's attributes again."""
+    if len(shape) == 4 and s[3] == 1 and not varlen:
+        if layout == "bhld":
+            return (s[0], s[1], s[2]), shape[1], shape[2]
+        if layout == "blhd":
+            return (s[0], s[2], s[1]), shape[2], shape[1]
+    return _strides_bhtd(t, layout, varlen)
+
+
 def _int32_vector(t, n: int, what: str):
     if t.dtype is not _I32 or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 [{n}] tensor")
@@ -143,8 +155,9 @@ def _rows_fields(k, v, layout, cu_seqlens, start, heads: int, d: int, device):
         raise TypeError("K and V must share one element type")
     if device.type != "cuda" or not k.get_device() == v.get_device() == device.index:
         _on_device(device, k=k, v=v)
-    ks, hk, n = _strides_bhtd(k, layout, varlen)
-    vs = ks if v.stride() == k.stride() else _strides_bhtd(v, layout, varlen)[0]
+    a, b = k.stride(), v.stride()
+    ks, hk, n = _strides(k, shape, a, layout, varlen)
+    vs = ks if a == b else _strides(v, shape, b, layout, varlen)[0]
     if hk != heads or shape[-1] != d:
         raise ValueError("K and V must have the cache's heads and head dimension")
     cu = first = 0
@@ -271,8 +284,10 @@ def _decode_fields(q, cache, block_table, seqlens, out, device, *, layout, max_s
     shape = q.shape
     if out.shape != shape or q.dtype is not out.dtype:
         raise ValueError("q and out must have one shape and type")
-    qs, hq, n = _strides_bhtd(q, layout, False)
-    os_ = qs if out.stride() == q.stride() else _strides_bhtd(out, layout, False)[0]
+    code = _dtype_code(q)
+    a, b = q.stride(), out.stride()
+    qs, hq, n = _strides(q, shape, a, layout, False)
+    os_ = qs if a == b else _strides(out, shape, b, layout, False)[0]
     heads, d = _heads_and_dim(cache)
     if shape[-1] != d or heads == 0 or hq % heads:
         raise ValueError("q must have the cache's head dimension and a multiple of its heads")
@@ -285,7 +300,6 @@ def _decode_fields(q, cache, block_table, seqlens, out, device, *, layout, max_s
     fixed = (q.data_ptr(), out.data_ptr(), *qs, *os_, batch, hq, n,
              _int32_vector(seqlens, batch, "seqlens"), int(max_seqlen),
              float(softmax_scale) if softmax_scale else 0.0, 1 if causal else 0, lse)
-    code = _dtype_code(q)
     return c, lambda ws, size: _native.DECODE4.pack(*fixed, ws, size, code)
 
 
