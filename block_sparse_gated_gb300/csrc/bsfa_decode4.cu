@@ -992,7 +992,9 @@ Plan plan_of(const bsfa_cache4* c, const bsfa_decode4_params* p) {
   pl.units = (p->max_seqlen + UNIT - 1) / UNIT;
   if (pl.units < 1) pl.units = 1;
   pl.segments = static_cast<long long>(p->batch) * c->num_heads_kv * pl.row_tiles;
-  pl.all_units = pl.segments * (pl.units + SEGMENT_UNITS);
+  // (Beyond 2^31 segments, which are refused, the product could overflow.)
+  pl.all_units =
+      pl.segments >> 31 ? pl.segments : pl.segments * (pl.units + SEGMENT_UNITS);
   if (rows <= 4) pl.nt = 0;
   constexpr int grids[5] = {Shape<0>::MAX_GRID, Shape<1>::MAX_GRID, Shape<2>::MAX_GRID,
                             Shape<3>::MAX_GRID, Shape<4>::MAX_GRID};

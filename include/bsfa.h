@@ -407,8 +407,9 @@ typedef struct {
  * workspace may be NULL.  0 for invalid parameters, too. */
 size_t bsfa_decode4_workspace_size(const bsfa_cache4* cache, const bsfa_decode4_params* p);
 
-/* Limits (BSFA_ERR_UNSUPPORTED beyond them): 4096 sequences, and
- * batch * Hkv * (query row tiles) * ceil(max_seqlen / 64) < 2^31. */
+/* Limits (BSFA_ERR_UNSUPPORTED beyond them): 4096 sequences, 2^24 query rows
+ * per KV head (Hq / Hkv * q_len), and with these in tiles of up to 32
+ *   batch * Hkv * tiles * (ceil(max_seqlen / 64) + 8) < 2^31 - 4096. */
 bsfa_status bsfa_decode4(const bsfa_cache4* cache, const bsfa_decode4_params* p,
                          bsfa_stream_t stream);
 
