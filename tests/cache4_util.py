@@ -62,6 +62,38 @@ def random_cache(bsfa, lens, page, heads, d, seed, device, *, layout="phtd", exp
     return bsfa.KVCache4(*t, *e, layout), torch.from_numpy(table).to(device), rows
 
 
+def long_cache(bsfa, lens, page, heads, d, seed, device, *, layout="phtd", block=4000):
+    """random_cache() for long sequences: the rows of every sequence repeat one
+    quantised block of ``block`` tokens, each sequence from another place in it,
+    and no row is set by itself."""
+    rng = np.random.default_rng(seed)
+    table, pool = table_for(lens, page, rng)
+    out, rows = [], [[] for _ in lens]
+    for i in range(2):
+        x = rng.standard_normal((heads, block, d))
+        if i == 0:
+            x *= 0.5 + np.abs(rng.standard_normal((heads, 1, d)))
+        code, byte = co.quantise(x)
+        code = co.pack(code)
+        stands = co.values(code, byte)
+        codes = np.full((pool, page, heads, d // 2), 0xFF, np.uint8)
+        scales = np.full((pool, page, heads, d // 16), 0xFF, np.uint8)
+        for b, L in enumerate(lens):
+            t = np.arange(L)
+            src = (t + 977 * b) % block
+            at = (table[b, t // page], t % page)
+            codes[at] = code[:, src].transpose(1, 0, 2)
+            scales[at] = byte[:, src].transpose(1, 0, 2)
+            rows[b].append(stands[:, src])
+        out.append((codes, scales))
+    t = [torch.from_numpy(out[i][j]).to(device) for j in range(2) for i in range(2)]
+    if layout == "phtd":
+        t = [y.transpose(1, 2).contiguous() for y in t]
+    t[2:] = [y.view(torch.float8_e4m3fn) for y in t[2:]]
+    return bsfa.KVCache4(*t, None, None, layout), torch.from_numpy(table).to(device), \
+        [tuple(kv) for kv in rows]
+
+
 def widen(table, page, tokens=70000):
     """The same table with unused columns up to a capacity of ``tokens``: the
     bound that a call works with when it is given none.  With the default a call

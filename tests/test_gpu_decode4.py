@@ -372,3 +372,66 @@ def test_prefill_then_decode_as_they_are_used(cuda_device):
     assert (whole["lse"] - chunk["lse"]).abs().max().item() < 2e-3
     assert torch.equal(chunk["out"][:, :, -1:], outs[-1]) or \
         (chunk["out"][:, :, -1:].float() - outs[-1].float()).abs().max().item() < 2e-2
+
+
+# Rows of one KV head for each width of the row tile: 4, 8, 12, 20, 32.
+WIDTHS = [(8, 2, 1), (16, 2, 1), (12, 1, 1), (4, 1, 5), (32, 1, 1)]
+
+
+@pytest.mark.parametrize("layout", ["phtd", "pthd"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads", WIDTHS)
+@pytest.mark.parametrize("bound", [256, 1400, 70000])
+def test_both_page_orders_at_every_row_width(cuda_device, layout, d, heads, bound):
+    """Pages laid out head first and token first, whatever the heads, by CTAs of
+    four and of sixteen warps in clusters and by cut pieces."""
+    b = _bsfa()
+    Hq, Hkv, n = heads
+    lens = [0, 250, 1, 33] if bound == 256 else [1301, 129, 0, 700, 16]
+    cache, table, rows = cu.random_cache(b, lens, 32, Hkv, d, Hq + d, cuda_device, layout=layout)
+    q = _queries(len(lens), Hq, n, d, HF if d == 64 else BF, Hq, cuda_device, 1.5)
+    res = b.decode4(q, cache, cu.widen(table, 32, bound), _i32(lens, cuda_device),
+                    max_seqlen=bound, return_lse=True)
+    cu.check_decode(res, q, rows, lens, HF if d == 64 else BF, d)
+
+
+@pytest.mark.parametrize("layout", ["phtd", "pthd"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,n", [(8, 1), (32, 1), (16, 2), (64, 1), (24, 2)])
+def test_many_short_sequences(cuda_device, layout, d, Hq, n):
+    """800 segments, more than are resident at once: CTAs of two warps, for one,
+    four, eight and six query rows of a KV head."""
+    b = _bsfa()
+    rng = np.random.default_rng(Hq + d)
+    lens = [int(x) for x in rng.integers(0, 101, 100)]
+    cache, table, rows = cu.random_cache(b, lens, 16, 8, d, 3, cuda_device, layout=layout)
+    q = _queries(100, Hq, n, d, BF, Hq, cuda_device, 1.5)
+    res = b.decode4(q, cache, table, _i32(lens, cuda_device), return_lse=True)
+    cu.check_decode(res, q, rows, lens, BF, d)
+
+
+@pytest.mark.parametrize("length,Hq,d,layout", [
+    (70000, 4, 128, "phtd"), (70000, 12, 64, "pthd"), (70000, 32, 128, "pthd"),
+    (150000, 4, 64, "phtd"), (150000, 8, 128, "phtd")])
+def test_a_history_of_hundreds_of_parts(cuda_device, length, Hq, d, layout):
+    """One sequence of one KV head, four units to a CTA: 276 and 588 parts for one
+    block of the join to add."""
+    b = _bsfa()
+    cache, table, rows = cu.long_cache(b, [length], 64, 1, d, Hq, cuda_device, layout=layout)
+    q = _queries(1, Hq, 1, d, BF, Hq, cuda_device, 1.5)
+    res = b.decode4(q, cache, table, _i32([length], cuda_device), return_lse=True)
+    cu.check_decode(res, q, rows, [length], BF, d)
+
+
+@pytest.mark.parametrize("Hq,n,d,longest", [(2, 1, 128, 20000), (12, 1, 64, 20000),
+                                            (4, 5, 128, 40000), (4, 1, 64, 131000)])
+def test_one_long_history_among_many_short_ones(cuda_device, Hq, n, d, longest):
+    """300 short sequences make few parts the rule; the long one has 46 to 256,
+    which one warp per row adds 32 at a time."""
+    b = _bsfa()
+    lens = [int(x) for x in np.random.default_rng(Hq).integers(0, 40, 300)]
+    lens.insert(123, longest)
+    cache, table, rows = cu.long_cache(b, lens, 16, 1, d, Hq, cuda_device)
+    q = _queries(301, Hq, n, d, HF, Hq, cuda_device, 1.5)
+    res = b.decode4(q, cache, table, _i32(lens, cuda_device), return_lse=True)
+    cu.check_decode(res, q, rows, lens, HF, d)
