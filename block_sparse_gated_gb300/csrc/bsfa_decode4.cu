@@ -2,7 +2,8 @@
 // over the 4-bit cache.
 //
 // Mathematics.  With k_t = code * scale (exact in fp16) and the query row
-// scaled by a power of two into fp16's range, S^T = K Q^T and O^T = V^T P^T are
+// scaled by a power of two into fp16's range (elements more than 2^28 below the
+// row's largest lose bits there), S^T = K Q^T and O^T = V^T P^T are
 // fp16 tensor-core products with fp32 sums.  The softmax is streamed: a
 // reference m (log2 units) is subtracted, p = 2^(y - m), and m is raised, with
 // O and the sum l rescaled, only when some score passes it by more than
@@ -380,8 +381,8 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) copy_tile(my_ring + s * St::BYTES);
 
-    // ---- queries: fragments of Q^T (fp16, row scaled to [2^14, 2^15)) and the
-    // factor that turns a product into a score in log2 units
+    // ---- queries: fragments of Q^T (fp16, a row's largest element scaled to
+    // [2^14, 2^15)) and the factor that turns a product into a score in log2 units
     for (int nt = warp; nt < NT; nt += WARPS) {
       const int q_row = HALF ? g >> 1 : nt * 8 + g, r = r0 + q_row;
       float f[D / 4];
@@ -408,12 +409,20 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       // A row with an infinity or a NaN stays as it is: its scores are not
-      // numbers in any scaling.
+      // numbers in any scaling.  2^126 is the largest factor whose inverse is a
+      // normal number, and it is enough: it turns bf16's least subnormal into
+      // 2^-7, so a row that stays below 2^14 for it is exact in fp16.  Elsewhere
+      // an element is exact that is scaled to 2^-14 or more (bf16 has 8 bits,
+      // fp16 11), and one below is off by 2^-25 at most, 2^-39 of the row's
+      // largest.
       const int ex = (__float_as_int(amax) >> 23) - 127;
-      const int up = amax == 0.f || ex > 127 ? 0 : min(14 - ex, 100);
+      const int up = amax == 0.f || ex > 127 ? 0 : min(14 - ex, 126);
       const float mul = pow2f(up);
       if (c == 0) {
-        sh_sc[q_row] = a.sigma_log2 * pow2f(-up) * pow2f(head_exp(a.kexp, kvh));
+        // The power of two in two factors of the same sign: only a result beyond
+        // fp32's range leaves it.
+        const int e = head_exp(a.kexp, kvh) - up;
+        sh_sc[q_row] = a.sigma_log2 * pow2f(e / 2) * pow2f(e - e / 2);
         // Rows past the last are computed along with the rest and not stored.
         sh_lim[q_row] = !a.causal || r >= a.rows ? len : len - a.q_len + r / a.group + 1;
       }

@@ -379,8 +379,10 @@ bsfa_status bsfa_cache4_read(const bsfa_cache4* cache, const bsfa_cache4_rows* r
  * seqlens stays on the device; entries are clamped to [0, max_seqlen].
  *
  * Products run on the tensor cores in fp16 with fp32 accumulation: cached
- * values are exact in fp16, queries are scaled per row by a power of two, and
- * the weights are rounded to fp16 (11 bits).  O is rounded to dtype once.
+ * values are exact in fp16, and the weights are rounded to fp16 (11 bits).
+ * Queries are scaled per row by a power of two, whatever their size, and are
+ * exact as long as a row's elements lie within 2^28 of its largest; a smaller
+ * one is off by at most 2^-39 of the largest.  O is rounded to dtype once.
  */
 typedef struct {
   const void* q;              /* [batch, Hq, q_len, d] by strides */

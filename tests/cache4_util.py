@@ -104,12 +104,26 @@ def widen(table, page, tokens=70000):
     return torch.cat([table, pad], 1)
 
 
-def bounds(out, lse, weighted, flat, span, dtype, d):
+def query_error(q, k, sigma):
+    """Largest score error [Hq, n] from holding query rows q [Hq, n, d] in fp16,
+    over keys k [Hkv, L, d].  The kernel scales a row by the power of two that
+    brings its largest element into [2^14, 2^15) (by 2^126 at most).  An element
+    that stays at 2^-14 or above is exact: bf16 has 8 bits, fp16 11.  One below
+    is rounded to a multiple of 2^-24, so it is off by 2^-25 at most."""
+    amax = np.abs(q).max(-1)
+    up = np.minimum(14 - np.floor(np.log2(np.where(amax > 0, amax, 1.0))), 126)
+    most = np.abs(k).sum(-1).max(-1, initial=0.0).repeat(q.shape[0] // k.shape[0])
+    return 2.0 ** (-25 - up) * most[:, None] * sigma
+
+
+def bounds(out, lse, weighted, flat, span, dtype, d, query=0.0):
     """Largest errors that the kernel's arithmetic allows, elementwise.
 
     Score: products are exact; d of them are added in fp32 (each addition off by
     at most 2^-23 of the running magnitude, which span bounds), and scaling,
-    the subtraction of the reference and 2^x add a few units: delta.
+    the subtraction of the reference and 2^x add a few units: delta.  Queries
+    whose elements differ in size by more than 2^28 are not exact in fp16: query
+    is what query_error() allows for that.
 
     Weights p are rounded to fp16: by 2^-11 of themselves, and below its normal
     range by 2^-25.  The largest weight of a row is at least 2^5: p carries
@@ -119,7 +133,7 @@ def bounds(out, lse, weighted, flat, span, dtype, d):
     not bounded by sum p |v|: the heavy tokens' values may be zero).
 
     Sums run in fp32, and the result is rounded once to dtype."""
-    delta = span * (d + 8) * 2.0 ** -23 + 2.0 ** -20
+    delta = span * (d + 8) * 2.0 ** -23 + 2.0 ** -20 + query
     half = torch.finfo(dtype).eps / 2
     tiny = torch.finfo(dtype).smallest_normal * half
     o = np.abs(out) * half + weighted * (2.0 ** -11 + 2.0 ** -16 + 2 * delta[..., None]) + \
@@ -127,8 +141,9 @@ def bounds(out, lse, weighted, flat, span, dtype, d):
     return o * 1.01, delta + np.abs(np.where(np.isfinite(lse), lse, 0.0)) * 2.0 ** -21
 
 
-def check_decode(res, q, rows, lens, dtype, d, *, sigma=None, causal=True):
-    """Every output row of every sequence against the oracle; q [B, Hq, n, d]."""
+def check_decode(res, q, rows, lens, dtype, d, *, sigma=None, causal=True, uneven=False):
+    """Every output row of every sequence against the oracle; q [B, Hq, n, d].
+    ``uneven``: with query_error()."""
     sigma = 1 / math.sqrt(d) if sigma is None else sigma
     got = res["out"].detach().cpu().double().numpy()
     got_lse = res["lse"].cpu().double().numpy() if "lse" in res else None
@@ -138,7 +153,8 @@ def check_decode(res, q, rows, lens, dtype, d, *, sigma=None, causal=True):
         qq = q[b].detach().cpu().double().numpy()
         out, lse, weighted, flat, span = co.attend(qq, k[:, :lens[b]], v[:, :lens[b]],
                                                    sigma=sigma, causal=causal)
-        tol, tol_lse = bounds(out, lse, weighted, flat, span, dtype, d)
+        query = query_error(qq, k[:, :lens[b]], sigma) if uneven else 0.0
+        tol, tol_lse = bounds(out, lse, weighted, flat, span, dtype, d, query)
         err = np.abs(got[b] - out)
         assert (err <= tol).all(), f"sequence {b}: {(err / tol).max():.2f} of the bound"
         worst = max(worst, float((err / tol).max(initial=0.0)))

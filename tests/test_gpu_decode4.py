@@ -435,3 +435,36 @@ def test_one_long_history_among_many_short_ones(cuda_device, Hq, n, d, longest):
     q = _queries(301, Hq, n, d, HF, Hq, cuda_device, 1.5)
     res = b.decode4(q, cache, table, _i32(lens, cuda_device), return_lse=True)
     cu.check_decode(res, q, rows, lens, HF, d)
+
+
+@pytest.mark.parametrize("dtype,power", [(BF, 18), (BF, 22), (BF, 26), (BF, 30), (HF, 15)])
+@pytest.mark.parametrize("heads", [(4, 1), (8, 1)])
+def test_queries_of_very_different_elements(cuda_device, dtype, power, heads):
+    """A row's largest element meets only zeros in the keys, so that the scores
+    come from elements that are 2^18 to 2^30 times smaller (in fp16 from 2^-9
+    beside 2^15)."""
+    b = _bsfa()
+    L, d = 300, 128
+    cache, table, rows = cu.random_cache(b, [L], 32, 1, d, power, cuda_device)
+    cache.k[..., 0] &= 0xF0  # element 0
+    rows[0][0][..., 0] = 0.0
+    q = _queries(1, heads[0], 1, d, dtype, power, cuda_device, 2.0 ** -9 if dtype == HF else 1.5)
+    q[..., 0] = 2.0 ** power
+    for t in (table, cu.widen(table, 32)):
+        res = b.decode4(q, cache, t, _i32([L], cuda_device), return_lse=True)
+        cu.check_decode(res, q, rows, [L], dtype, d, uneven=True)
+
+
+@pytest.mark.parametrize("power", [-90, -105, -115, -122, -126, -130])
+def test_tiny_queries_and_a_large_scale(cuda_device, power):
+    """Query rows down to bf16's subnormals, with the softmax scale that makes
+    their scores ordinary: they are scaled without losing a bit."""
+    b = _bsfa()
+    L, d = 200, 64
+    cache, table, rows = cu.random_cache(b, [L], 16, 1, d, 7, cuda_device)
+    q = (_queries(1, 8, 1, d, BF, 7, "cpu", 1.5).float() * 2.0 ** power).to(BF).to(cuda_device)
+    assert q.any()
+    sigma = 2.0 ** -power / 8
+    for t in (table, cu.widen(table, 16)):
+        res = b.decode4(q, cache, t, _i32([L], cuda_device), softmax_scale=sigma, return_lse=True)
+        cu.check_decode(res, q, rows, [L], BF, d, sigma=sigma)
