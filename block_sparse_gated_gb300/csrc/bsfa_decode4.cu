@@ -38,6 +38,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -420,9 +421,10 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
       const float mul = pow2f(up);
       if (c == 0) {
         // The power of two in two factors of the same sign: only a result beyond
-        // fp32's range leaves it.
+        // fp32's range leaves it, and is cut to its largest number there, so that
+        // products of zero stay scores of zero.
         const int e = head_exp(a.kexp, kvh) - up;
-        sh_sc[q_row] = a.sigma_log2 * pow2f(e / 2) * pow2f(e - e / 2);
+        sh_sc[q_row] = fminf(a.sigma_log2 * pow2f(e / 2) * pow2f(e - e / 2), FLT_MAX);
         // Rows past the last are computed along with the rest and not stored.
         sh_lim[q_row] = !a.causal || r >= a.rows ? len : len - a.q_len + r / a.group + 1;
       }

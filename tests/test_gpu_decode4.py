@@ -468,3 +468,21 @@ def test_tiny_queries_and_a_large_scale(cuda_device, power):
     for t in (table, cu.widen(table, 16)):
         res = b.decode4(q, cache, t, _i32([L], cuda_device), softmax_scale=sigma, return_lse=True)
         cu.check_decode(res, q, rows, [L], BF, d, sigma=sigma)
+
+
+def test_zero_keys_of_a_head_with_a_large_exponent(cuda_device):
+    """Scores of zero stay zero where the factor from products to scores passes
+    fp32's range (queries of 2^120, keys in units of 2^100): equal weights."""
+    b = _bsfa()
+    L, d, page = 40, 64, 16
+    big = torch.tensor([100], dtype=torch.int32, device=cuda_device)
+    cache = b.cache4_empty(3, 1, page, d, k_exp=big, device=cuda_device)
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device=cuda_device)
+    g = torch.Generator().manual_seed(3)
+    v = torch.randn(1, 1, L, d, generator=g).to(BF).to(cuda_device)
+    b.cache4_write(cache, torch.zeros_like(v), v, table)
+    _, v = b.cache4_read(cache, table, seqlen=L)
+    rows = [(np.zeros((1, L, d)), v[0].cpu().double().numpy())]
+    q = (_queries(1, 4, 1, d, BF, 3, cuda_device) * 2.0 ** 120)
+    res = b.decode4(q, cache, table, _i32([L], cuda_device), return_lse=True)
+    cu.check_decode(res, q, rows, [L], BF, d)
