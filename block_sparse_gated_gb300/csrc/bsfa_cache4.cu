@@ -47,7 +47,7 @@ struct Slot {
 
 __device__ __forceinline__ Slot find_slot(const RowsArgs& a, int t) {
   Slot s;
-  int pos;
+  long long pos;  // offsets below zero put rows of a sequence beyond 2^31
   if (a.cu == nullptr) {
     s.b = t / a.seqlen;
     s.i = t - s.b * a.seqlen;
@@ -66,11 +66,11 @@ __device__ __forceinline__ Slot find_slot(const RowsArgs& a, int t) {
     s.i = t;
     if (s.b >= 0 && t >= __ldg(a.cu + s.b + 1)) s.b = -1;
     if (s.b < 0) return s;
-    pos = s.i - __ldg(a.cu + s.b);
+    pos = static_cast<long long>(t) - __ldg(a.cu + s.b);
   }
   s.page = -1;
   s.token = 0;
-  const long long p = static_cast<long long>(pos) + (a.start ? __ldg(a.start + s.b) : 0);
+  const long long p = pos + (a.start ? __ldg(a.start + s.b) : 0);
   if (p >= 0 && p < static_cast<long long>(a.table_width) * a.page_size) {
     const int col = static_cast<int>(p) / a.page_size;
     const int page = __ldg(a.table + static_cast<long long>(s.b) * a.table_stride + col);

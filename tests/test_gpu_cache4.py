@@ -341,3 +341,19 @@ def test_offsets_beyond_32_bits(cuda_device):
     for a, e in zip(b.cache4_read(cache, table, seqlen=L), b.cache4_read(small, table, seqlen=L)):
         assert torch.equal(a, e)
     assert torch.equal(b.decode4(q, cache, table, n)["out"], b.decode4(q, small, table, n)["out"])
+
+
+def test_packed_offsets_far_below_zero(cuda_device):
+    """Rows whose place in their sequence passes 2^31: their positions lie beyond
+    the table, whatever the start."""
+    b = _bsfa()
+    cache = b.cache4_empty(1, 1, 16, 64, device=cuda_device)
+    table = torch.zeros(1, 1, dtype=torch.int32, device=cuda_device)
+    x = torch.ones(1, 8, 64, dtype=BF, device=cuda_device)
+    where = dict(cu_seqlens=torch.tensor([-(1 << 31), 8], dtype=torch.int32, device=cuda_device),
+                 start=torch.tensor([(1 << 31) - 1], dtype=torch.int32, device=cuda_device))
+    b.cache4_write(cache, x, x, table, **where)
+    assert not cache.k.any()
+    cache.k.fill_(0x22), cache.k_scale.view(torch.uint8).fill_(0x38)
+    k, _ = b.cache4_read(cache, table, total=8, **where)
+    assert not k.any()
