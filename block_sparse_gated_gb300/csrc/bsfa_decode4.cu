@@ -1078,6 +1078,15 @@ bsfa_status validate_sizes(const bsfa_cache4* c, const bsfa_decode4_params* p) {
   return BSFA_OK;
 }
 
+// The status of a runtime call.  The runtime keeps the error of one that failed
+// until it is asked for it: asked here, a later launch does not report it as its
+// own.
+bsfa_status status_of(cudaError_t e) {
+  if (e == cudaSuccess) return BSFA_OK;
+  cudaGetLastError();
+  return BSFA_ERR_CUDA;
+}
+
 template <int D, int NT, bool DENSE, int W = WARPS>
 bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaStream_t stream) {
   constexpr int smem = smem_bytes<D, NT, W>(true);
@@ -1086,9 +1095,9 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
   static std::atomic<uint64_t> ready{0};
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    if (cudaFuncSetAttribute(decode4_kernel<D, NT, DENSE, W>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-      return BSFA_ERR_CUDA;
+    const bsfa_status v = status_of(cudaFuncSetAttribute(
+        decode4_kernel<D, NT, DENSE, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    if (v != BSFA_OK) return v;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   if (!pl.split) {
@@ -1103,8 +1112,7 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, decode4_kernel<D, NT, DENSE, W>, args);
-    return e == cudaSuccess ? BSFA_OK : BSFA_ERR_CUDA;
+    return status_of(cudaLaunchKernelEx(&cfg, decode4_kernel<D, NT, DENSE, W>, args));
   }
   if constexpr (W == WARPS) {  // other CTAs never cut
     const long long full = static_cast<long long>(sms) * Shape<NT>::CTAS;
@@ -1130,10 +1138,8 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e =
-        by_rows ? cudaLaunchKernelEx(&cfg, decode4_join_rows_kernel<D, ROWS>, a)
-                : cudaLaunchKernelEx(&cfg, decode4_join_kernel<D, ROWS>, a);
-    return e == cudaSuccess ? BSFA_OK : BSFA_ERR_CUDA;
+    return status_of(by_rows ? cudaLaunchKernelEx(&cfg, decode4_join_rows_kernel<D, ROWS>, a)
+                             : cudaLaunchKernelEx(&cfg, decode4_join_kernel<D, ROWS>, a));
   }
   return BSFA_ERR_CUDA;
 }
@@ -1217,9 +1223,10 @@ bsfa_status bsfa_decode4(const bsfa_cache4* cache, const bsfa_decode4_params* p,
   a.joins = reinterpret_cast<int4*>(ws + cv.joins);
 
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-    return BSFA_ERR_CUDA;
+  v = status_of(cudaGetDevice(&dev));
+  if (v != BSFA_OK) return v;
+  v = status_of(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  if (v != BSFA_OK || sms <= 0) return BSFA_ERR_CUDA;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   const int row = cache->head_dim / 2, z = cache->head_dim / FP4_GROUP;
   const bool dense = cache->k_stride[2] == row && cache->v_stride[2] == row &&

@@ -486,3 +486,32 @@ def test_zero_keys_of_a_head_with_a_large_exponent(cuda_device):
     q = (_queries(1, 4, 1, d, BF, 3, cuda_device) * 2.0 ** 120)
     res = b.decode4(q, cache, table, _i32([L], cuda_device), return_lse=True)
     cu.check_decode(res, q, rows, [L], BF, d)
+
+
+def test_a_launch_that_failed_leaves_no_error_behind(cuda_device):
+    """The runtime refuses a launch on the legacy stream while this thread
+    captures a blocking stream; the calls after it answer for themselves."""
+    import ctypes
+    b = _bsfa()
+    cache, table, rows = cu.random_cache(b, [100], 16, 2, 64, 5, cuda_device)
+    q = _queries(1, 4, 1, 64, BF, 5, cuda_device)
+    n32, out = _i32([100], cuda_device), torch.empty_like(q)
+    x = torch.zeros(1, 2, 10, 64, dtype=BF, device=cuda_device)
+    b.decode4(q, cache, table, n32, out=out)
+    torch.cuda.synchronize()
+    with open("/proc/self/maps") as f:  # the runtime that torch has loaded
+        rt = ctypes.CDLL(next(line.split()[-1] for line in f if "libcudart" in line))
+    stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    assert rt.cudaStreamCreate(ctypes.byref(stream)) == 0
+    assert rt.cudaStreamBeginCapture(stream, 0) == 0
+    try:
+        with pytest.raises(b.BsfaError) as e:
+            b.decode4(q, cache, table, n32, out=out, stream=torch.cuda.default_stream())
+    finally:
+        rt.cudaStreamEndCapture(stream, ctypes.byref(graph))
+        rt.cudaGetLastError()
+        rt.cudaStreamDestroy(stream)
+    assert e.value.status == 3
+    spare = b.cache4_empty(1, 2, 16, 64, device=cuda_device)
+    b.cache4_write(spare, x, x, torch.zeros(1, 1, dtype=torch.int32, device=cuda_device))
+    cu.check_decode(b.decode4(q, cache, table, n32), q, rows, [100], BF, 64)
