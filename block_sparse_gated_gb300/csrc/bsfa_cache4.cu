@@ -360,7 +360,9 @@ bsfa_status validate_cache4_pointers(const bsfa_cache4* c) {
   const uintptr_t scale_bits =
       reinterpret_cast<uintptr_t>(c->k_scale) | reinterpret_cast<uintptr_t>(c->v_scale);
   if ((code_bits & 15u) || (scale_bits & (unit - 1))) return BSFA_ERR_UNSUPPORTED;
+  const int extent[3] = {c->num_pages, c->num_heads_kv, c->page_size};
   for (int i = 0; i < 3; ++i) {
+    if (extent[i] == 1) continue;  // only ever multiplied by 0
     if (c->k_stride[i] <= 0 || c->v_stride[i] <= 0 || c->k_scale_stride[i] <= 0 ||
         c->v_scale_stride[i] <= 0)
       return BSFA_ERR_UNSUPPORTED;

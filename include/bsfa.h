@@ -323,7 +323,8 @@ typedef struct {
   /* Strides in BYTES as {page, head, token}: token t of page p of head h
    * begins at base + p*stride[0] + h*stride[1] + t*stride[2].  Codes: bases
    * and strides are multiples of 16; scales: multiples of head_dim / 16 (the
-   * bytes of a row).  stride[0] < 2^34, page_size * stride[2] < 2^31. */
+   * bytes of a row).  stride[0] < 2^34, page_size * stride[2] < 2^31.  With one
+   * page or one head its stride says nothing. */
   int64_t k_stride[3], v_stride[3], k_scale_stride[3], v_scale_stride[3];
   int num_pages;              /* pages in each pool (>= 1) */
   int page_size;              /* tokens per page: a positive multiple of 16 */

@@ -121,6 +121,25 @@ def test_cache_strides_that_are_refused(lib):
         assert lib.bsfa_cache4_read(ctypes.byref(c), ctypes.byref(r), None) == UNSUPPORTED
 
 
+def test_strides_of_one_element_dimensions_say_nothing(lib):
+    """A pool of one page and one head is not refused for strides that no call
+    multiplies by anything but 0; of two, it is."""
+    for pages, heads, status in ((1, 1, WORKSPACE), (2, 1, UNSUPPORTED), (1, 2, UNSUPPORTED)):
+        c = _cache(num_pages=pages, num_heads_kv=heads, block_table_width=2000,
+                   block_table_stride=2000)
+        for s in (c.k_stride, c.v_stride, c.k_scale_stride, c.v_scale_stride):
+            if pages == 1:
+                s[0] = 1
+            if heads == 1:
+                s[1] = 0
+        if pages == 2:
+            c.k_stride[0] = 8
+        if heads == 2:
+            c.v_scale_stride[1] = 0
+        p = _decode(max_seqlen=100000)  # long enough to need the workspace it lacks
+        assert lib.bsfa_decode4(ctypes.byref(c), ctypes.byref(p), None) == status
+
+
 def test_rows_that_are_refused(lib):
     c = ctypes.byref(_cache())
     for change, status in ((dict(batch=-1), INVALID), (dict(seqlen=-1), INVALID),

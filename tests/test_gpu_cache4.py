@@ -357,3 +357,29 @@ def test_packed_offsets_far_below_zero(cuda_device):
     cache.k.fill_(0x22), cache.k_scale.view(torch.uint8).fill_(0x38)
     k, _ = b.cache4_read(cache, table, total=8, **where)
     assert not k.any()
+
+
+@pytest.mark.parametrize("layout", ["phtd", "pthd"])
+@pytest.mark.parametrize("stride", [0, 1, 8])
+def test_pools_of_one_page_and_one_head(cuda_device, layout, stride):
+    """The strides of dimensions of one element say nothing."""
+    b = _bsfa()
+    L, d, page = 40, 128, 48
+    g = torch.Generator().manual_seed(6)
+    k, v = torch.randn(2, 1, 1, L, d, generator=g).to(BF).to(cuda_device)
+    q = torch.randn(1, 4, 1, d, generator=g).to(BF).to(cuda_device)
+    table = torch.zeros(1, 1, dtype=torch.int32, device=cuda_device)
+    n32 = torch.tensor([L], dtype=torch.int32, device=cuda_device)
+    plain = b.cache4_empty(1, 1, page, d, layout=layout, device=cuda_device)
+    raw = b.cache4_empty(1, 1, page, d, layout=layout, device=cuda_device)
+    head = 1 if layout == "phtd" else 2
+    odd = raw._replace(**{n: t.as_strided(t.shape, [stride if i in (0, head) else s
+                                                    for i, s in enumerate(t.stride())])
+                          for n, t in zip(("k", "v", "k_scale", "v_scale"), raw)})
+    got = []
+    for c in (plain, odd):
+        b.cache4_write(c, k, v, table)
+        got.append((*b.cache4_read(c, table, seqlen=L), b.decode4(q, c, table, n32)["out"]))
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+    for x, y in zip(plain[:4], raw[:4]):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
