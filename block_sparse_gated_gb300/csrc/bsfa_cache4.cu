@@ -353,7 +353,8 @@ bsfa_status validate_cache4(const bsfa_cache4* c) {
 }
 
 bsfa_status validate_cache4_pointers(const bsfa_cache4* c) {
-  if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->block_table)
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale ||
+      (!c->block_table && c->block_table_width > 0))
     return BSFA_ERR_INVALID_ARG;
   const int64_t unit = c->head_dim / FP4_GROUP;  // bytes of a row's scales
   const uintptr_t code_bits = reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v);

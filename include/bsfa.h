@@ -335,7 +335,8 @@ typedef struct {
    * [0, num_pages), or a position outside [0, block_table_width*page_size),
    * names no row: a write there is dropped, a read gives zeros, and attention
    * sees a zero key and a zero value (a prefill's page table does the same). */
-  const int32_t* block_table; /* device int32 [batch][block_table_stride] */
+  const int32_t* block_table; /* device int32 [batch][block_table_stride]; may be null where
+                                 block_table_width is 0 */
   int block_table_stride;     /* elements between two sequences' rows, >= width */
   int block_table_width;      /* entries of each row that may be read;
                                  block_table_width * page_size <= 2^30 */

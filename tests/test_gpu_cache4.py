@@ -383,3 +383,20 @@ def test_pools_of_one_page_and_one_head(cuda_device, layout, stride):
     assert all(torch.equal(x, y) for x, y in zip(*got))
     for x, y in zip(plain[:4], raw[:4]):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_a_table_of_no_pages(cuda_device):
+    """A block table of width 0 names no row: nothing is written, rows read as
+    zeros, and a query sees nothing."""
+    b = _bsfa()
+    cache = b.cache4_empty(2, 2, 16, 64, device=cuda_device)
+    table = torch.zeros(3, 0, dtype=torch.int32, device=cuda_device)
+    x = torch.ones(3, 2, 5, 64, dtype=BF, device=cuda_device)
+    b.cache4_write(cache, x, x, table)
+    assert not any(t.view(torch.uint8).any() for t in cache[:4])
+    k, v = b.cache4_read(cache, table, seqlen=5)
+    assert not k.any() and not v.any()
+    q = torch.ones(3, 4, 1, 64, dtype=BF, device=cuda_device)
+    res = b.decode4(q, cache, table, torch.tensor([0, 7, 1], dtype=torch.int32, device=cuda_device),
+                    return_lse=True)
+    assert not res["out"].any() and bool(torch.isneginf(res["lse"]).all())
