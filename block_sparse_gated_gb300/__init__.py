@@ -20,4 +20,5 @@ from .cache4 import (  # noqa: F401
     cache4_read,
     cache4_write,
     decode4,
+    decode4_workspace_bytes,
 )

@@ -318,6 +318,12 @@ def test_cache_allocation_checks():
             b.cache4_empty(**kw)
 
 
+def test_the_workspace_size_is_reached_from_the_package():
+    b = _bsfa()
+    from block_sparse_gated_gb300 import cache4
+    assert b.decode4_workspace_bytes is cache4.decode4_workspace_bytes
+
+
 # ------------------------------------------------------------------ the oracle
 def test_oracle_format_by_hand():
     """The e4m3 table's landmarks, ties to the even code, saturation, the least
