@@ -308,10 +308,10 @@ bsfa_status bsfa_calibrate(const void* const* q_samples, const void* const* k_sa
  *     scale = min(max(e4m3(a / 6), 2^-9), 448),  code = e2m1(x' / scale),
  * both rounded to nearest, ties to the even code; magnitudes beyond 6 scales
  * saturate.  A group that holds an infinity or a NaN is stored as scale NaN
- * and reads back as NaN.  Scales keep 3 mantissa bits for a in [0.09, 2880];
- * exponents move that window to a head's values (e = ceil(log2(amax / 2688))
- * puts the largest value amax of a head at its top).  A value that rounds to
- * zero loses its sign.
+ * and reads back as NaN.  Scales keep 3 mantissa bits for a in [0.094, 2688];
+ * beyond it x' is cut to 2688.  Exponents move that window to a head's values:
+ * e = ceil(log2(amax / 2688)) puts the largest value amax of a head at its top.
+ * A value that rounds to zero loses its sign.
  */
 typedef struct {
   uint8_t* k;                 /* code bytes of the keys' pages */

@@ -3,6 +3,7 @@ the binding refuse before anything is launched, and the fp64 oracle's own
 format against hand-written values."""
 import ctypes
 import os
+import re
 import subprocess
 import tempfile
 
@@ -367,3 +368,20 @@ def test_oracle_attention_by_hand():
     assert out[0, 0, 1] == 0 and np.isneginf(lse[0, 0]) and np.isclose(out[0, 1, 1], 10.0)
     out, _, _, _, _ = co.attend(q, k, v, sigma=1.0, causal=False)
     assert np.allclose(out[0, :, 1], (3 * 10 + 9 * 20) / 12)
+
+
+def test_the_window_of_scales_that_the_header_states():
+    """Within it a group's scale is amax / 6 to 3 mantissa bits and its largest
+    element is kept to the half step of a scale; above it that element is cut."""
+    with open(os.path.join(ROOT, "include", "bsfa.h")) as f:
+        text = re.sub(r"\s*\n \*\s*", " ", f.read())
+    lo, hi = map(float, re.search(r"3 mantissa bits for a in \[([\d.]+), ([\d.]+)\]", text).groups())
+
+    def back(a):
+        code, byte = co.quantise(np.full(16, a))
+        return co.values(co.pack(code), byte)[0]
+
+    for a in np.geomspace(lo, hi, 2000):
+        assert abs(back(a) - a) <= a / 16
+    assert back(hi) == hi == back(hi * 1.001) == back(hi * 2)
+    assert 6 * 2.0 ** -6 <= lo <= 6 * 2.0 ** -6 * 1.01  # e4m3's least normal number
