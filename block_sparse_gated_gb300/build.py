@@ -53,6 +53,8 @@ def _compile(src: str, verbose_ptxas: bool) -> tuple[str, str]:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+    with open(obj + ".log", "w") as f:  # what the compiler had to say, spills among it
+        f.write(r.stdout + r.stderr)
     return obj, r.stdout + r.stderr
 
 

@@ -862,9 +862,11 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
 // of job x, which is segment x, or where there are more segments than CTAs the
 // one that CTA x began and did not finish -- if that was cut.  The parts lie in
 // the CTAs first (its second slot) .. last (their first slots).  The references
-// come first, all at once, so that the sums' loads wait for nothing.
+// come first, all at once, so that the sums' loads wait for nothing.  Four blocks
+// to an SM are asked for: left to itself the compiler keeps to 32 registers and
+// spills at d = 128 (61 registers; 1 x 128K: 34.4 -> 32.9 us).
 template <int D, int ROWS>
-__global__ void __launch_bounds__(JOIN_THREADS) decode4_join_kernel(const DecArgs a) {
+__global__ void __launch_bounds__(JOIN_THREADS, 4) decode4_join_kernel(const DecArgs a) {
   constexpr int LANES = D / 4;                 // threads that cover a row, four elements each
   constexpr int PARTS = JOIN_THREADS / LANES;  // parts read at once
   __shared__ float4 sh_y[PARTS][LANES];

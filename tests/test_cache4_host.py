@@ -194,6 +194,17 @@ def test_decode_parameters_that_are_refused(lib):
         assert lib.bsfa_decode4(c, ctypes.byref(p), None) == OK
 
 
+@pytest.mark.parametrize("source", ["bsfa_cache4", "bsfa_decode4"])
+def test_kernels_do_not_spill(lib, source):
+    """The compiler warns of registers that it spills to local memory."""
+    from block_sparse_gated_gb300 import build
+    log = os.path.join(build.OBJDIR, source + ".o.log")
+    if not os.path.exists(log):
+        pytest.skip("the library was built without a log")
+    with open(log) as f:
+        assert "are spilled" not in f.read()
+
+
 def _bsfa():
     import block_sparse_gated_gb300 as b
     return b
