@@ -59,6 +59,7 @@ constexpr float HEADROOM = 5.f;     // log2 a score may pass the reference by
 constexpr float SHIFT = 10.f;       // log2 of the factor that p carries: p < 2^15
 constexpr int MIN_UNITS = 4;        // shortest piece of the line worth a CTA
 constexpr int SEGMENT_UNITS = 8;    // a segment's fixed cost, in units
+constexpr int RUN_UNITS = 256;      // units of a segment summed at once, at most
 constexpr int JOIN_THREADS = 256;   // of the kernel that joins parts
 constexpr int JOIN_ROWS_PARTS = 8;  // a warp to a row below, a block above
 constexpr int MAX_PARTS = 768;      // parts of a segment, at most: CTAs of a cut call
@@ -171,7 +172,8 @@ template <int D>
 constexpr int MERGE_ROW = D + 12;
 
 // Dynamic shared memory: the rings, whose place the warps' sums take later, and
-// behind them what the CTAs of a cluster send each other.
+// behind them what the CTAs of a cluster send each other, or what a CTA carries
+// from one run of a segment to the next.
 template <int D, int NT, int W>
 constexpr int ring_bytes() {
   constexpr int ring = W * Shape<NT>::STAGES * Stage<D>::BYTES;
@@ -179,19 +181,19 @@ constexpr int ring_bytes() {
   return ring > merge ? ring : merge;
 }
 template <int D, int NT, int W>
-constexpr int smem_bytes(bool cluster) {
-  return ring_bytes<D, NT, W>() + (cluster ? rows_of(NT) * D * 4 : 0);
+constexpr int smem_bytes(bool more) {
+  return ring_bytes<D, NT, W>() + (more ? rows_of(NT) * D * 4 : 0);
 }
 
 // Where a CTA's piece of the line begins.
 struct Piece {
   int begin, end;   // units
   int b, base;      // sequence of `begin`, and the units before it
-  int per_cta;
 };
 
 // Cuts the line.  Every CTA adds up the lengths by itself: a few loads per
-// thread, no extra launch.
+// thread, no extra launch.  sh: a word for each warp, and behind them the piece's
+// b and base and the units of every piece.
 __device__ __forceinline__ Piece cut(const DecArgs& a, int* sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int chunk = (a.batch + THREADS - 1) / THREADS;
@@ -215,10 +217,10 @@ __device__ __forceinline__ Piece cut(const DecArgs& a, int* sh) {
   }
   Piece p;
   const int all = total * per_unit;
-  p.per_cta = max(MIN_UNITS, (all + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+  const int grid = static_cast<int>(gridDim.x), per_cta = max(MIN_UNITS, (all + grid - 1) / grid);
   p.begin = static_cast<int>(min(static_cast<long long>(all),
-                                 static_cast<long long>(blockIdx.x) * p.per_cta));
-  p.end = min(all, p.begin + p.per_cta);
+                                 static_cast<long long>(blockIdx.x) * per_cta));
+  p.end = min(all, p.begin + per_cta);
   const int at = p.begin / per_unit;
   if (at >= before && at < before + sum) {
     int base = before;
@@ -232,6 +234,7 @@ __device__ __forceinline__ Piece cut(const DecArgs& a, int* sh) {
       base += n;
     }
   }
+  if (tid == 0) sh[WARPS + 2] = per_cta;
   __syncthreads();
   p.b = sh[WARPS];
   p.base = sh[WARPS + 1];
@@ -269,12 +272,12 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
   constexpr int ROWS = rows_of(NTILES);
   using St = Stage<D>;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ int sh_cut[WARPS + 2];
+  __shared__ int sh_cut[WARPS + 3];
   __shared__ uint2 sh_q[NT * KSTEPS * 32];
   __shared__ float sh_sc[ROWS];
   __shared__ int sh_lim[ROWS];  // positions below it are visible to the row
   __shared__ float2 sh_ml[WARPS][ROWS];
-  __shared__ float2 sh_cluster[MAX_CLUSTER][ROWS];
+  __shared__ float2 sh_cluster[MAX_CLUSTER][ROWS];  // of a cluster's CTAs, or carried
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
@@ -294,9 +297,16 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
     piece.base = 0;
     piece.begin = (seg - piece.b * per_b) * n;
     piece.end = piece.begin + n;
-    piece.per_cta = n;
   }
 
+  // The tensor cores cut off what they add to a sum instead of rounding it, so O
+  // falls behind by about 2^-24 of itself with each of a warp's tiles where values
+  // have one sign (640 histories of 1M tokens, each in about one piece: 1.35e-3,
+  // three half steps of fp16).  So no more than RUN_UNITS of a segment are summed
+  // at once, 256 tiles to a warp (2^-16), and a CTA adds its runs in fp32.  Calls
+  // whose pieces are shorter pay 0.3 to 1.2% for it (64 ragged sequences to 16K
+  // 103.4 -> 103.8 us, five tokens over 16 to 32K 119.7 -> 121.4).
+  const bool cuts = W == bsfa::WARPS && a.split;
   const uint32_t my_ring = smem_u32(ring) + warp * STAGES * St::BYTES;
   int u = piece.begin, b = piece.b, base = piece.base;
   while (u < piece.end) {
@@ -304,7 +314,7 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
     const int n_units = units_of(len);
     const int seg = (u - base) / n_units;  // kvh * row_tiles + row tile
     const int u0 = u - base - seg * n_units;
-    const int u1 = min(n_units, u0 + piece.end - u);
+    const int u1 = min(n_units, u0 + min(piece.end - u, cuts ? RUN_UNITS : n_units));
     const int kvh = seg / a.row_tiles;
     const int r0 = (seg - kvh * a.row_tiles) * ROWS;  // first query row
     const int n_rows = min(ROWS, a.rows - r0);
@@ -816,8 +826,17 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
       }
       return;
     }
-    const bool whole = u0 == 0 && u1 == n_units;
-    const int part = 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0);
+    // Whether the segment began in this CTA, the runs of it that the CTA has
+    // summed before this one, and whether one follows.
+    const int seg_begin = u - u0, per_cta = cuts ? sh_cut[WARPS + 2] : 1;
+    const int cta_begin = cuts ? static_cast<int>(blockIdx.x) * per_cta : 0;
+    const bool began = seg_begin >= cta_begin;
+    const int carried = cuts ? (u - max(seg_begin, cta_begin)) / RUN_UNITS : 0;
+    const bool more = cuts && u1 < n_units && u + (u1 - u0) < piece.end;
+    float4* carry = reinterpret_cast<float4*>(ring + ring_bytes<D, NTILES, W>());
+    float2* const carry_ml = sh_cluster[carried & 1];  // and the next run's in the other
+    const bool whole = began && u1 == n_units;
+    const int part = 2 * static_cast<int>(blockIdx.x) + (began ? 1 : 0);
     for (int x = tid; x < n_rows * (D / 4); x += THREADS) {
       const int r = x / (D / 4), d0 = (x % (D / 4)) * 4;
       float m = sh_ml[0][r].x;
@@ -832,7 +851,21 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
         const float* src = merge + (w * ROWS + r) * MERGE_ROW<D> + merge_pos<D>(d0);
         y.x += src[0], y.y += src[1], y.z += src[2], y.w += src[3];
       }
-      if (whole) {
+      if (carried > 0) {
+        const float2 ml = carry_ml[r];
+        const float4 z = carry[x];
+        const float m1 = fmaxf(m, ml.x);
+        const float f = m1 == -INFINITY ? 1.f : ex2_approx(m - m1);
+        const float fz = m1 == -INFINITY ? 1.f : ex2_approx(ml.x - m1);
+        m = m1;
+        l = l * f + ml.y * fz;
+        y.x = y.x * f + z.x * fz, y.y = y.y * f + z.y * fz;
+        y.z = y.z * f + z.z * fz, y.w = y.w * f + z.w * fz;
+      }
+      if (more) {
+        carry[x] = y;
+        if (d0 == 0) sh_cluster[(carried & 1) ^ 1][r] = make_float2(m, l);
+      } else if (whole) {
         store_row4(a, b, kvh, r0 + r, d0, m, l, y);
       } else {
         *reinterpret_cast<float4*>(
@@ -840,9 +873,9 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
         if (d0 == 0) a.part_ml[static_cast<long long>(part) * ROWS + r] = make_float2(m, l);
       }
     }
-    if (u0 == 0 && tid == 0) {
+    if (cuts && began && !more && tid == 0) {
       const int4 job =
-          make_int4(whole ? -1 : b, seg, blockIdx.x, (u + n_units - 1) / piece.per_cta);
+          make_int4(whole ? -1 : b, seg, blockIdx.x, (seg_begin + n_units - 1) / per_cta);
       if (a.join_by_segment)
         a.joins[b * a.heads_kv * a.row_tiles + seg] = job;
       else if (!whole)
@@ -1124,7 +1157,7 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
     DecArgs a = args;
     a.join_by_segment = pl.segments <= grid;
     decode4_kernel<D, NT, DENSE, W>
-        <<<static_cast<unsigned>(grid), THREADS, smem_bytes<D, NT, W>(false), stream>>>(a);
+        <<<static_cast<unsigned>(grid), THREADS, smem_bytes<D, NT, W>(true), stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return BSFA_ERR_CUDA;
     // About grid / segments parts to a segment.
     const bool by_rows = grid < JOIN_ROWS_PARTS * pl.segments;

@@ -62,10 +62,11 @@ def random_cache(bsfa, lens, page, heads, d, seed, device, *, layout="phtd", exp
     return bsfa.KVCache4(*t, *e, layout), torch.from_numpy(table).to(device), rows
 
 
-def long_cache(bsfa, lens, page, heads, d, seed, device, *, layout="phtd", block=4000):
+def long_cache(bsfa, lens, page, heads, d, seed, device, *, layout="phtd", block=4000,
+               positive=False):
     """random_cache() for long sequences: the rows of every sequence repeat one
     quantised block of ``block`` tokens, each sequence from another place in it,
-    and no row is set by itself."""
+    and no row is set by itself.  ``positive``: values in [0.75, 1.25]."""
     rng = np.random.default_rng(seed)
     table, pool = table_for(lens, page, rng)
     out, rows = [], [[] for _ in lens]
@@ -73,6 +74,8 @@ def long_cache(bsfa, lens, page, heads, d, seed, device, *, layout="phtd", block
         x = rng.standard_normal((heads, block, d))
         if i == 0:
             x *= 0.5 + np.abs(rng.standard_normal((heads, 1, d)))
+        elif positive:
+            x = rng.uniform(0.75, 1.25, x.shape)
         code, byte = co.quantise(x)
         code = co.pack(code)
         stands = co.values(code, byte)

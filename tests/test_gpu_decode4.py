@@ -515,3 +515,48 @@ def test_a_launch_that_failed_leaves_no_error_behind(cuda_device):
     spare = b.cache4_empty(1, 2, 16, 64, device=cuda_device)
     b.cache4_write(spare, x, x, torch.zeros(1, 1, dtype=torch.int32, device=cuda_device))
     cu.check_decode(b.decode4(q, cache, table, n32), q, rows, [100], BF, 64)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads", [(4, 1), (8, 1), (12, 1), (4, 5), (32, 1)])
+def test_pieces_of_more_than_one_run(cuda_device, d, heads):
+    """650 histories of 20000 to 40000 tokens, read from the same pages: a CTA's
+    piece of a history is longer than what is summed at once, with histories that
+    begin and end within pieces."""
+    b = _bsfa()
+    Hq, n = heads
+    rng = np.random.default_rng(Hq + d)
+    cache, table, rows = cu.long_cache(b, [40000], 64, 1, d, Hq, cuda_device)
+    lens = [int(x) for x in rng.integers(20000, 40001, 650)]
+    q = _queries(650, Hq, n, d, HF, Hq, cuda_device, 1.5)
+    res = b.decode4(q, cache, table.repeat(650, 1), _i32(lens, cuda_device), return_lse=True)
+    some = [0, 1, 314, 649]
+    lse = res["lse"].view(Hq, 650, n)
+    for i in some:
+        cu.check_decode({"out": res["out"][i:i + 1], "lse": lse[:, i]}, q[i:i + 1], rows,
+                        [lens[i]], HF, d)
+
+
+def test_sums_of_a_million_values_of_one_sign(cuda_device):
+    """640 histories of 2^20 tokens, read from the same pages, each the work of
+    about one CTA: the tensor cores' sums do not fall behind."""
+    b = _bsfa()
+    L, d, B = 1 << 20, 64, 640
+    cache, table, rows = cu.long_cache(b, [L], 256, 1, d, 5, cuda_device, positive=True)
+    q = _queries(1, 1, 1, d, HF, 5, cuda_device, 0.3)
+    res = b.decode4(q.repeat(B, 1, 1, 1), cache, table.repeat(B, 1), _i32([L] * B, cuda_device),
+                    return_lse=True)
+    cu.check_decode({"out": res["out"][:1], "lse": res["lse"][:, :1]}, q, rows, [L], HF, d)
+    # The others are the same sum, cut elsewhere.  Output and weights are rounded to
+    # fp16 (2^-11 each), and a run of 256 tiles is 512 products added, each cut by less
+    # than 2^-23 of the sum (2^-14).  In the mean over 64 elements the roundings leave
+    # 2^-11 / sqrt(3 * 64) beside that.
+    want = rows[0][1][0].T @ _softmax(rows[0][0][0] @ q[0, 0, 0].cpu().double().numpy() / 8)
+    off = res["out"][:, 0, 0].cpu().double().numpy() / want - 1
+    assert abs(off).max() <= 2 * 2.0 ** -11 + 2.0 ** -14
+    assert abs(off.mean()) <= 3 * 2.0 ** -11 / math.sqrt(3 * 64) + 2.0 ** -14
+
+
+def _softmax(s):
+    p = np.exp(s - s.max())
+    return p / p.sum()
