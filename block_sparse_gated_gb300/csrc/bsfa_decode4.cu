@@ -189,11 +189,11 @@ constexpr int smem_bytes(bool more) {
 struct Piece {
   int begin, end;   // units
   int b, base;      // sequence of `begin`, and the units before it
+  int per_cta;
 };
 
 // Cuts the line.  Every CTA adds up the lengths by itself: a few loads per
-// thread, no extra launch.  sh: a word for each warp, and behind them the piece's
-// b and base and the units of every piece.
+// thread, no extra launch.
 __device__ __forceinline__ Piece cut(const DecArgs& a, int* sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int chunk = (a.batch + THREADS - 1) / THREADS;
@@ -217,10 +217,10 @@ __device__ __forceinline__ Piece cut(const DecArgs& a, int* sh) {
   }
   Piece p;
   const int all = total * per_unit;
-  const int grid = static_cast<int>(gridDim.x), per_cta = max(MIN_UNITS, (all + grid - 1) / grid);
+  p.per_cta = max(MIN_UNITS, (all + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
   p.begin = static_cast<int>(min(static_cast<long long>(all),
-                                 static_cast<long long>(blockIdx.x) * per_cta));
-  p.end = min(all, p.begin + per_cta);
+                                 static_cast<long long>(blockIdx.x) * p.per_cta));
+  p.end = min(all, p.begin + p.per_cta);
   const int at = p.begin / per_unit;
   if (at >= before && at < before + sum) {
     int base = before;
@@ -234,7 +234,6 @@ __device__ __forceinline__ Piece cut(const DecArgs& a, int* sh) {
       base += n;
     }
   }
-  if (tid == 0) sh[WARPS + 2] = per_cta;
   __syncthreads();
   p.b = sh[WARPS];
   p.base = sh[WARPS + 1];
@@ -258,7 +257,16 @@ __device__ __forceinline__ void store_row4(const DecArgs& a, int b, int kvh, int
 
 // DENSE: the tokens of a page lie together in each pool, so that the strides of
 // the copies are constants.
-template <int D, int NTILES, bool DENSE, int W>
+//
+// RUNS: of a call whose pieces may be longer than RUN_UNITS.  The tensor cores cut
+// off what they add to a sum instead of rounding it, so O falls behind by about
+// 2^-24 of itself with each of a warp's tiles where values have one sign (640
+// histories of 1M tokens, each in about one piece: 1.35e-3, three half steps of
+// fp16).  So no more than RUN_UNITS of a segment are summed at once, 256 tiles to
+// a warp (2^-16), and a CTA adds its runs in fp32.  (A kernel of its own: in one
+// for all, shorter pieces paid for it, 64 x 4K 39.0 -> 39.6 us, five tokens over 16
+// to 32K 119.6 -> 120.9; as it is 39.1 and 120.0.)
+template <int D, int NTILES, bool DENSE, int W, bool RUNS>
 __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WARPS / W : 1)
     decode4_kernel(const DecArgs a) {
   constexpr bool HALF = NTILES == 0;
@@ -272,7 +280,7 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
   constexpr int ROWS = rows_of(NTILES);
   using St = Stage<D>;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ int sh_cut[WARPS + 3];
+  __shared__ int sh_cut[WARPS + 2];
   __shared__ uint2 sh_q[NT * KSTEPS * 32];
   __shared__ float sh_sc[ROWS];
   __shared__ int sh_lim[ROWS];  // positions below it are visible to the row
@@ -297,16 +305,9 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
     piece.base = 0;
     piece.begin = (seg - piece.b * per_b) * n;
     piece.end = piece.begin + n;
+    piece.per_cta = n;
   }
 
-  // The tensor cores cut off what they add to a sum instead of rounding it, so O
-  // falls behind by about 2^-24 of itself with each of a warp's tiles where values
-  // have one sign (640 histories of 1M tokens, each in about one piece: 1.35e-3,
-  // three half steps of fp16).  So no more than RUN_UNITS of a segment are summed
-  // at once, 256 tiles to a warp (2^-16), and a CTA adds its runs in fp32.  Calls
-  // whose pieces are shorter pay 0.3 to 1.2% for it (64 ragged sequences to 16K
-  // 103.4 -> 103.8 us, five tokens over 16 to 32K 119.7 -> 121.4).
-  const bool cuts = W == bsfa::WARPS && a.split;
   const uint32_t my_ring = smem_u32(ring) + warp * STAGES * St::BYTES;
   int u = piece.begin, b = piece.b, base = piece.base;
   while (u < piece.end) {
@@ -314,7 +315,8 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
     const int n_units = units_of(len);
     const int seg = (u - base) / n_units;  // kvh * row_tiles + row tile
     const int u0 = u - base - seg * n_units;
-    const int u1 = min(n_units, u0 + min(piece.end - u, cuts ? RUN_UNITS : n_units));
+    const int left = RUNS ? min(RUN_UNITS, piece.end - u) : piece.end - u;
+    const int u1 = min(n_units, u0 + left);
     const int kvh = seg / a.row_tiles;
     const int r0 = (seg - kvh * a.row_tiles) * ROWS;  // first query row
     const int n_rows = min(ROWS, a.rows - r0);
@@ -828,11 +830,11 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
     }
     // Whether the segment began in this CTA, the runs of it that the CTA has
     // summed before this one, and whether one follows.
-    const int seg_begin = u - u0, per_cta = cuts ? sh_cut[WARPS + 2] : 1;
-    const int cta_begin = cuts ? static_cast<int>(blockIdx.x) * per_cta : 0;
-    const bool began = seg_begin >= cta_begin;
-    const int carried = cuts ? (u - max(seg_begin, cta_begin)) / RUN_UNITS : 0;
-    const bool more = cuts && u1 < n_units && u + (u1 - u0) < piece.end;
+    const int seg_begin = u - u0;
+    const int cta_begin = static_cast<int>(blockIdx.x) * piece.per_cta;
+    const bool began = RUNS ? seg_begin >= cta_begin : u0 == 0;
+    const int carried = RUNS ? (u - max(seg_begin, cta_begin)) / RUN_UNITS : 0;
+    const bool more = RUNS && u1 < n_units && u + (u1 - u0) < piece.end;
     float4* carry = reinterpret_cast<float4*>(ring + ring_bytes<D, NTILES, W>());
     float2* const carry_ml = sh_cluster[carried & 1];  // and the next run's in the other
     const bool whole = began && u1 == n_units;
@@ -851,7 +853,7 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
         const float* src = merge + (w * ROWS + r) * MERGE_ROW<D> + merge_pos<D>(d0);
         y.x += src[0], y.y += src[1], y.z += src[2], y.w += src[3];
       }
-      if (carried > 0) {
+      if (RUNS && carried > 0) {
         const float2 ml = carry_ml[r];
         const float4 z = carry[x];
         const float m1 = fmaxf(m, ml.x);
@@ -873,9 +875,9 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
         if (d0 == 0) a.part_ml[static_cast<long long>(part) * ROWS + r] = make_float2(m, l);
       }
     }
-    if (cuts && began && !more && tid == 0) {
+    if (began && !more && tid == 0) {
       const int4 job =
-          make_int4(whole ? -1 : b, seg, blockIdx.x, (seg_begin + n_units - 1) / per_cta);
+          make_int4(whole ? -1 : b, seg, blockIdx.x, (seg_begin + n_units - 1) / piece.per_cta);
       if (a.join_by_segment)
         a.joins[b * a.heads_kv * a.row_tiles + seg] = job;
       else if (!whole)
@@ -1122,20 +1124,35 @@ bsfa_status status_of(cudaError_t e) {
   return BSFA_ERR_CUDA;
 }
 
-template <int D, int NT, bool DENSE, int W = WARPS>
-bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaStream_t stream) {
-  constexpr int smem = smem_bytes<D, NT, W>(true);
-  static_assert(Shape<NT>::MAX_GRID <= MAX_PARTS, "the join's weights");
-  // The shared-memory size of a kernel is set once per device.
+// Sets a kernel's shared-memory size, once per device.
+template <int D, int NT, bool DENSE, int W, bool RUNS>
+bsfa_status prepare(int dev) {
   static std::atomic<uint64_t> ready{0};
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    const bsfa_status v = status_of(cudaFuncSetAttribute(
-        decode4_kernel<D, NT, DENSE, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    if (v != BSFA_OK) return v;
-    ready.fetch_or(bit, std::memory_order_relaxed);
-  }
+  if (ready.load(std::memory_order_relaxed) & bit) return BSFA_OK;
+  const bsfa_status v = status_of(cudaFuncSetAttribute(decode4_kernel<D, NT, DENSE, W, RUNS>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       smem_bytes<D, NT, W>(true)));
+  if (v == BSFA_OK) ready.fetch_or(bit, std::memory_order_relaxed);
+  return v;
+}
+
+// The first kernel of a call that cuts.
+template <int D, int NT, bool DENSE, bool RUNS>
+bsfa_status launch_cut(const DecArgs& a, int grid, int dev, cudaStream_t stream) {
+  const bsfa_status v = prepare<D, NT, DENSE, WARPS, RUNS>(dev);
+  if (v != BSFA_OK) return v;
+  decode4_kernel<D, NT, DENSE, WARPS, RUNS>
+      <<<static_cast<unsigned>(grid), THREADS, smem_bytes<D, NT, WARPS>(RUNS), stream>>>(a);
+  return status_of(cudaGetLastError());
+}
+
+template <int D, int NT, bool DENSE, int W = WARPS>
+bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaStream_t stream) {
+  static_assert(Shape<NT>::MAX_GRID <= MAX_PARTS, "the join's weights");
   if (!pl.split) {
+    const bsfa_status v = prepare<D, NT, DENSE, W, false>(dev);
+    if (v != BSFA_OK) return v;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(pl.segments * pl.cluster));
     cfg.blockDim = dim3(32 * W);
@@ -1147,18 +1164,20 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return status_of(cudaLaunchKernelEx(&cfg, decode4_kernel<D, NT, DENSE, W>, args));
+    return status_of(cudaLaunchKernelEx(&cfg, decode4_kernel<D, NT, DENSE, W, false>, args));
   }
   if constexpr (W == WARPS) {  // other CTAs never cut
     const long long full = static_cast<long long>(sms) * Shape<NT>::CTAS;
-    long long grid = full < pl.max_grid ? full : pl.max_grid;
+    int grid = static_cast<int>(full < pl.max_grid ? full : pl.max_grid);
     const long long most = (pl.all_units + MIN_UNITS - 1) / MIN_UNITS;
-    if (most < grid) grid = most;
+    if (most < grid) grid = static_cast<int>(most);
     DecArgs a = args;
     a.join_by_segment = pl.segments <= grid;
-    decode4_kernel<D, NT, DENSE, W>
-        <<<static_cast<unsigned>(grid), THREADS, smem_bytes<D, NT, W>(true), stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return BSFA_ERR_CUDA;
+    // The lengths' bound bounds the pieces.
+    const bool runs = (pl.all_units + grid - 1) / grid > RUN_UNITS;
+    const bsfa_status v = runs ? launch_cut<D, NT, DENSE, true>(a, grid, dev, stream)
+                               : launch_cut<D, NT, DENSE, false>(a, grid, dev, stream);
+    if (v != BSFA_OK) return v;
     // About grid / segments parts to a segment.
     const bool by_rows = grid < JOIN_ROWS_PARTS * pl.segments;
     constexpr int ROWS = rows_of(NT);
