@@ -78,10 +78,10 @@ constexpr int WIDE_UNITS = 32;      // units of a segment per CTA of that size, 
 constexpr int rows_of(int nt) { return nt == 0 ? 4 : 8 * nt; }
 
 // Per row-tile width: CTAs per SM, ring stages, whether the main loop goes around
-// the ring in one piece (64 ragged sequences to 16K, NT = 1: 121 us by single
-// tiles, 118 unrolled with 5 stages, 115 with 4; five tokens over 16 to 32K, NT =
-// 3: 133 and 141), and the most CTAs a launch has (the workspace holds two partial
-// results each).
+// the ring in one piece (64 ragged sequences to 16K, four and eight query rows:
+// 105.4 and 119.4 us by single tiles, 104.0 and 111.2 unrolled, with five stages
+// 106.2 and 111.9; five tokens over 16 to 32K, NT = 3: 119.6, unrolled 123.6), and
+// the most CTAs a launch has (the workspace holds two partial results each).
 template <int NT>
 struct Shape;
 template <>
@@ -489,7 +489,9 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
       constexpr bool MASKED = decltype(masked_tag)::value;
       // ---- S^T = K Q^T.  Three row tiles leave registers for two sums per tile,
       // which halves the chain of dependent products (five tokens over 16 to 32K:
-      // 122.8 -> 120.5 us; one and two row tiles lose by it).
+      // 121.6 -> 119.9 us).  One row tile gains nothing by it, two and four lose (64
+      // ragged sequences to 16K with twelve rows 145.6 and 154.6, eight tokens over
+      // 16 to 32K 148.4 and 149.8).
       constexpr int SUMS = NT == 3 ? 2 : 1;
       float s[NT][4], s2[SUMS == 2 ? NT : 1][4];
 #pragma unroll
@@ -594,6 +596,13 @@ __global__ void __launch_bounds__(32 * W, W <= WARPS ? Shape<NTILES>::CTAS * WAR
           }
         weigh();
       }
+      // The products take 16-bit factors, so a weight is rounded to fp16, 2^-11 of
+      // it at most; the sum l, and with it the log-sum-exp, is that of the weights
+      // before.  Against 64 bits an fp16 O is off by 2.6e-4 (2-norm, 256 ragged
+      // sequences to 600) where its own rounding alone is 2.1e-4, a bf16 O by its
+      // rounding, 1.66e-3.  A second product with the weights' remainders makes O as
+      // exact as fp32 weights do, for 104 -> 117 us at 64 ragged sequences to 16K and
+      // 120 -> 151 for five tokens.
       uint32_t pb[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -965,10 +974,14 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) decode4_join_kernel(const Dec
   store_row4(a, b, kvh, row, 4 * lane, m, l, y);
 }
 
-// The same where a segment has few parts: a warp takes a row of job x by itself,
-// 32 parts' references at a time (five tokens over 16 sequences to 32K, about
-// four parts to each of 2560 rows: 125.5 us, and 128.8 with a block to a row; 1 x
-// 128K, 76 parts: 46.1 and 36.4).
+// The same where segments have few parts: a warp takes a row of job x by itself,
+// 32 parts' references at a time (by rows and by blocks: 64 ragged sequences to
+// 16K, about one part to a row, 104.1 and 106.8 us; five tokens over 16 ragged
+// sequences to 32K, two, 119.3 and 122.7; 12 x 32K, six, 76.4 and 75.9; 8 x 64K,
+// ten, 99.3 and 98.0; 4 x 64K, 19, 57.6 and 55.2; 1 x 128K, 76, 44.4 and 34.4).  The
+// choice goes by the average, which one long history among many short ones
+// misleads: 300 of 20 tokens and one of 128K on one KV head take 47.4 us, by blocks
+// 21.1.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(JOIN_THREADS) decode4_join_rows_kernel(const DecArgs a) {
   constexpr int E = D / 32;  // elements of a lane
@@ -1047,6 +1060,9 @@ Plan plan_of(const bsfa_cache4* c, const bsfa_decode4_params* p) {
   constexpr int grids[5] = {Shape<0>::MAX_GRID, Shape<1>::MAX_GRID, Shape<2>::MAX_GRID,
                             Shape<3>::MAX_GRID, Shape<4>::MAX_GRID};
   pl.max_grid = grids[pl.nt];
+  // CTAs of other sizes than four warps are for eight query rows at most: a thread
+  // of more needs over 128 registers, which a CTA of 16 warps does not have, and
+  // CTAs of two were not tried there.
   // Few segments, of half a thousand tokens or more: a CTA of 16 warps to an SM
   // (19 ragged sequences to 1024: 13.8 -> 9.5 us; 1 x 4097: 9.4 -> 8.8; 1 x 300
   // would go from 6.6 to 7.1).  Otherwise CTAs of four, or where those would not

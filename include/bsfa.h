@@ -384,7 +384,9 @@ bsfa_status bsfa_cache4_read(const bsfa_cache4* cache, const bsfa_cache4_rows* r
  * values are exact in fp16, and the weights are rounded to fp16 (11 bits).
  * Queries are scaled per row by a power of two, whatever their size, and are
  * exact as long as a row's elements lie within 2^28 of its largest; a smaller
- * one is off by at most 2^-39 of the largest.  O is rounded to dtype once.
+ * one is off by at most 2^-39 of the largest.  O is rounded to dtype once; the
+ * weights' rounding adds a quarter to the error of an fp16 O (2.6e-4 where the
+ * last rounding alone is 2.1e-4, in the 2-norm) and 1% to that of a bf16 O.
  */
 typedef struct {
   const void* q;              /* [batch, Hq, q_len, d] by strides */
