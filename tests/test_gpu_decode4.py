@@ -517,16 +517,17 @@ def test_a_launch_that_failed_leaves_no_error_behind(cuda_device):
     cu.check_decode(b.decode4(q, cache, table, n32), q, rows, [100], BF, 64)
 
 
+@pytest.mark.parametrize("layout", ["phtd", "pthd"])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("heads", [(4, 1), (8, 1), (12, 1), (4, 5), (32, 1)])
-def test_pieces_of_more_than_one_run(cuda_device, d, heads):
+def test_pieces_of_more_than_one_run(cuda_device, layout, d, heads):
     """650 histories of 20000 to 40000 tokens, read from the same pages: a CTA's
     piece of a history is longer than what is summed at once, with histories that
     begin and end within pieces."""
     b = _bsfa()
     Hq, n = heads
     rng = np.random.default_rng(Hq + d)
-    cache, table, rows = cu.long_cache(b, [40000], 64, 1, d, Hq, cuda_device)
+    cache, table, rows = cu.long_cache(b, [40000], 64, 1, d, Hq, cuda_device, layout=layout)
     lens = [int(x) for x in rng.integers(20000, 40001, 650)]
     q = _queries(650, Hq, n, d, HF, Hq, cuda_device, 1.5)
     res = b.decode4(q, cache, table.repeat(650, 1), _i32(lens, cuda_device), return_lse=True)
@@ -560,3 +561,37 @@ def test_sums_of_a_million_values_of_one_sign(cuda_device):
 def _softmax(s):
     p = np.exp(s - s.max())
     return p / p.sum()
+
+
+def test_graphs_follow_the_lengths_over_more_than_one_run(cuda_device):
+    """A captured call whose bound allows long pieces, replayed for long histories
+    and for short ones, with another call on another stream beside it."""
+    b = _bsfa()
+    from block_sparse_gated_gb300 import cache4
+    B, d = 650, 64
+    cache, table, rows = cu.long_cache(b, [30000], 64, 1, d, 8, cuda_device)
+    table = table.repeat(B, 1)
+    q = [_queries(B, 4, 1, d, HF, s, cuda_device) for s in (1, 2)]
+    n32 = _i32([30000] * B, cuda_device)
+    need = cache4.decode4_workspace_bytes(q[0], cache, table, n32)
+    outs, graphs, ws = [torch.empty_like(x) for x in q], [], []
+    for i in range(2):
+        ws.append(torch.empty(need, dtype=torch.uint8, device=cuda_device))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            b.decode4(q[i], cache, table, n32, out=outs[i], workspace=ws[i])
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    rng = np.random.default_rng(8)
+    for lo, hi in ((25000, 30001), (0, 40), (0, 30001)):
+        now = [int(x) for x in rng.integers(lo, hi, B)]
+        n32.copy_(_i32(now, cuda_device))
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+                g.replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            for j in (0, 77, 649):
+                cu.check_decode({"out": outs[i][j:j + 1]}, q[i][j:j + 1], rows, [now[j]], HF, d)
