@@ -14,6 +14,13 @@ from .api import (  # noqa: F401
     calibrate,
     prefill,
 )
+from .cache16 import (  # noqa: F401
+    KVCache16,
+    Rope,
+    cache16_empty,
+    cache16_write,
+    rotary,
+)
 from .cache4 import (  # noqa: F401
     KVCache4,
     cache4_empty,

@@ -70,10 +70,45 @@ class Decode4Params(ctypes.Structure):
     ]
 
 
-# The same three as struct formats, fields in the same order.
+class Cache16(ctypes.Structure):
+    """Mirror of bsfa_cache16."""
+    _fields_ = [
+        ("k", c_void_p), ("v", c_void_p), ("k_stride", c_int64 * 3), ("v_stride", c_int64 * 3),
+        ("num_pages", c_int), ("page_size", c_int), ("num_heads_kv", c_int),
+        ("head_dim", c_int),
+        ("block_table", c_void_p), ("block_table_stride", c_int), ("block_table_width", c_int),
+        ("dtype", c_int),
+    ]
+
+
+class Rope(ctypes.Structure):
+    """Mirror of bsfa_rope."""
+    _fields_ = [
+        ("inv_freq", c_void_p), ("positions", c_void_p), ("position_stride", c_int64 * 2),
+        ("pairs", c_int), ("interleaved", c_int), ("inverse", c_int), ("num_axes", c_int),
+        ("axis", ctypes.c_uint8 * 64),
+    ]
+
+
+class Rows16(ctypes.Structure):
+    """Mirror of bsfa_rows16."""
+    _fields_ = [
+        ("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("q_out", c_void_p),
+        ("k_out", c_void_p),
+        ("q_stride", c_int64 * 3), ("k_stride", c_int64 * 3), ("v_stride", c_int64 * 3),
+        ("q_out_stride", c_int64 * 3), ("k_out_stride", c_int64 * 3),
+        ("batch", c_int), ("num_heads_q", c_int), ("num_heads_kv", c_int), ("seqlen", c_int),
+        ("head_dim", c_int), ("cu_seqlens", c_void_p), ("start", c_void_p), ("dtype", c_int),
+    ]
+
+
+# The same as struct formats, fields in the same order.
 CACHE4 = struct.Struct("@6P12q4iP2i")
 CACHE4_ROWS = struct.Struct("@2P6q2i2Pi0P")
 DECODE4 = struct.Struct("@2P6q3iPifiPPNi0P")
+CACHE16 = struct.Struct("@2P6q4iP3i0P")
+ROPE = struct.Struct("@2P2q4i64s")
+ROWS16 = struct.Struct("@5P15q5i2Pi0P")
 
 
 # bsfa_dtype
@@ -104,6 +139,8 @@ SIGNATURES = [
     ("bsfa_cache4_read", c_int, [c_void_p, c_void_p, c_void_p]),
     ("bsfa_decode4_workspace_size", c_size_t, [c_void_p, c_void_p]),
     ("bsfa_decode4", c_int, [c_void_p, c_void_p, c_void_p]),
+    ("bsfa_rotary", c_int, [c_void_p, c_void_p, c_void_p]),
+    ("bsfa_cache16_write", c_int, [c_void_p, c_void_p, c_void_p, c_void_p]),
     ("bsfa_selftest_wait_guard", c_int, [ctypes.c_uint, c_void_p]),
 ]
 

@@ -1,0 +1,250 @@
+"""Rotary positions and the 16-bit paged K/V cache: torch-facing wrappers over
+the C ABI (argument marshalling only).
+
+The calls around a prefill over pages: ``cache16_write`` rotates queries and keys
+by their positions and puts keys and values into the page pools that ``prefill``
+reads through a block table; ``rotary`` rotates without a cache.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple, Optional, Sequence
+
+import torch
+
+from . import _native
+from .api import _DTYPES, _on_device
+from .cache4 import _BAD_TABLE, _I32, _call, _empty, _int32_vector, _strides
+
+MAX_AXES = 4
+
+
+class KVCache16(NamedTuple):
+    """Page pools of a 16-bit cache: views into memory that the caller owns.
+
+    ``layout`` "phtd" (the default, and the faster one for single tokens: a head's
+    tokens lie together): bf16 or fp16 [pages, Hkv, page_size, d]; "pthd": [pages,
+    page_size, Hkv, d].  ``prefill`` takes the same pools:
+    ``prefill(q, cache.k, cache.v, block_table=..., kv_layout=cache.layout)``."""
+    k: torch.Tensor
+    v: torch.Tensor
+    layout: str = "phtd"
+
+
+class Rope(NamedTuple):
+    """A rotation: ``inv_freq`` float32 [pairs] on the device (a multiple of 8, at
+    most half the head dimension; elements behind the last pair pass).  Pair j of
+    a row is turned by position * inv_freq[j], with the position on axis
+    ``axes[j]`` (None: one axis; at most 4, such as time, height and width).
+    Pairs are elements j and j + pairs, or with ``interleaved`` 2j and 2j + 1."""
+    inv_freq: torch.Tensor
+    axes: Optional[Sequence[int]] = None
+    interleaved: bool = False
+
+
+def cache16_empty(num_pages: int, num_heads_kv: int, page_size: int, head_dim: int, *,
+                  layout: str = "phtd", dtype=torch.bfloat16, device="cuda") -> KVCache16:
+    """Pools of zeros for ``num_pages`` pages of ``page_size`` tokens (a multiple
+    of 16; for a prefill over them, of 128) of ``num_heads_kv`` heads."""
+    if layout not in ("phtd", "pthd"):
+        raise ValueError(layout)
+    if head_dim not in (64, 128) or page_size <= 0 or page_size % 16:
+        raise ValueError("head_dim must be 64 or 128 and page_size a positive multiple of 16")
+    if dtype not in _DTYPES:
+        raise TypeError("expected bfloat16 or float16")
+    inner = (num_heads_kv, page_size) if layout == "phtd" else (page_size, num_heads_kv)
+    return KVCache16(*[torch.zeros(num_pages, *inner, head_dim, dtype=dtype, device=device)
+                       for _ in range(2)], layout)
+
+
+def _cache_fields(cache: KVCache16, block_table: torch.Tensor, device, batch: int):
+    """The packed bsfa_cache16 of a call on ``device`` with ``batch`` sequences,
+    its heads, head dimension and element type, and the tokens that a row of the
+    block table can hold."""
+    k, v, layout = cache
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError("page pools are 4-D")
+    n, x, y, d = shape
+    if layout == "phtd":
+        heads, page, h, t = x, y, 1, 2
+    elif layout == "pthd":
+        heads, page, h, t = y, x, 2, 1
+    else:
+        raise ValueError(layout)
+    index = device.index
+    if device.type != "cuda" or not k.get_device() == v.get_device() == \
+            block_table.get_device() == index:
+        _on_device(device, k=k, v=v, block_table=block_table)
+    a, b = k.stride(), v.stride()
+    code = _DTYPES.get(k.dtype)
+    if code is None or v.dtype is not k.dtype:
+        raise TypeError("page pools are bfloat16 or float16, both of one type")
+    if v.shape != shape or a[3] != 1 or b[3] != 1:
+        raise ValueError("K and V pools must have one shape, with the head dimension contiguous")
+    if block_table.dtype is not _I32 or block_table.dim() != 2:
+        raise ValueError(_BAD_TABLE)
+    rows, width = block_table.shape
+    pitch, unit = block_table.stride()
+    if unit != 1 and width > 1:
+        raise ValueError(_BAD_TABLE)
+    if rows < batch:
+        raise ValueError("block_table has fewer rows than sequences")
+    return _native.CACHE16.pack(
+        k.data_ptr(), v.data_ptr(), a[0], a[h], a[t], b[0], b[h], b[t], n, page, heads, d,
+        block_table.data_ptr(), pitch if rows > 1 else width, width, code), heads, d, code, \
+        width * page
+
+
+def _rope_fields(rope: Rope, positions, inverse: bool, varlen: bool, batch: int, n: int, device):
+    """The packed bsfa_rope of a call on n rows of each of ``batch`` sequences, or
+    on n packed rows."""
+    f, axes, interleaved = rope
+    if f.dtype is not torch.float32 or f.dim() != 1 or not f.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float32 [pairs] tensor")
+    pairs = f.shape[0]
+    if not 0 < pairs <= 64:
+        raise ValueError("inv_freq must have 1 to 64 pairs")
+    if f.get_device() != device.index:
+        _on_device(device, inv_freq=f)
+    if axes is None:
+        code, num_axes = b"", 1
+    else:
+        if len(axes) != pairs or min(axes) < 0 or max(axes) >= MAX_AXES:
+            raise ValueError(f"axes must name one of at most {MAX_AXES} axes for each pair")
+        code, num_axes = bytes(axes), max(axes) + 1
+    at = axis_stride = batch_stride = 0
+    if positions is not None:
+        want = (n,) if varlen else (batch, n)
+        shape = tuple(positions.shape)
+        if shape == want and num_axes == 1:
+            strides = (0, *positions.stride())
+        elif shape[1:] == want and num_axes <= shape[0] <= MAX_AXES:
+            strides = positions.stride()
+        else:
+            raise ValueError(f"positions must be an int32 [axes, {', '.join(map(str, want))}] tensor")
+        if positions.dtype is not _I32 or (strides[-1] != 1 and n > 1):
+            raise ValueError("positions must be int32 with the positions of a sequence contiguous")
+        if positions.get_device() != device.index:
+            _on_device(device, positions=positions)
+        at, axis_stride = positions.data_ptr(), strides[0]
+        batch_stride = 0 if varlen else strides[1]
+    return _native.ROPE.pack(f.data_ptr(), at, axis_stride, batch_stride, pairs,
+                             1 if interleaved else 0, 1 if inverse else 0, num_axes, code)
+
+
+_NONE = (0, 0, 0)
+
+
+def _rows_fields(q, k, v, q_out, k_out, layout, cu_seqlens, start, device):
+    """The packed bsfa_rows16 of a call (q, v and k_out may be None, and k where
+    q is not), its number of sequences, rows (of each sequence or packed), KV
+    heads, head dimension and element type, and whether the rows are packed."""
+    varlen = cu_seqlens is not None
+    if layout is None:
+        layout = "htd" if varlen else "bhld"
+    one = k if k is not None else q
+    shape, dtype, index = one.shape, one.dtype, device.index
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError("expected a bfloat16 or float16 tensor")
+    heads, rows, d = [0, 0], None, shape[-1]
+    given = []
+    for which, t, like in ((0, q, None), (1, k, None), (1, v, k), (0, q_out, q), (1, k_out, k)):
+        if t is None:
+            given.append((0, _NONE))
+            continue
+        size = t.shape
+        if t.dtype is not dtype:
+            raise TypeError("all rows must share one element type")
+        if device.type != "cuda" or t.get_device() != index:
+            _on_device(device, rows=t)
+        s, h, n = _strides(t, size, t.stride(), layout, varlen)
+        if like is not None and size != like.shape:
+            raise ValueError("tensors of one kind must have one shape")
+        if size[-1] != d or len(size) != len(shape) or rows not in (None, n) or \
+                len(size) == 4 and size[0] != shape[0]:
+            raise ValueError("Q, K and V shapes disagree")
+        rows, heads[which] = n, h
+        given.append((t.data_ptr(), s))
+    cu = first = 0
+    if varlen:
+        if cu_seqlens.dtype is not _I32 or cu_seqlens.dim() != 1 or \
+                not cu_seqlens.is_contiguous() or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be a contiguous int32 [batch + 1] tensor")
+        if cu_seqlens.get_device() != index:
+            _on_device(device, cu_seqlens=cu_seqlens)
+        batch, cu = cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
+    else:
+        batch = 1 if len(shape) == 3 else shape[0]
+    if start is not None:
+        first = _int32_vector(start, batch, "start")
+        if start.get_device() != index:
+            _on_device(device, start=start)
+    (qp, qs), (kp, ks), (vp, vs), (qo, qos), (ko, kos) = given
+    return _native.ROWS16.pack(qp, kp, vp, qo, ko, *qs, *ks, *vs, *qos, *kos, batch, heads[0],
+                               heads[1], rows, d, cu, first, code), \
+        batch, rows, heads[1], d, code, varlen
+
+
+def rotary(rope: Rope, q, k=None, *, positions=None, start=None, cu_seqlens=None, layout=None,
+           inverse=False, out=None, stream=None):
+    """Queries and keys rotated by their positions; returns (q', k'), k' None
+    without k.  Batched: q [B, Hq, L, d] and k [B, Hkv, L, d] (layout "bhld") or
+    [B, L, H, d] ("blhd"), or [H, L, d] for one sequence; varlen (cu_seqlens int32
+    on the device): [H, T, d] ("htd") or [T, H, d] ("thd"), rows outside every
+    sequence are left as they are.
+
+    Row i of sequence b has the position start[b] + i on every axis (``start``
+    int32 [B] on the device, None: 0), or what ``positions`` says: int32 [axes, B,
+    L] batched, [axes, T] varlen, without the first dimension where there is one
+    axis.  Angles are exact at any position; products are formed in fp32 and
+    rounded once.
+
+    ``inverse`` turns back.  It is also the gradient: of the rotated rows' it
+    makes the rows'.  ``out``, a pair of tensors, may be (q, k) themselves; other
+    tensors must not overlap them."""
+    dev = q.device
+    varlen = cu_seqlens is not None
+    if out is None:
+        q_out = torch.empty_like(q) if stream is None else _empty(stream, dev, q.shape, q.dtype)
+        k_out = None if k is None else torch.empty_like(k) if stream is None else \
+            _empty(stream, dev, k.shape, k.dtype)
+    else:
+        q_out, k_out = out
+        if (k_out is None) != (k is None):
+            raise ValueError("out must be a pair, with None where there is no k")
+    r, batch, n, *_ = _rows_fields(q, k, None, q_out, k_out, layout, cu_seqlens, start, dev)
+    f = _rope_fields(rope, positions, inverse, varlen, batch, n, dev)
+    _call(_native.lib().bsfa_rotary, dev, stream, f, r)
+    return q_out, k_out
+
+
+def cache16_write(cache: KVCache16, k, v, block_table, *, rope: Optional[Rope] = None, q=None,
+                  positions=None, start=None, cu_seqlens=None, layout=None, q_out=None,
+                  stream=None):
+    """Keys and values into the cache, the keys rotated on the way where there is
+    a ``rope``, and with ``q`` the queries of the same tokens rotated beside them
+    (returned: ``q_out``, else a new tensor; None without q).  Layouts, ``start``
+    and ``positions`` as for ``rotary``.  Row i of sequence b becomes cache
+    position start[b] + i, whatever its rotary positions are: token pos %
+    page_size of page block_table[b, pos // page_size].  A position beyond the
+    table, or an entry outside the pool, is dropped.  The positions of one call
+    must differ."""
+    dev = k.device
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    elif rope is None:
+        raise ValueError("q is only rotated: it needs a rope")
+    elif q_out is None:
+        q_out = torch.empty_like(q) if stream is None else _empty(stream, dev, q.shape, q.dtype)
+    if rope is None and positions is not None:
+        raise ValueError("positions without a rope")
+    r, batch, n, heads, d, code, varlen = _rows_fields(q, k, v, q_out, None, layout, cu_seqlens,
+                                                       start, dev)
+    c, *have, _ = _cache_fields(cache, block_table, dev, batch)
+    if have != [heads, d, code]:
+        raise ValueError("K and V must have the cache's heads, head dimension and type")
+    f = None if rope is None else _rope_fields(rope, positions, False, varlen, batch, n, dev)
+    _call(_native.lib().bsfa_cache16_write, dev, stream, c, f, r)
+    return q_out

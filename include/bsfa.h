@@ -419,6 +419,108 @@ size_t bsfa_decode4_workspace_size(const bsfa_cache4* cache, const bsfa_decode4_
 bsfa_status bsfa_decode4(const bsfa_cache4* cache, const bsfa_decode4_params* p,
                          bsfa_stream_t stream);
 
+/*
+ * --------------------------------------------- rotary positions, 16-bit K/V cache
+ * bsfa_rotary, bsfa_cache16_write and bsfa_decode16 go around a prefill over
+ * pages (block_table in bsfa_fwd_params): queries and keys are rotated by their
+ * positions, keys and values enter the page pools that the prefill reads, and
+ * the tokens that follow attend to them.
+ */
+
+/* 16-bit page pools: what bsfa_fwd_params takes as k and v with a block table,
+ * in either order of tokens and heads. */
+typedef struct {
+  void* k;                    /* rows of the keys' pages */
+  void* v;                    /* ... and of the values' */
+  /* Strides in ELEMENTS as {page, head, token}: token t of page p of head h
+   * begins at base + p*stride[0] + h*stride[1] + t*stride[2].  Bases are 16-byte
+   * aligned and strides multiples of 8; page_size * stride[2] < 2^30.  With one
+   * page or one head its stride says nothing. */
+  int64_t k_stride[3], v_stride[3];
+  int num_pages;              /* pages in each pool (>= 1) */
+  int page_size;              /* tokens per page: a positive multiple of 16 (a prefill over
+                                 them wants a multiple of 128) */
+  int num_heads_kv;           /* Hkv, at most 4096 */
+  int head_dim;               /* 64 or 128 */
+  /* Position pos of sequence b is token pos % page_size of page
+   * block_table[b*block_table_stride + pos/page_size].  An entry outside
+   * [0, num_pages), or a position outside [0, block_table_width*page_size),
+   * names no row: a write there is dropped, and attention sees a zero key and a
+   * zero value (as the prefill does). */
+  const int32_t* block_table; /* device int32 [batch][block_table_stride]; may be null where
+                                 block_table_width is 0 */
+  int block_table_stride;     /* elements between two sequences' rows, >= width */
+  int block_table_width;      /* entries of each row that may be read;
+                                 block_table_width * page_size <= 2^30 */
+  int dtype;                  /* bsfa_dtype of the rows */
+} bsfa_cache16;
+
+enum { BSFA_ROPE_MAX_AXES = 4 };
+
+/* Rotary positions.  Pair j of a row, (x[j], x[j + pairs]) or where they are
+ * interleaved (x[2j], x[2j + 1]), is turned by the angle
+ *     position[axis[j]] * inv_freq[j]:
+ * (a, b) -> (a cos - b sin, b cos + a sin), in fp32, rounded once.  Elements
+ * from 2 * pairs on pass as they are.  The position is an integer and inv_freq
+ * taken as exact; the angle is reduced to a turn in integers, so it is as good at
+ * position 2^30 as at 1: within (1 + |inv_freq|) * |position| * 2^-64 + 2^-33
+ * turns. */
+typedef struct {
+  const float* inv_freq;      /* device fp32 [pairs] */
+  const int32_t* positions;   /* device int32, nullable: position of row i of sequence b on axis
+                                 x is positions[x*stride[0] + b*stride[1] + i], with packed rows
+                                 (cu_seqlens) positions[x*stride[0] + row].  NULL: start[b] + i
+                                 on every axis */
+  int64_t position_stride[2]; /* {axis, batch} in elements */
+  int pairs;                  /* a positive multiple of 8, 2 * pairs <= head_dim */
+  int interleaved;            /* nonzero: neighbours are pairs */
+  int inverse;                /* nonzero: turn back.  As a rotation's transpose is its inverse,
+                                 this is also the gradient: of the rotated rows in, of the rows
+                                 out */
+  int num_axes;               /* 1 .. BSFA_ROPE_MAX_AXES */
+  uint8_t axis[64];           /* axis of each pair, below num_axes */
+} bsfa_rope;
+
+/* Rows of a call.  Layouts as in bsfa_fwd_params: batched (cu_seqlens == NULL,
+ * `seqlen` rows of each of `batch` sequences) or varlen (`seqlen` packed rows,
+ * sequence b owns [cu_seqlens[b], cu_seqlens[b+1]); rows outside every sequence
+ * are neither read nor written; offsets need not be checked by the caller: a row
+ * belongs to the last sequence that begins at or before it, if that one reaches
+ * it).  Row i of sequence b has position start[b] + i.  Strides are {batch, head,
+ * token} in ELEMENTS, multiples of 8. */
+typedef struct {
+  const void* q;              /* [.., Hq, .., d], nullable */
+  const void* k;              /* [.., Hkv, .., d] */
+  const void* v;
+  void* q_out;                /* as q; may be q itself with the same strides, and must not overlap
+                                 it otherwise */
+  void* k_out;
+  int64_t q_stride[3], k_stride[3], v_stride[3], q_out_stride[3], k_out_stride[3];
+  int batch;                  /* 0 .. 4096 (0 is a no-op) */
+  int num_heads_q;            /* Hq, at most 4096 */
+  int num_heads_kv;           /* Hkv, at most 4096 */
+  int seqlen;                 /* rows per sequence (batched; batch * seqlen < 2^31) or in
+                                 total (varlen) */
+  int head_dim;               /* 64 or 128 */
+  const int32_t* cu_seqlens;  /* device int32 [batch+1], non-decreasing; nullable */
+  const int32_t* start;       /* device int32 [batch], nullable (0) */
+  int dtype;                  /* bsfa_dtype of all rows */
+} bsfa_rows16;
+
+/* q_out = q rotated, k_out = k rotated; either of q and k may be NULL (v is not
+ * looked at). */
+bsfa_status bsfa_rotary(const bsfa_rope* rope, const bsfa_rows16* rows, bsfa_stream_t stream);
+
+/* Writes k and v into their cache positions, in one launch.  With a rope the
+ * keys are rotated on the way, and q, where it is not NULL, into q_out
+ * (rope->inverse must be 0); rope == NULL writes the keys as they are, and q must
+ * be NULL.  num_heads_kv, head_dim and dtype must be the cache's.  Rows whose
+ * position names no cache row are dropped, and their queries rotated all the same.
+ * Positions of one call must differ: where two rows share one, it holds some
+ * mixture of the two. */
+bsfa_status bsfa_cache16_write(const bsfa_cache16* cache, const bsfa_rope* rope,
+                               const bsfa_rows16* rows, bsfa_stream_t stream);
+
 /* Synchronises `stream`, then reports (and clears) the device error word set
  * by a kernel whose bounded wait ran out.  *code receives the raw word (0 if
  * none).  Returns BSFA_ERR_DEVICE_TIMEOUT if it was set, BSFA_ERR_CUDA if the
