@@ -19,6 +19,8 @@ from .cache16 import (  # noqa: F401
     Rope,
     cache16_empty,
     cache16_write,
+    decode16,
+    decode16_workspace_bytes,
     rotary,
 )
 from .cache4 import (  # noqa: F401

@@ -141,6 +141,8 @@ SIGNATURES = [
     ("bsfa_decode4", c_int, [c_void_p, c_void_p, c_void_p]),
     ("bsfa_rotary", c_int, [c_void_p, c_void_p, c_void_p]),
     ("bsfa_cache16_write", c_int, [c_void_p, c_void_p, c_void_p, c_void_p]),
+    ("bsfa_decode16_workspace_size", c_size_t, [c_void_p, c_void_p]),
+    ("bsfa_decode16", c_int, [c_void_p, c_void_p, c_void_p]),
     ("bsfa_selftest_wait_guard", c_int, [ctypes.c_uint, c_void_p]),
 ]
 

@@ -3,7 +3,8 @@ the C ABI (argument marshalling only).
 
 The calls around a prefill over pages: ``cache16_write`` rotates queries and keys
 by their positions and puts keys and values into the page pools that ``prefill``
-reads through a block table; ``rotary`` rotates without a cache.
+reads through a block table, ``decode16`` attends to them with the tokens that
+follow, and ``rotary`` rotates without a cache.
 """
 from __future__ import annotations
 
@@ -12,7 +13,7 @@ from typing import NamedTuple, Optional, Sequence
 import torch
 
 from . import _native
-from .api import _DTYPES, _on_device
+from .api import _DTYPES, _dtype_code, _nbytes, _on_device, _strides_bhtd
 from .cache4 import _BAD_TABLE, _I32, _call, _empty, _int32_vector, _strides
 
 MAX_AXES = 4
@@ -248,3 +249,84 @@ def cache16_write(cache: KVCache16, k, v, block_table, *, rope: Optional[Rope] =
     f = None if rope is None else _rope_fields(rope, positions, False, varlen, batch, n, dev)
     _call(_native.lib().bsfa_cache16_write, dev, stream, c, f, r)
     return q_out
+
+
+def _decode_fields(q, cache, block_table, seqlens, out, device, *, layout, max_seqlen,
+                   softmax_scale, causal, lse=0):
+    """The packed bsfa_cache16 of a decode call, and a function of a workspace's
+    address and size that gives its packed bsfa_decode4_params."""
+    if layout is None:
+        layout = "bhld"
+    shape = q.shape
+    if out.shape != shape or q.dtype is not out.dtype:
+        raise ValueError("q and out must have one shape and type")
+    code = _dtype_code(q)
+    a, b = q.stride(), out.stride()
+    qs, hq, n = _strides(q, shape, a, layout, False)
+    os_ = qs if a == b else _strides(out, shape, b, layout, False)[0]
+    batch = 1 if len(shape) == 3 else shape[0]
+    c, heads, d, kind, most = _cache_fields(cache, block_table, device, batch)
+    if shape[-1] != d or heads == 0 or hq % heads or kind != code:
+        raise ValueError("q must have the cache's head dimension and type and a multiple of its "
+                         "heads")
+    if max_seqlen is None:
+        max_seqlen = most
+    elif max_seqlen > most:
+        raise ValueError("block_table has too few pages per row for max_seqlen")
+    fixed = (q.data_ptr(), out.data_ptr(), *qs, *os_, batch, hq, n,
+             _int32_vector(seqlens, batch, "seqlens"), int(max_seqlen),
+             float(softmax_scale) if softmax_scale else 0.0, 1 if causal else 0, lse)
+    return c, lambda ws, size: _native.DECODE4.pack(*fixed, ws, size, code)
+
+
+def decode16(q, cache: KVCache16, block_table, seqlens, *, max_seqlen=None, softmax_scale=None,
+             causal=True, layout=None, out=None, return_lse=False, workspace=None, stream=None):
+    """Attention of new tokens over the 16-bit cache: q [B, Hq, n, d] (layout
+    "bhld") or [B, n, Hq, d] ("blhd"), or [Hq, n, d] for one sequence, n = 1 for a
+    decode step, of the cache's type.  The new tokens' own keys and values are in
+    the cache already; ``seqlens`` (int32 [B] on the device) counts them.  Query i
+    of sequence b attends to positions t <= seqlens[b] - n + i, or with
+    ``causal=False`` to every t < seqlens[b].  Returns a dict with "out" and, on
+    request, "lse" (float32 [Hq, B * n], natural log).  A query that sees nothing
+    gives zeros and -inf.
+
+    ``max_seqlen`` bounds the lengths (default: what the block table can hold;
+    longer entries of seqlens are cut to it); the call reads lengths on the device
+    only, so a captured graph stays right as they grow within it.  ``workspace``: at
+    least ``decode16_workspace_bytes`` of device memory (0 where the lengths' bound
+    and the batch are small), not shared by calls that may overlap (default:
+    allocated for the call)."""
+    dev = q.device
+    if dev.type != "cuda" or not seqlens.get_device() == dev.index or \
+            out is not None and out.device != dev or \
+            workspace is not None and workspace.device != dev:
+        _on_device(dev, out=out, seqlens=seqlens, workspace=workspace)
+    if out is None:
+        out = torch.empty_like(q) if stream is None else _empty(stream, dev, q.shape, q.dtype)
+    res = {"out": out}
+    lse = 0
+    if return_lse:
+        _, hq, n = _strides_bhtd(q, layout or "bhld", False)
+        rows = n if q.dim() == 3 else q.shape[0] * n
+        res["lse"] = _empty(stream, dev, (hq, rows), torch.float32)
+        lse = res["lse"].data_ptr()
+    c, fields = _decode_fields(q, cache, block_table, seqlens, out, dev, layout=layout,
+                               max_seqlen=max_seqlen, softmax_scale=softmax_scale, causal=causal,
+                               lse=lse)
+    if workspace is None:
+        need = _native.lib().bsfa_decode16_workspace_size(c, fields(0, 0))
+        if need:
+            workspace = _empty(stream, dev, (need,), torch.uint8)
+    elif not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    _call(_native.lib().bsfa_decode16, dev, stream, c,
+          fields(0, 0) if workspace is None else fields(workspace.data_ptr(), _nbytes(workspace)))
+    return res
+
+
+def decode16_workspace_bytes(q, cache: KVCache16, block_table, seqlens, *, max_seqlen=None,
+                             layout=None) -> int:
+    """Workspace bytes that decode16 needs for this call's shapes."""
+    c, fields = _decode_fields(q, cache, block_table, seqlens, q, q.device, layout=layout,
+                               max_seqlen=max_seqlen, softmax_scale=None, causal=True)
+    return int(_native.lib().bsfa_decode16_workspace_size(c, fields(0, 0)))

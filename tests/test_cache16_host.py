@@ -109,6 +109,14 @@ def _rotary(lib, rope, r):
                            None if r is None else ctypes.byref(r), None)
 
 
+def _decode(**kw):
+    p = _native().Decode4Params()
+    p.q = p.o = p.seqlens = 1 << 20
+    p.q_stride[:] = p.o_stride[:] = (8 * 128, 128, 128)
+    p.batch, p.num_heads_q, p.q_len, p.max_seqlen = 3, 8, 1, 256
+    return _set(p, kw)
+
+
 @pytest.mark.parametrize("change,status", [
     (dict(head_dim=96), UNSUPPORTED), (dict(page_size=24), UNSUPPORTED),
     (dict(page_size=0), INVALID), (dict(num_pages=0), INVALID), (dict(num_heads_kv=0), INVALID),
@@ -121,6 +129,8 @@ def test_cache_descriptors_that_are_refused(lib, change, status):
     r = _rows(head_dim=change.get("head_dim", 128))
     want = UNSUPPORTED if "head_dim" in change else status
     assert _write(lib, _cache(**change), _rope(pairs=32), r) == want
+    c, p = _cache(**change), _decode()
+    assert lib.bsfa_decode16(ctypes.byref(c), ctypes.byref(p), None) == status
 
 
 def test_cache_strides_that_are_refused(lib):
@@ -129,6 +139,63 @@ def test_cache_strides_that_are_refused(lib):
         c = _cache()
         getattr(c, field)[i] = bad
         assert _write(lib, c, _rope(), _rows()) == UNSUPPORTED
+        p = _decode()
+        assert lib.bsfa_decode16(ctypes.byref(c), ctypes.byref(p), None) == UNSUPPORTED
+
+
+def test_decode_parameters_that_are_refused(lib):
+    c = ctypes.byref(_cache())
+    size = lib.bsfa_decode16_workspace_size
+    for change, status in ((dict(num_heads_q=7), INVALID), (dict(num_heads_q=0), INVALID),
+                           (dict(batch=-1), INVALID), (dict(q_len=-1), INVALID),
+                           (dict(max_seqlen=-1), INVALID), (dict(max_seqlen=257), INVALID),
+                           (dict(dtype=3), UNSUPPORTED), (dict(dtype=1), INVALID),
+                           (dict(batch=4097), UNSUPPORTED), (dict(q_len=1 << 27), UNSUPPORTED),
+                           (dict(batch=4096, q_len=1 << 22), UNSUPPORTED)):
+        p = _decode(**change)
+        assert lib.bsfa_decode16(c, ctypes.byref(p), None) == status, change
+        assert size(c, ctypes.byref(p)) == 0, change
+    long = _cache(block_table_width=2000, block_table_stride=2000)
+    c2 = ctypes.byref(long)  # a bound this long needs a workspace
+    need = size(c2, ctypes.byref(_decode(max_seqlen=100000)))
+    assert need > 0 and size(c2, ctypes.byref(_decode(max_seqlen=256))) == 0
+    for change, status in ((dict(q=0), INVALID), (dict(seqlens=0), INVALID),
+                           (dict(o=(1 << 20) + 8), UNSUPPORTED), (dict(), WORKSPACE),
+                           (dict(workspace=128, workspace_bytes=1 << 30), WORKSPACE),
+                           (dict(workspace=1 << 20, workspace_bytes=0), WORKSPACE),
+                           (dict(workspace=1 << 20, workspace_bytes=need - 1), WORKSPACE)):
+        p = _decode(max_seqlen=100000, **change)
+        assert lib.bsfa_decode16(c2, ctypes.byref(p), None) == status, change
+    p = _decode(max_seqlen=100000)
+    p.q_stride[1] = 4
+    assert lib.bsfa_decode16(c2, ctypes.byref(p), None) == UNSUPPORTED
+    p = _decode(max_seqlen=100000)
+    p.q_stride[2] = 3  # the only token's stride says nothing
+    assert lib.bsfa_decode16(c2, ctypes.byref(p), None) == WORKSPACE
+    for empty in (dict(batch=0), dict(q_len=0)):
+        p = _decode(q=0, o=0, **empty)
+        assert lib.bsfa_decode16(c, ctypes.byref(p), None) == OK
+    assert lib.bsfa_decode16(None, ctypes.byref(p), None) == INVALID
+    assert lib.bsfa_decode16(c, None, None) == INVALID
+
+
+def test_strides_of_one_element_dimensions_say_nothing(lib):
+    """A pool of one page and one head is not refused for strides that no call multiplies by
+    anything but 0; of two, it is."""
+    for pages, heads, status in ((1, 1, WORKSPACE), (2, 1, UNSUPPORTED), (1, 2, UNSUPPORTED)):
+        c = _cache(num_pages=pages, num_heads_kv=heads, block_table_width=2000,
+                   block_table_stride=2000)
+        for s in (c.k_stride, c.v_stride):
+            if pages == 1:
+                s[0] = 1
+            if heads == 1:
+                s[1] = 0
+        if pages == 2:
+            c.k_stride[0] = 4
+        if heads == 2:
+            c.v_stride[1] = 0
+        p = _decode(max_seqlen=100000)  # long enough to need the workspace it lacks
+        assert lib.bsfa_decode16(ctypes.byref(c), ctypes.byref(p), None) == status
 
 
 def test_ropes_that_are_refused(lib):
@@ -178,10 +245,11 @@ def test_rows_that_are_refused(lib):
         assert _write(lib, _cache(), None, r) == OK
 
 
-def test_kernels_do_not_spill(lib):
+@pytest.mark.parametrize("source", ["bsfa_cache16", "bsfa_decode16"])
+def test_kernels_do_not_spill(lib, source):
     """The compiler warns of registers that it spills to local memory."""
     from block_sparse_gated_gb300 import build
-    log = os.path.join(build.OBJDIR, "bsfa_cache16.o.log")
+    log = os.path.join(build.OBJDIR, source + ".o.log")
     if not os.path.exists(log):
         pytest.skip("the library was built without a log")
     with open(log) as f:
@@ -198,6 +266,8 @@ def test_binding_refuses_host_tensors():
         b.cache16_write(cache, x, x, table)
     with pytest.raises(ValueError, match="CUDA"):
         b.rotary(rope, x, x)
+    with pytest.raises(ValueError, match="CUDA"):
+        b.decode16(x, cache, table, torch.zeros(1, dtype=torch.int32))
 
 
 class Cuda:  # stands for the host tensors' device
@@ -299,6 +369,24 @@ def test_binding_checks_what_the_library_cannot_see(monkeypatch):
                   (b.Rope(f), dict(positions=torch.zeros(5, 3, 10, dtype=torch.int32)))):
         with pytest.raises(ValueError):
             rope(r, **kw)
+    q1, lens = torch.zeros(3, 8, 1, 128, dtype=BF), torch.zeros(3, dtype=torch.int32)
+
+    def decode(*a, **kw):
+        kw = dict(dict(layout=None, max_seqlen=None, softmax_scale=None, causal=True), **kw)
+        return n.Decode4Params.from_buffer_copy(m._decode_fields(*a, dev, **kw)[1](4096, 77))
+
+    d = decode(q1, cache, table, lens, q1, lse=512, softmax_scale=0.5)
+    assert (d.batch, d.num_heads_q, d.q_len, d.max_seqlen, d.dtype, d.causal) == (3, 8, 1, 64, 0, 1)
+    assert (d.q, d.o, d.seqlens, d.lse) == (q1.data_ptr(), q1.data_ptr(), lens.data_ptr(), 512)
+    assert (d.workspace, d.workspace_bytes, d.softmax_scale) == (4096, 77, 0.5)
+    for bad, what in (((q1[:, :7], cache, table, lens, q1[:, :7]), "heads"),
+                      ((q1, cache, table, lens, q1.half()), "shape and type"),
+                      ((q1.half(), cache, table, lens, q1.half()), "type"),
+                      ((q1, cache, table, lens.long(), q1), "seqlens")):
+        with pytest.raises(ValueError, match=what):
+            decode(*bad)
+    with pytest.raises(ValueError, match="pages"):
+        decode(q1, cache, table, lens, q1, max_seqlen=65)
     with pytest.raises(ValueError, match="rope"):
         b.cache16_write(cache, k, k, table, q=q)
     with pytest.raises(ValueError, match="rope"):
