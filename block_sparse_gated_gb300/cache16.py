@@ -13,10 +13,11 @@ from typing import NamedTuple, Optional, Sequence
 import torch
 
 from . import _native
-from .api import _DTYPES, _dtype_code, _nbytes, _on_device, _strides_bhtd
+from .api import _DTYPES, _nbytes, _on_device
 from .cache4 import _BAD_TABLE, _I32, _call, _empty, _int32_vector, _strides
 
 MAX_AXES = 4
+_F32 = torch.float32
 
 
 class KVCache16(NamedTuple):
@@ -96,13 +97,30 @@ def _cache_fields(cache: KVCache16, block_table: torch.Tensor, device, batch: in
         width * page
 
 
+def _positions_fields(positions, num_axes: int, varlen: bool, batch: int, n: int, device):
+    """Address and {axis, batch} strides of a call's positions."""
+    want = (n,) if varlen else (batch, n)
+    shape = tuple(positions.shape)
+    if shape == want and num_axes == 1:
+        strides = (0, *positions.stride())
+    elif shape[1:] == want and num_axes <= shape[0] <= MAX_AXES:
+        strides = positions.stride()
+    else:
+        raise ValueError(f"positions must be an int32 [axes, {', '.join(map(str, want))}] tensor")
+    if positions.dtype is not _I32 or (strides[-1] != 1 and n > 1):
+        raise ValueError("positions must be int32 with the positions of a sequence contiguous")
+    if positions.get_device() != device.index:
+        _on_device(device, positions=positions)
+    return positions.data_ptr(), strides[0], 0 if varlen else strides[1]
+
+
 def _rope_fields(rope: Rope, positions, inverse: bool, varlen: bool, batch: int, n: int, device):
     """The packed bsfa_rope of a call on n rows of each of ``batch`` sequences, or
     on n packed rows."""
     f, axes, interleaved = rope
-    if f.dtype is not torch.float32 or f.dim() != 1 or not f.is_contiguous():
+    if f.dtype is not _F32 or f.dim() != 1 or not f.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float32 [pairs] tensor")
-    pairs = f.shape[0]
+    pairs = f.numel()
     if not 0 < pairs <= 64:
         raise ValueError("inv_freq must have 1 to 64 pairs")
     if f.get_device() != device.index:
@@ -113,27 +131,27 @@ def _rope_fields(rope: Rope, positions, inverse: bool, varlen: bool, batch: int,
         if len(axes) != pairs or min(axes) < 0 or max(axes) >= MAX_AXES:
             raise ValueError(f"axes must name one of at most {MAX_AXES} axes for each pair")
         code, num_axes = bytes(axes), max(axes) + 1
-    at = axis_stride = batch_stride = 0
-    if positions is not None:
-        want = (n,) if varlen else (batch, n)
-        shape = tuple(positions.shape)
-        if shape == want and num_axes == 1:
-            strides = (0, *positions.stride())
-        elif shape[1:] == want and num_axes <= shape[0] <= MAX_AXES:
-            strides = positions.stride()
-        else:
-            raise ValueError(f"positions must be an int32 [axes, {', '.join(map(str, want))}] tensor")
-        if positions.dtype is not _I32 or (strides[-1] != 1 and n > 1):
-            raise ValueError("positions must be int32 with the positions of a sequence contiguous")
-        if positions.get_device() != device.index:
-            _on_device(device, positions=positions)
-        at, axis_stride = positions.data_ptr(), strides[0]
-        batch_stride = 0 if varlen else strides[1]
-    return _native.ROPE.pack(f.data_ptr(), at, axis_stride, batch_stride, pairs,
-                             1 if interleaved else 0, 1 if inverse else 0, num_axes, code)
+    at = (0, 0, 0) if positions is None else \
+        _positions_fields(positions, num_axes, varlen, batch, n, device)
+    return _native.ROPE.pack(f.data_ptr(), *at, pairs, 1 if interleaved else 0,
+                             1 if inverse else 0, num_axes, code)
 
 
 _NONE = (0, 0, 0)
+
+
+def _like(t, given, layout, varlen: bool, device):
+    """Strides of a tensor that must have the shape and type of ``given``, whose
+    shape, strides, type and strides {batch, head, token} these are."""
+    shape, strides, dtype, s = given
+    if t.dtype is not dtype:
+        raise TypeError("all rows must share one element type")
+    if t.shape != shape:
+        raise ValueError("tensors of one kind must have one shape")
+    if t.get_device() != device.index:
+        _on_device(device, rows=t)
+    a = t.stride()
+    return s if a == strides else _strides(t, shape, a, layout, varlen)[0]
 
 
 def _rows_fields(q, k, v, q_out, k_out, layout, cu_seqlens, start, device):
@@ -148,25 +166,35 @@ def _rows_fields(q, k, v, q_out, k_out, layout, cu_seqlens, start, device):
     code = _DTYPES.get(dtype)
     if code is None:
         raise TypeError("expected a bfloat16 or float16 tensor")
-    heads, rows, d = [0, 0], None, shape[-1]
-    given = []
-    for which, t, like in ((0, q, None), (1, k, None), (1, v, k), (0, q_out, q), (1, k_out, k)):
-        if t is None:
-            given.append((0, _NONE))
-            continue
-        size = t.shape
-        if t.dtype is not dtype:
-            raise TypeError("all rows must share one element type")
-        if device.type != "cuda" or t.get_device() != index:
-            _on_device(device, rows=t)
-        s, h, n = _strides(t, size, t.stride(), layout, varlen)
-        if like is not None and size != like.shape:
-            raise ValueError("tensors of one kind must have one shape")
-        if size[-1] != d or len(size) != len(shape) or rows not in (None, n) or \
-                len(size) == 4 and size[0] != shape[0]:
-            raise ValueError("Q, K and V shapes disagree")
-        rows, heads[which] = n, h
-        given.append((t.data_ptr(), s))
+    if device.type != "cuda" or one.get_device() != index:
+        _on_device(device, rows=one)
+    a = one.stride()
+    s, h, n = _strides(one, shape, a, layout, varlen)
+    d = shape[-1]
+    given = (shape, a, dtype, s)
+    qp = kp = vp = qo = ko = hq = hkv = 0
+    qs = ks = vs = qos = kos = _NONE
+    if k is not None:
+        kp, ks, hkv = k.data_ptr(), s, h
+        if v is not None:
+            vp, vs = v.data_ptr(), _like(v, given, layout, varlen, device)
+        if k_out is not None:
+            ko, kos = k_out.data_ptr(), _like(k_out, given, layout, varlen, device)
+        if q is not None:
+            size = q.shape
+            if q.dtype is not dtype:
+                raise TypeError("all rows must share one element type")
+            if q.get_device() != index:
+                _on_device(device, rows=q)
+            a = q.stride()
+            s, h, m = _strides(q, size, a, layout, varlen)
+            if m != n or size[-1] != d or len(size) != len(shape) or \
+                    len(size) == 4 and size[0] != shape[0]:
+                raise ValueError("Q, K and V shapes disagree")
+            given = (size, a, dtype, s)
+    if q is not None:
+        qp, qs, hq = q.data_ptr(), s, h
+        qo, qos = q_out.data_ptr(), _like(q_out, given, layout, varlen, device)
     cu = first = 0
     if varlen:
         if cu_seqlens.dtype is not _I32 or cu_seqlens.dim() != 1 or \
@@ -181,10 +209,8 @@ def _rows_fields(q, k, v, q_out, k_out, layout, cu_seqlens, start, device):
         first = _int32_vector(start, batch, "start")
         if start.get_device() != index:
             _on_device(device, start=start)
-    (qp, qs), (kp, ks), (vp, vs), (qo, qos), (ko, kos) = given
-    return _native.ROWS16.pack(qp, kp, vp, qo, ko, *qs, *ks, *vs, *qos, *kos, batch, heads[0],
-                               heads[1], rows, d, cu, first, code), \
-        batch, rows, heads[1], d, code, varlen
+    return _native.ROWS16.pack(qp, kp, vp, qo, ko, *qs, *ks, *vs, *qos, *kos, batch, hq, hkv, n, d,
+                               cu, first, code), batch, n, hkv, d, code, varlen
 
 
 def rotary(rope: Rope, q, k=None, *, positions=None, start=None, cu_seqlens=None, layout=None,
@@ -253,14 +279,16 @@ def cache16_write(cache: KVCache16, k, v, block_table, *, rope: Optional[Rope] =
 
 def _decode_fields(q, cache, block_table, seqlens, out, device, *, layout, max_seqlen,
                    softmax_scale, causal, lse=0):
-    """The packed bsfa_cache16 of a decode call, and a function of a workspace's
-    address and size that gives its packed bsfa_decode4_params."""
+    """The packed bsfa_cache16 of a decode call, and the fields of its
+    bsfa_decode4_params up to the workspace's address and size, and behind them."""
     if layout is None:
         layout = "bhld"
     shape = q.shape
-    if out.shape != shape or q.dtype is not out.dtype:
+    code = _DTYPES.get(q.dtype)
+    if code is None:
+        raise TypeError("expected a bfloat16 or float16 tensor")
+    if out.shape != shape or out.dtype is not q.dtype:
         raise ValueError("q and out must have one shape and type")
-    code = _dtype_code(q)
     a, b = q.stride(), out.stride()
     qs, hq, n = _strides(q, shape, a, layout, False)
     os_ = qs if a == b else _strides(out, shape, b, layout, False)[0]
@@ -273,10 +301,9 @@ def _decode_fields(q, cache, block_table, seqlens, out, device, *, layout, max_s
         max_seqlen = most
     elif max_seqlen > most:
         raise ValueError("block_table has too few pages per row for max_seqlen")
-    fixed = (q.data_ptr(), out.data_ptr(), *qs, *os_, batch, hq, n,
-             _int32_vector(seqlens, batch, "seqlens"), int(max_seqlen),
-             float(softmax_scale) if softmax_scale else 0.0, 1 if causal else 0, lse)
-    return c, lambda ws, size: _native.DECODE4.pack(*fixed, ws, size, code)
+    return c, (q.data_ptr(), out.data_ptr(), *qs, *os_, batch, hq, n,
+               _int32_vector(seqlens, batch, "seqlens"), int(max_seqlen),
+               float(softmax_scale) if softmax_scale else 0.0, 1 if causal else 0, lse), code
 
 
 def decode16(q, cache: KVCache16, block_table, seqlens, *, max_seqlen=None, softmax_scale=None,
@@ -306,27 +333,33 @@ def decode16(q, cache: KVCache16, block_table, seqlens, *, max_seqlen=None, soft
     res = {"out": out}
     lse = 0
     if return_lse:
-        _, hq, n = _strides_bhtd(q, layout or "bhld", False)
-        rows = n if q.dim() == 3 else q.shape[0] * n
-        res["lse"] = _empty(stream, dev, (hq, rows), torch.float32)
+        *b, h, n, _ = q.shape
+        if layout == "blhd" and b:
+            h, n = n, h
+        res["lse"] = _empty(stream, dev, (h, b[0] * n if b else n), _F32)
         lse = res["lse"].data_ptr()
-    c, fields = _decode_fields(q, cache, block_table, seqlens, out, dev, layout=layout,
+    c, fields, code = _decode_fields(q, cache, block_table, seqlens, out, dev, layout=layout,
                                max_seqlen=max_seqlen, softmax_scale=softmax_scale, causal=causal,
                                lse=lse)
+    at = size = 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous")
+        at, size = workspace.data_ptr(), _nbytes(workspace)
+    p = _native.DECODE4.pack(*fields, at, size, code)
     if workspace is None:
-        need = _native.lib().bsfa_decode16_workspace_size(c, fields(0, 0))
-        if need:
-            workspace = _empty(stream, dev, (need,), torch.uint8)
-    elif not workspace.is_contiguous():
-        raise ValueError("the workspace must be contiguous")
-    _call(_native.lib().bsfa_decode16, dev, stream, c,
-          fields(0, 0) if workspace is None else fields(workspace.data_ptr(), _nbytes(workspace)))
+        size = _native.lib().bsfa_decode16_workspace_size(c, p)
+        if size:
+            workspace = _empty(stream, dev, (size,), torch.uint8)
+            p = _native.DECODE4.pack(*fields, workspace.data_ptr(), size, code)
+    _call(_native.lib().bsfa_decode16, dev, stream, c, p)
     return res
 
 
 def decode16_workspace_bytes(q, cache: KVCache16, block_table, seqlens, *, max_seqlen=None,
                              layout=None) -> int:
     """Workspace bytes that decode16 needs for this call's shapes."""
-    c, fields = _decode_fields(q, cache, block_table, seqlens, q, q.device, layout=layout,
-                               max_seqlen=max_seqlen, softmax_scale=None, causal=True)
-    return int(_native.lib().bsfa_decode16_workspace_size(c, fields(0, 0)))
+    c, fields, code = _decode_fields(q, cache, block_table, seqlens, q, q.device, layout=layout,
+                                     max_seqlen=max_seqlen, softmax_scale=None, causal=True)
+    return int(_native.lib().bsfa_decode16_workspace_size(
+        c, _native.DECODE4.pack(*fields, 0, 0, code)))

@@ -25,8 +25,8 @@ namespace {
 
 constexpr int THREADS = 128;
 constexpr int CHUNK = 16;  // elements of a row that a thread owns: eight pairs
-constexpr int AHEAD = 4;   // heads whose loads a thread issues at once
-constexpr int FILL = 2048; // blocks that a call with few rows is spread over
+constexpr int AHEAD = 3;   // heads whose loads a thread issues at once
+constexpr int FILL = 600;  // blocks that a call with few rows is spread over
 
 enum Kind { QUERIES, KEYS, VALUES };
 
@@ -63,30 +63,20 @@ struct Row {
   long long pos;  // its position (offsets below zero put rows beyond 2^31)
 };
 
-__device__ __forceinline__ Row find_row(const RowsArgs& a, int t) {
-  Row r;
-  if (a.cu == nullptr) {
-    r.b = t / a.seqlen;
-    r.i = t - r.b * a.seqlen;
-    r.pos = r.i;
-  } else {
-    // The last sequence that begins at or before row t.
-    int lo = 0, hi = a.batch;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(a.cu + mid) <= t)
-        lo = mid + 1;
-      else
-        hi = mid;
-    }
-    r.b = lo - 1;
-    r.i = t;
-    if (r.b >= 0 && t >= __ldg(a.cu + r.b + 1)) r.b = -1;
-    if (r.b < 0) return r;
-    r.pos = static_cast<long long>(t) - __ldg(a.cu + r.b);
+// The sequence and position of packed row r.i.
+__device__ __forceinline__ void find_sequence(const RowsArgs& a, Row& r) {
+  // The last sequence that begins at or before it.
+  int lo = 0, hi = a.batch;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.cu + mid) <= r.i)
+      lo = mid + 1;
+    else
+      hi = mid;
   }
-  if (a.start) r.pos += __ldg(a.start + r.b);
-  return r;
+  r.b = lo - 1;
+  if (r.b >= 0 && r.i >= __ldg(a.cu + r.b + 1)) r.b = -1;
+  if (r.b >= 0) r.pos = static_cast<long long>(r.i) - __ldg(a.cu + r.b);
 }
 
 // The page of a row and its token there; false where the position names no row.
@@ -99,18 +89,20 @@ __device__ __forceinline__ bool find_page(const RowsArgs& a, const Row& r, int& 
 }
 
 // |f| / 2pi in units of 2^-64 turn, modulo one turn: f is m * 2^(e - 150) with a
-// 24-bit m, and m * floor(2^66 / 2pi) is shifted by e - 152.
+// 24-bit m, and the 88 bits of m * floor(2^66 / 2pi) are shifted by e - 152.
 __device__ __forceinline__ uint64_t turns_per_position(float f) {
   constexpr uint64_t INV_2PI = 0xA2F9836E4E441529ull;  // floor(2^66 / (2 pi))
   const uint32_t bits = __float_as_uint(f);
   const int e = max(1, static_cast<int>(bits >> 23 & 0xffu));
-  const uint64_t m = (bits & 0x7fffffu) | (bits & 0x7f800000u ? 0x800000u : 0u);
-  const uint64_t hi = __umul64hi(m, INV_2PI), lo = m * INV_2PI;
+  const uint32_t m = (bits & 0x7fffffu) | (bits & 0x7f800000u ? 0x800000u : 0u);
+  const uint64_t low = static_cast<uint64_t>(m) * static_cast<uint32_t>(INV_2PI);
+  const uint64_t high = static_cast<uint64_t>(m) * static_cast<uint32_t>(INV_2PI >> 32) +
+                        (low >> 32);  // the upper 56 bits
   const int down = 152 - e;
-  if (down < 0) return down > -64 ? lo << -down : 0;
-  if (down == 0) return lo;
-  if (down < 64) return lo >> down | hi << (64 - down);
-  return down < 128 ? hi >> (down - 64) : 0;
+  if (down >= 32) return down < 96 ? high >> (down - 32) : 0;
+  const uint64_t lowest = low & 0xffffffffu;
+  if (down >= 0) return high << (32 - down) | lowest >> down;
+  return down > -32 ? (high << 32 | lowest) << -down : 0;
 }
 
 // cos and sin of position * f.
@@ -119,10 +111,20 @@ __device__ __forceinline__ void turn(float f, long long position, float& c, floa
   if (f < 0.f) phase = 0 - phase;
   const uint32_t p = static_cast<uint32_t>((phase + (1ull << 31)) >> 32);
   const uint32_t quarter = (p + (1u << 29)) >> 30;
-  // In half turns, at most a quarter of one: exact to 2^-24 of itself.
-  const float x = static_cast<float>(static_cast<int32_t>(p - (quarter << 30))) * 0x1p-31f;
-  float c0, s0;
-  sincospif(x, &s0, &c0);
+  // The angle beyond the nearest quarter turn, at most pi / 4 and three roundings off
+  // (an integer's, the constant's, the product's), and the Taylor series there: sin to
+  // x^9 / 9!, cos to x^10 / 10!, which leave 2^-29 and 2^-33.
+  const float x = static_cast<float>(static_cast<int32_t>(p - (quarter << 30))) * 0x1.921fb6p-30f;
+  const float y = x * x;
+  float s0 = fmaf(y, 1.f / 362880.f, -1.f / 5040.f);
+  s0 = fmaf(y, s0, 1.f / 120.f);
+  s0 = fmaf(y, s0, -1.f / 6.f);
+  s0 = fmaf(x * y, s0, x);
+  float c0 = fmaf(y, -1.f / 3628800.f, 1.f / 40320.f);
+  c0 = fmaf(y, c0, -1.f / 720.f);
+  c0 = fmaf(y, c0, 1.f / 24.f);
+  c0 = fmaf(y, c0, -0.5f);
+  c0 = fmaf(y, c0, 1.f);
   const bool odd = quarter & 1u;
   c = odd ? s0 : c0;
   s = odd ? c0 : s0;
@@ -141,8 +143,6 @@ __global__ void __launch_bounds__(THREADS) rows16_kernel(const __grid_constant__
   int y = blockIdx.y, kind = QUERIES;
   while (y >= a.part[kind].blocks) y -= a.part[kind++].blocks;
   const Part& part = a.part[kind];
-  const Row r = find_row(a, static_cast<int>(t));
-  if (r.b < 0) return;
   const int h0 = y * a.heads_per_block, h1 = min(h0 + a.heads_per_block, part.heads);
 
   // This thread's two pieces of eight elements: of the rotated part, of what
@@ -157,9 +157,35 @@ __global__ void __launch_bounds__(THREADS) rows16_kernel(const __grid_constant__
     const int x = 8 * (g - a.pairs / 8), passing = D / 2 - a.pairs;
     lo = 2 * a.pairs + x, hi = lo + passing;
   }
-  const long long batch = a.cu == nullptr ? r.b : 0;
+  const int gap = hi - lo;
+  Row r;
+  r.i = static_cast<int>(t), r.b = 0;
+  if (a.cu == nullptr) {
+    r.b = r.i / a.seqlen;
+    r.i -= r.b * a.seqlen;
+    r.pos = r.i;
+  }
+  const long long batch = r.b;
   const uint16_t* in =
       part.in + batch * part.in_s[0] + h0 * part.in_s[1] + r.i * part.in_s[2] + lo;
+  uint4 x[AHEAD], z[AHEAD];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int n = 0; n < AHEAD; ++n)
+      if (h + n < h1) {
+        const uint16_t* src = in + n * part.in_s[1];
+        x[n] = *reinterpret_cast<const uint4*>(src);
+        z[n] = *reinterpret_cast<const uint4*>(src + gap);
+      }
+    in += AHEAD * part.in_s[1];
+  };
+  // In flight while the sequence, the page and the angles are found (of a packed row
+  // outside every sequence for nothing).
+  load(h0);
+
+  if (a.cu != nullptr) find_sequence(a, r);
+  if (r.b < 0) return;
+  if (a.start) r.pos += __ldg(a.start + r.b);
   long long at;
   if (kind != QUERIES && a.paged) {
     int page, token;
@@ -169,7 +195,6 @@ __global__ void __launch_bounds__(THREADS) rows16_kernel(const __grid_constant__
     at = batch * part.out_s[0] + r.i * part.out_s[2];
   }
   uint16_t* out = part.out + at + h0 * part.out_s[1] + lo;
-  const int gap = hi - lo;
 
   // Eight pairs: elements e of both pieces, or the neighbours of the first piece
   // and then of the second.
@@ -186,16 +211,7 @@ __global__ void __launch_bounds__(THREADS) rows16_kernel(const __grid_constant__
     }
   }
 
-  for (int h = h0; h < h1; h += AHEAD) {
-    uint4 x[AHEAD], z[AHEAD];
-#pragma unroll
-    for (int n = 0; n < AHEAD; ++n)
-      if (h + n < h1) {
-        const uint16_t* src = in + n * part.in_s[1];
-        x[n] = *reinterpret_cast<const uint4*>(src);
-        z[n] = *reinterpret_cast<const uint4*>(src + gap);
-      }
-    in += AHEAD * part.in_s[1];
+  for (int h = h0;;) {
 #pragma unroll
     for (int n = 0; n < AHEAD; ++n) {
       if (h + n >= h1) return;
@@ -223,6 +239,9 @@ __global__ void __launch_bounds__(THREADS) rows16_kernel(const __grid_constant__
       *reinterpret_cast<uint4*>(out + gap) = z[n];
       out += part.out_s[1];
     }
+    h += AHEAD;
+    if (h >= h1) return;
+    load(h);
   }
 }
 

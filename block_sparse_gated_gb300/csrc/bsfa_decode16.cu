@@ -1,840 +1,30 @@
-// bsfa_decode16.cu -- bsfa_decode16: attention of a few new tokens per sequence
-// over the 16-bit paged cache.
-//
-// Mathematics.  S^T = K Q^T and O^T = V^T P^T are tensor-core products of 16-bit
-// factors with fp32 sums.  The softmax is streamed: a weight is p = 2^(y + z) with y
-// the score in log2 units and z the row's offset, which falls, with O and the sum l
-// rescaled, only when some weight would pass 2^(SHIFT + HEADROOM); the factor
-// 2^SHIFT that p carries cancels in O / l and keeps small weights out of fp16's
-// subnormals.
-//
-// Layout.  Cached tokens are the rows (M) of the products and query rows
-// (Hq/Hkv heads times q_len tokens) the columns (N = 8 per tile), so that a decode
-// step of up to 8 query heads per KV head wastes no tensor work.  Each warp streams
-// its own 16-token tiles through a private ring of asynchronous copies; no barrier
-// is met inside a segment.
-//
-// Work split.  A segment is one (sequence, KV head, row tile).  Where it is short by
-// the caller's bound, a CTA takes it, or a cluster of up to eight, which joins its
-// sums through distributed shared memory: one launch, no workspace.  Longer ones are
-// counted in units of 64 tokens; the units of all segments form one line, which is
-// cut into equal pieces, one per CTA, from the lengths on the device.  Long and
-// short sequences balance without the host knowing them, and a captured call stays
-// right as they grow.  A segment that a cut crosses leaves partial sums in the
-// workspace, which a second kernel joins in a fixed order.
-//
-// Bound.  512 bytes per (token, KV head) at d = 128: HBM.
+// bsfa_decode16.cu -- bsfa_decode16: the host side.  The kernels are in
+// bsfa_decode16.cuh, instantiated by inst_decode16_*.cu.
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cmath>
 #include <cstdint>
-#include <type_traits>
 
 #include "bsfa.h"
 #include "bsfa_cache16.h"
 #include "bsfa_cache4.h"
-#include "fp4.cuh"
+#include "bsfa_decode16.cuh"
 
 namespace bsfa {
 
+namespace decode16 {
+extern template bsfa_status run<64, false>(const DecArgs&, const Plan&, int, int, cudaStream_t);
+extern template bsfa_status run<64, true>(const DecArgs&, const Plan&, int, int, cudaStream_t);
+extern template bsfa_status run<128, false>(const DecArgs&, const Plan&, int, int, cudaStream_t);
+extern template bsfa_status run<128, true>(const DecArgs&, const Plan&, int, int, cudaStream_t);
+}  // namespace decode16
+
 namespace {
 
-constexpr int WARPS = 4;
-constexpr int THREADS = 32 * WARPS;
-constexpr int TOK = 16;             // tokens of a warp's tile
-constexpr int UNIT = TOK * WARPS;   // tokens of a work unit
-constexpr float HEADROOM = 5.f;     // log2 a weight may pass 2^SHIFT by
-constexpr float SHIFT = 10.f;       // log2 of the factor that a weight carries
-constexpr float NO_SCORE = 3e38f;   // a row's offset before its first score
-constexpr int MIN_UNITS = 4;        // shortest piece of the line worth a CTA
-constexpr int SEGMENT_UNITS = 3;    // a segment's fixed cost, in units
-constexpr int JOIN_THREADS = 256;   // of the kernel that joins parts
-constexpr int JOIN_ROWS_PARTS = 8;  // a warp to a row below, a block above
-constexpr int CTAS = 2;             // CTAs of a cut call on an SM
-constexpr int MAX_GRID = 320;       // CTAs of a cut call, at most
-constexpr int MAX_PARTS = 512;      // what the join's table holds: at least MAX_GRID
-constexpr int MAX_CLUSTER = 8;      // CTAs that share a segment, at most
-constexpr int CLUSTER_UNITS = 16;   // units of a segment per CTA of a cluster, at most
-
-template <int D>
-struct Ring {
-  static constexpr int HALF = TOK * D * 2;  // bytes of a tile's keys, or values
-  static constexpr int STAGE = 2 * HALF;
-  static constexpr int STAGES = D == 128 ? 3 : 6;
-  static constexpr int BYTES = STAGE * STAGES;  // of a warp
-};
-
-// Row stride of a warp's sums in shared memory, in floats: the eight elements and
-// four columns of a fragment fall into different banks.
-template <int D>
-constexpr int MERGE_ROW = D + 4;
-
-// Dynamic shared memory: the rings, whose place the warps' sums take later, and
-// behind them what the CTAs of a cluster send each other.
-template <int D, int NT, int W>
-constexpr int ring_bytes() {
-  constexpr int ring = W * Ring<D>::BYTES;
-  constexpr int merge = W * MERGE_ROW<D> * 8 * NT * 4;
-  return ring > merge ? ring : merge;
-}
-template <int D, int NT, int W>
-constexpr int smem_bytes(bool cluster) {
-  return ring_bytes<D, NT, W>() + (cluster ? 8 * NT * D * 4 : 0);
-}
-
-struct DecArgs {
-  const uint8_t *k, *v;
-  long long k_sp, k_sh, v_sp, v_sh;  // page and head strides in bytes
-  int k_st, v_st;                    // token strides in bytes
-  const int32_t* table;
-  int table_stride, num_pages, tiles_per_page;
-  const uint16_t* q;
-  uint16_t* o;
-  long long q_s[3], o_s[3];
-  const int32_t* seqlens;
-  int batch, heads_kv, group, q_len, rows, row_tiles, max_len;
-  int causal, f16, split, cluster, join_by_segment;
-  float sigma_log2;
-  float* lse;
-  long long lse_pitch;
-  float* part_o;    // [grid][2][rows of a CTA][d]
-  float2* part_ml;  // [grid][2][rows of a CTA]
-  int4* joins;      // [jobs]: {sequence, kvh * row_tiles + row tile, first, last CTA}, or x < 0
-};
-
-// The sequence length that the call sees.
-__device__ __forceinline__ int clamp_len(const DecArgs& a, int b) {
-  return max(0, min(__ldg(a.seqlens + b), a.max_len));
-}
-// Units of a segment on the line: its tokens', and what a CTA spends on any segment
-// (queries, the first copies' latency, the join of its warps).
-__device__ __forceinline__ int units_of(int len) { return SEGMENT_UNITS + (len + UNIT - 1) / UNIT; }
-
-// Where a CTA's piece of the line begins.
-struct Piece {
-  int begin, end;   // units
-  int b, base;      // sequence of `begin`, and the units before it
-  int per_cta;
-};
-
-// Cuts the line.  Every CTA adds up the lengths by itself: a few loads per
-// thread, no extra launch.
-__device__ __forceinline__ Piece cut(const DecArgs& a, int* sh) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int chunk = (a.batch + THREADS - 1) / THREADS;
-  const int b0 = min(a.batch, tid * chunk), b1 = min(a.batch, b0 + chunk);
-  const int per_unit = a.heads_kv * a.row_tiles;
-  int sum = 0;
-  for (int b = b0; b < b1; ++b) sum += units_of(clamp_len(a, b));
-  int incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) sh[warp] = incl;
-  __syncthreads();
-  int before = incl - sum, total = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    if (w < warp) before += sh[w];
-    total += sh[w];
-  }
-  Piece p;
-  const int all = total * per_unit;
-  p.per_cta = max(MIN_UNITS, (all + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
-  p.begin = static_cast<int>(min(static_cast<long long>(all),
-                                 static_cast<long long>(blockIdx.x) * p.per_cta));
-  p.end = min(all, p.begin + p.per_cta);
-  const int at = p.begin / per_unit;
-  if (at >= before && at < before + sum) {
-    int base = before;
-    for (int b = b0; b < b1; ++b) {
-      const int n = units_of(clamp_len(a, b));
-      if (at < base + n) {
-        sh[WARPS] = b;
-        sh[WARPS + 1] = base * per_unit;
-        break;
-      }
-      base += n;
-    }
-  }
-  __syncthreads();
-  p.b = sh[WARPS];
-  p.base = sh[WARPS + 1];
-  return p;
-}
-
-// Four elements of an output row, and with the first of them its log-sum-exp:
-// `row` is the query row within the KV head's group, y and l are relative to 2^m.
-__device__ __forceinline__ void store_row4(const DecArgs& a, int b, int kvh, int row, int d0,
-                                           float m, float l, float4 y) {
-  const int i = row / a.group, h = kvh * a.group + (row - i * a.group);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint2 w;
-  w.x = f32_to_x2(y.x * inv, y.y * inv, a.f16);
-  w.y = f32_to_x2(y.z * inv, y.w * inv, a.f16);
-  *reinterpret_cast<uint2*>(a.o + b * a.o_s[0] + h * a.o_s[1] + i * a.o_s[2] + d0) = w;
-  if (a.lse != nullptr && d0 == 0)
-    a.lse[h * a.lse_pitch + static_cast<long long>(b) * a.q_len + i] =
-        l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-}
-
-template <bool F16>
-__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                          uint32_t b1) {
-  if constexpr (F16)
-    mma_f16_16816(c, a[0], a[1], a[2], a[3], b0, b1);
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Four 8 x 8 matrices of 16-bit elements, row pointers from the lanes in order;
-// transposed, or as they lie.
-__device__ __forceinline__ void ldmatrix(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldmatrix_trans(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-
-// Two elements, those that are not finite as zeros.
-template <bool F16>
-__device__ __forceinline__ uint32_t finite_or_zero(uint32_t x) {
-  constexpr uint32_t LOW = F16 ? 0x7c00u : 0x7f80u, HIGH = LOW << 16;
-  if ((x & LOW) == LOW) x &= 0xffff0000u;
-  if ((x & HIGH) == HIGH) x &= 0xffffu;
-  return x;
-}
-
-// Four 16-byte copies, `step` bytes of global memory apart; `ok` false reads
-// nothing and writes zeros.
-__device__ __forceinline__ void cp_async4(uint32_t d0, uint32_t d1, uint32_t d2, uint32_t d3,
-                                          const uint8_t* src, int step, bool ok) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %8, 0;\n\t"
-      "cp.async.cg.shared.global [%0], [%4], 16, p;\n\t"
-      "cp.async.cg.shared.global [%1], [%5], 16, p;\n\t"
-      "cp.async.cg.shared.global [%2], [%6], 16, p;\n\t"
-      "cp.async.cg.shared.global [%3], [%7], 16, p;\n\t}" ::"r"(d0),
-      "r"(d1), "r"(d2), "r"(d3), "l"(src), "l"(src + step), "l"(src + 2 * step),
-      "l"(src + 3 * step), "r"(static_cast<uint32_t>(ok))
-      : "memory");
-}
-
-template <int D, int NT, bool F16, int W>
-__global__ void __launch_bounds__(32 * W, CTAS) decode16_kernel(const __grid_constant__ DecArgs a) {
-  constexpr int WARPS = W, THREADS = 32 * W;  // of this CTA
-  constexpr int UNIT_TILES = UNIT / TOK;
-  constexpr int STAGES = Ring<D>::STAGES, STAGE = Ring<D>::STAGE, HALF = Ring<D>::HALF;
-  constexpr int KSTEPS = D / 16;  // 16-element steps of K Q^T
-  constexpr int MT = D / 16;      // 16-row tiles of V^T P^T
-  constexpr int ROWS = 8 * NT;
-  constexpr int PITCH = 2 * D;    // bytes of a row
-  constexpr int CHUNKS = D / 8;   // ... in pieces of 16
-  extern __shared__ __align__(1024) uint8_t ring[];
-  __shared__ int sh_cut[WARPS + 2];
-  __shared__ uint2 sh_q[NT * KSTEPS * 32];
-  __shared__ int sh_lim[ROWS];  // positions below it are visible to the row
-  __shared__ float2 sh_ml[WARPS][ROWS];
-  __shared__ float2 sh_cluster[MAX_CLUSTER][ROWS];
-
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, c = lane & 3;
-  // The query row (of the CTA's) of this lane's column e of tile nt.
-  auto col_row = [&](int nt, int e) { return nt * 8 + 2 * c + e; };
-
-  if (a.cluster > 1) cluster_arrive();
-  Piece piece;
-  if (W == bsfa::WARPS && a.split) {
-    if (tid == 0 && !a.join_by_segment) a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    piece = cut(a, sh_cut);
-  } else {  // one segment per cluster; u walks over it once
-    const int seg = static_cast<int>(blockIdx.x) / a.cluster, per_b = a.heads_kv * a.row_tiles;
-    piece.b = seg / per_b;
-    const int n = units_of(clamp_len(a, piece.b));
-    piece.base = 0;
-    piece.begin = (seg - piece.b * per_b) * n;
-    piece.end = piece.begin + n;
-    piece.per_cta = n;
-  }
-
-  const uint32_t my_ring = smem_u32(ring) + warp * Ring<D>::BYTES;
-  int u = piece.begin, b = piece.b, base = piece.base;
-  while (u < piece.end) {
-    const int len = clamp_len(a, b);
-    const int n_units = units_of(len);
-    const int seg = (u - base) / n_units;  // kvh * row_tiles + row tile
-    const int u0 = u - base - seg * n_units;
-    const int u1 = min(n_units, u0 + piece.end - u);
-    const int kvh = seg / a.row_tiles;
-    const int r0 = (seg - kvh * a.row_tiles) * ROWS;  // first query row
-    const int n_rows = min(ROWS, a.rows - r0);
-
-    // Positions that the rows of this tile see: each row its own limit, all of
-    // them below max_lim, and everything below min_lim by all.
-    const int first_i = r0 / a.group, last_i = (r0 + n_rows - 1) / a.group;
-    const int min_lim = a.causal ? max(0, len - a.q_len + first_i + 1) : len;
-    const int max_lim = a.causal ? max(0, len - a.q_len + last_i + 1) : len;
-
-    // ---- this warp's tiles: an equal run of the piece's
-    int t0 = max(0, u0 - SEGMENT_UNITS) * UNIT_TILES;
-    int t1 = min(max(0, u1 - SEGMENT_UNITS) * UNIT_TILES, (max_lim + TOK - 1) / TOK);
-    if (a.cluster > 1) {  // this CTA's share of the segment
-      const int share = (t1 + a.cluster - 1) / a.cluster;
-      t0 = min(t1, static_cast<int>(cluster_rank()) * share);
-      t1 = min(t1, t0 + share);
-    }
-    const int run = (max(0, t1 - t0) + WARPS - 1) / WARPS;
-    const int t_begin = t0 + warp * run, t_end = min(t1, t_begin + run);
-    const int n_tiles = max(0, t_end - t_begin);
-
-    // ---- copies: a lane copies piece cp_chunk of rows cp_row, cp_row + 32 / CHUNKS
-    // and so on; its source addresses step through a page and are formed anew where
-    // one begins, with the next page's table entry in flight meanwhile.  Piece c of
-    // row t lies at place c ^ (t & 7) of its row: eight rows' pieces at once, what
-    // ldmatrix reads, fall into different banks.
-    constexpr int COPIES = TOK * CHUNKS / 32;  // of a lane, of the keys of a tile
-    constexpr int STEP = 32 / CHUNKS;          // rows that a copy of all lanes covers
-    const int cp_row = lane / CHUNKS, cp_chunk = lane % CHUNKS;
-    // The first copy's place in a stage; copy i's is i * STEP rows on, with the bits of
-    // i * STEP exclusive-ored into its piece.
-    const uint32_t cp_at = cp_row * PITCH + ((cp_chunk ^ cp_row) << 4);
-    const int32_t* table = a.table + static_cast<long long>(b) * a.table_stride;
-    int cp_left = n_tiles;  // tiles of pages not opened yet
-    int cp_col = 0, cp_entry = -1;
-    int cp_run = 0;  // tiles of the open page still to copy
-    bool cp_ok = false;
-    const uint8_t *k_src = a.k, *v_src = a.v;
-    auto open_page = [&](int off) {  // the page cp_entry names, from its tile `off`
-      cp_ok = static_cast<uint32_t>(cp_entry) < static_cast<uint32_t>(a.num_pages);
-      const long long page = cp_ok ? cp_entry : 0;
-      const int row = off * TOK + cp_row;
-      k_src = a.k + (page * a.k_sp + kvh * a.k_sh + row * a.k_st + cp_chunk * 16);
-      v_src = a.v + (page * a.v_sp + kvh * a.v_sh + row * a.v_st + cp_chunk * 16);
-      cp_run = min(cp_left, a.tiles_per_page - off);
-      cp_left -= cp_run;
-      if (cp_left > 0) cp_entry = __ldg(table + ++cp_col);
-    };
-    auto copy_tile = [&](uint32_t dst) {
-      if (cp_run > 0) {
-        const uint32_t at = dst + cp_at;
-        auto place = [&](int i) {
-          return (at ^ (((i * STEP) & 7) << 4)) + static_cast<uint32_t>(i * STEP * PITCH);
-        };
-#pragma unroll
-        for (int i = 0; i < COPIES; i += 4)
-          cp_async4(place(i), place(i + 1), place(i + 2), place(i + 3), k_src + i * STEP * a.k_st,
-                    STEP * a.k_st, cp_ok);
-#pragma unroll
-        for (int i = 0; i < COPIES; i += 4)
-          cp_async4(place(i) + HALF, place(i + 1) + HALF, place(i + 2) + HALF, place(i + 3) + HALF,
-                    v_src + i * STEP * a.v_st, STEP * a.v_st, cp_ok);
-        k_src += TOK * a.k_st;
-        v_src += TOK * a.v_st;
-        if (--cp_run == 0 && cp_left > 0) open_page(0);
-      }
-      cp_async_commit();
-    };
-    auto start = [&]() {  // the first copies of this warp's run
-      cp_left = n_tiles;
-      cp_col = t_begin / a.tiles_per_page;
-      cp_entry = cp_left > 0 ? __ldg(table + cp_col) : -1;
-      if (cp_left > 0) open_page(t_begin - cp_col * a.tiles_per_page);
-#pragma unroll
-      for (int s = 0; s < STAGES - 1; ++s) copy_tile(my_ring + s * STAGE);
-    };
-    start();
-
-    // ---- queries: fragments of Q^T
-    for (int nt = warp; nt < NT; nt += WARPS) {
-      const int q_row = nt * 8 + g, r = r0 + q_row;
-      uint2 f[KSTEPS];
-#pragma unroll
-      for (int j = 0; j < KSTEPS; ++j) f[j] = make_uint2(0u, 0u);
-      if (r < a.rows) {
-        const int i = r / a.group, h = kvh * a.group + (r - i * a.group);
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(
-            a.q + b * a.q_s[0] + h * a.q_s[1] + i * a.q_s[2] + 2 * c);
-#pragma unroll
-        for (int j = 0; j < KSTEPS; ++j) f[j] = make_uint2(__ldg(src + 8 * j), __ldg(src + 8 * j + 4));
-      }
-      // Rows past the last are computed along with the rest and not stored.
-      if (c == 0) sh_lim[q_row] = !a.causal || r >= a.rows ? len : len - a.q_len + r / a.group + 1;
-#pragma unroll
-      for (int j = 0; j < KSTEPS; ++j) sh_q[(nt * KSTEPS + j) * 32 + lane] = f[j];
-    }
-    __syncthreads();
-
-    // ---- per-lane columns: 2c and 2c + 1 of each row tile
-    float acc[NT][MT][4];
-    float sum[NT][2];
-    float zn[NT][2];  // a weight is 2^(score + zn)
-    uint2 qf[NT == 1 ? KSTEPS : 1];  // one row tile's queries stay in registers
-    auto clear = [&]() {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[nt][mt][e] = 0.f;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) zn[nt][e] = NO_SCORE, sum[nt][e] = 0.f;
-      }
-    };
-    clear();
-    if constexpr (NT == 1) {
-#pragma unroll
-      for (int j = 0; j < KSTEPS; ++j) qf[j] = sh_q[j * 32 + lane];
-    }
-    const uint32_t q_addr = smem_u32(sh_q) + lane * 8;
-    // This lane's row pointers in a stage: of keys, token lane & 15, element 8 (lane
-    // >> 4); of values, token (lane & 7) + 8 (lane >> 4), element 8 (lane >> 3 & 1).
-    // Pieces 2j on are an exclusive or away.
-    const uint32_t k_at = (lane & 15) * PITCH + (((lane >> 4) ^ (lane & 7)) << 4);
-    const uint32_t v_at = HALF + ((lane & 7) + (lane >> 4) * 8) * PITCH +
-                          ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
-
-    // MASKED: some row does not see the whole tile.  EXACT: values that are not finite
-    // stay out of the products and are added one by one, see below.
-    auto tile = [&](const uint32_t st, const int tok0, auto masked_tag, auto exact_tag) {
-      constexpr bool MASKED = decltype(masked_tag)::value, EXACT = decltype(exact_tag)::value;
-      // ---- S^T = K Q^T; up to two row tiles leave registers for two sums each, which
-      // halves the chain of dependent products
-      constexpr int SUMS = NT <= 2 ? 2 : 1;
-      float s[NT][4], s2[SUMS == 2 ? NT : 1][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = s2[SUMS == 2 ? nt : 0][e] = 0.f;
-#pragma unroll
-      for (int j = 0; j < KSTEPS; ++j) {
-        uint32_t k[4];
-        ldmatrix(k, (st + k_at) ^ (j << 5));
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint2 q2 = NT == 1 ? qf[NT == 1 ? j : 0] : lds64(q_addr + (nt * KSTEPS + j) * 256);
-          mma_16816<F16>(SUMS == 2 && (j & 1) ? s2[SUMS == 2 ? nt : 0] : s[nt], k, q2.x, q2.y);
-        }
-      }
-      // ---- weights; the offset falls where one would pass 2^(SHIFT + HEADROOM)
-      float y[NT][4];
-      auto hidden = [&](int nt, int e) {
-        return tok0 + g + (e & 2) * 4 >= sh_lim[col_row(nt, e & 1)];
-      };
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (SUMS == 2) s[nt][e] += s2[nt][e];
-          s[nt][e] *= a.sigma_log2;
-          if (MASKED && hidden(nt, e)) s[nt][e] = -INFINITY;
-        }
-      bool over = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[nt][e] = s[nt][e] + zn[nt][e & 1];
-          over |= y[nt][e] > SHIFT + HEADROOM;
-        }
-      if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float m = fmaxf(s[nt][e], s[nt][e + 2]);
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-            const float z = fminf(zn[nt][e], SHIFT - m);
-            const float f = ex2_approx(z - zn[nt][e]);
-            zn[nt][e] = z;
-            sum[nt][e] *= f;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              acc[nt][mt][e] *= f;
-              acc[nt][mt][e + 2] *= f;
-            }
-            y[nt][e] = s[nt][e] + z;
-            y[nt][e + 2] = s[nt][e + 2] + z;
-          }
-      }
-      // The products take 16-bit factors: a weight goes in as two, itself rounded and
-      // the remainder rounded, which leaves 2^-16 of it (bf16; fp16 2^-22) and makes
-      // O as good as its own rounding.
-      uint32_t hi[NT][2], lo[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[nt][e] = ex2_approx(y[nt][e]);
-          sum[nt][e & 1] += y[nt][e];
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t w = pack_x2<F16>(y[nt][2 * x], y[nt][2 * x + 1]);
-          const float2 r = x2_to_f32(w, F16);
-          hi[nt][x] = movmatrix_trans(w);
-          lo[nt][x] = movmatrix_trans(pack_x2<F16>(y[nt][2 * x] - r.x, y[nt][2 * x + 1] - r.y));
-        }
-      }
-      if (MASKED && tok0 + TOK > max_lim) {
-        // A hidden value weighs nothing even where it is not a number.
-        const int first = max(0, max_lim - tok0);
-        for (int x = first * CHUNKS + lane; x < TOK * CHUNKS; x += 32)
-          asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(st + HALF + x * 16), "r"(0)
-                       : "memory");
-        __syncwarp();
-      }
-      // ---- O^T += V^T P^T.  The tensor cores cut off what they add to a sum instead
-      // of rounding it, so a tile's sum starts at zero and is added in fp32.
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        uint32_t v[4];
-        ldmatrix_trans(v, (st + v_at) ^ (mt << 5));
-        if constexpr (EXACT) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) v[x] = finite_or_zero<F16>(v[x]);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float o[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_16816<F16>(o, v, lo[nt][0], lo[nt][1]);
-          mma_16816<F16>(o, v, hi[nt][0], hi[nt][1]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[nt][mt][e] += o[e];
-        }
-      }
-      if constexpr (EXACT) {
-#pragma unroll 1
-        for (int t = 0; t < TOK; ++t) {
-          float p[NT][2];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float w =
-                  __shfl_sync(0xffffffffu, t < 8 ? y[nt][e] : y[nt][e + 2], 4 * (t & 7) + c);
-              p[nt][e] = tok0 + t < sh_lim[col_row(nt, e)] ? w : -1.f;  // a weight is not negative
-            }
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t at = st + HALF + t * PITCH + (((2 * mt + x) ^ (t & 7)) << 4) + 2 * g;
-              const float v = x2_to_f32(lds16(at), F16).x;
-              if (fabsf(v) < INFINITY) continue;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  if (!(p[nt][e] < 0.f))
-                    acc[nt][mt][e + 2 * x] = fmaf(p[nt][e], v, acc[nt][mt][e + 2 * x]);
-            }
-        }
-      }
-    };
-
-    uint32_t rd = my_ring, wr = my_ring + (STAGES - 1) * STAGE;
-    const uint32_t ring_end = my_ring + STAGES * STAGE;
-    auto next_tile = [&]() {
-      cp_async_wait<STAGES - 2>();
-      __syncwarp();  // every lane's copies of this tile are in, and the last one is read
-      copy_tile(wr);
-      const uint32_t st = rd;
-      rd = rd + STAGE == ring_end ? my_ring : rd + STAGE;
-      wr = wr + STAGE == ring_end ? my_ring : wr + STAGE;
-      return st;
-    };
-    // Tiles that every row sees in whole come first; the few others take the
-    // masked path in a loop of their own.
-    const int t_full = max(t_begin, min(t_end, min_lim / TOK));
-    int t = t_begin;
-    for (; t < t_full; ++t) tile(next_tile(), 0, std::false_type{}, std::false_type{});
-    for (; t < t_end; ++t) tile(next_tile(), t * TOK, std::true_type{}, std::false_type{});
-    cp_async_wait<0>();
-
-    // A value that is not finite makes the products of every row NaN: of those that
-    // do not see its token (weight 0), and of those whose weight leaves no remainder
-    // or a negative one.  So sums that are not finite are formed once more, with such
-    // values apart; the others' sums are the same bit for bit.
-    bool finite = true;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) finite = finite && fabsf(acc[nt][mt][e]) < INFINITY;
-    if (!__all_sync(0xffffffffu, finite)) {
-      clear();
-      __syncwarp();
-      start();
-      rd = my_ring, wr = my_ring + (STAGES - 1) * STAGE;
-      for (t = t_begin; t < t_end; ++t) tile(next_tile(), t * TOK, std::true_type{}, std::true_type{});
-      cp_async_wait<0>();
-    }
-
-    // ---- join the warps: common offset, then one sum of the scaled parts
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float l = sum[nt][e];
-        l += __shfl_xor_sync(0xffffffffu, l, 4);
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (g == 0) sh_ml[warp][col_row(nt, e)] = make_float2(-zn[nt][e], l);
-      }
-    __syncthreads();  // also: every warp is done with its ring, which the sums reuse
-    float* merge = reinterpret_cast<float*>(ring);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = col_row(nt, e);
-        float m = sh_ml[0][r].x;
-#pragma unroll
-        for (int w = 1; w < WARPS; ++w) m = fmaxf(m, sh_ml[w][r].x);
-        const float f = ex2_approx(-zn[nt][e] - m);
-        float* dst = merge + (warp * ROWS + r) * MERGE_ROW<D> + g;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          dst[16 * mt] = acc[nt][mt][e] * f;
-          dst[16 * mt + 8] = acc[nt][mt][e + 2] * f;
-        }
-      }
-    __syncthreads();
-    // Row r's offset and sum, and the sum of four elements of it, over the warps.
-    auto joined_ml = [&](int r) {
-      float m = sh_ml[0][r].x, l = 0.f;
-#pragma unroll
-      for (int w = 1; w < WARPS; ++w) m = fmaxf(m, sh_ml[w][r].x);
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) l += sh_ml[w][r].y * ex2_approx(sh_ml[w][r].x - m);
-      return make_float2(m, l);
-    };
-    auto joined = [&](int r, int d0) {
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float4 x =
-            *reinterpret_cast<const float4*>(merge + (w * ROWS + r) * MERGE_ROW<D> + d0);
-        y.x += x.x, y.y += x.y, y.z += x.z, y.w += x.w;
-      }
-      return y;
-    };
-    if (a.cluster > 1) {
-      // Output x of the segment (four elements) is joined by CTA x % cluster: each
-      // CTA stores its sums, and the offsets, straight into the joining CTAs' shared
-      // memory, and after one barrier every CTA adds what it got, over the CTAs in
-      // order.
-      const int items = ROWS * (D / 4) / a.cluster;  // the cluster is a power of two
-      const uint32_t rank = cluster_rank(), got = smem_u32(ring) + ring_bytes<D, NT, W>();
-      cluster_wait();  // the one of the kernel's beginning: every CTA runs
-      for (int x = tid; x < n_rows * (D / 4); x += THREADS) {
-        const int r = x / (D / 4), d0 = (x % (D / 4)) * 4;
-        cluster_st4(got + (rank * items + x / a.cluster) * 16, x % a.cluster, joined(r, d0));
-      }
-      for (int x = tid; x < n_rows * a.cluster; x += THREADS) {
-        const int r = x / a.cluster;
-        cluster_st2(smem_u32(&sh_cluster[rank][r]), x % a.cluster, joined_ml(r));
-      }
-      cluster_arrive();
-      cluster_wait();
-      const float4* parts = reinterpret_cast<const float4*>(ring + ring_bytes<D, NT, W>());
-      for (int k = tid; k * a.cluster + rank < n_rows * (D / 4); k += THREADS) {
-        const int x = k * a.cluster + rank, r = x / (D / 4), d0 = (x % (D / 4)) * 4;
-        float m = sh_cluster[0][r].x;
-        for (int c1 = 1; c1 < a.cluster; ++c1) m = fmaxf(m, sh_cluster[c1][r].x);
-        float l = 0.f;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c1 = 0; c1 < a.cluster; ++c1) {
-          const float2 ml = sh_cluster[c1][r];
-          const float4 p = parts[c1 * items + k];
-          const float f = ex2_approx(ml.x - m);
-          l += ml.y * f;
-          y.x += p.x * f, y.y += p.y * f, y.z += p.z * f, y.w += p.w * f;
-        }
-        store_row4(a, b, kvh, r0 + r, d0, m, l, y);
-      }
-      return;
-    }
-    const bool began = u0 == 0, whole = began && u1 == n_units;
-    const int part = 2 * static_cast<int>(blockIdx.x) + (began ? 1 : 0);
-    for (int x = tid; x < n_rows * (D / 4); x += THREADS) {
-      const int r = x / (D / 4), d0 = (x % (D / 4)) * 4;
-      const float2 ml = joined_ml(r);
-      const float4 y = joined(r, d0);
-      if (whole) {
-        store_row4(a, b, kvh, r0 + r, d0, ml.x, ml.y, y);
-      } else {
-        *reinterpret_cast<float4*>(a.part_o + (static_cast<long long>(part) * ROWS + r) * D + d0) =
-            y;
-        if (d0 == 0) a.part_ml[static_cast<long long>(part) * ROWS + r] = ml;
-      }
-    }
-    if (began && tid == 0) {
-      const int4 job =
-          make_int4(whole ? -1 : b, seg, blockIdx.x, (u + n_units - 1) / piece.per_cta);
-      if (a.join_by_segment)
-        a.joins[b * a.heads_kv * a.row_tiles + seg] = job;
-      else if (!whole)
-        a.joins[blockIdx.x] = job;
-    }
-    __syncthreads();  // the ring and sh_ml are free again
-
-    u += u1 - u0;
-    if (u1 == n_units && seg == a.heads_kv * a.row_tiles - 1) {
-      base += n_units * a.heads_kv * a.row_tiles;
-      ++b;
-    }
-  }
-}
-
-// Joins the parts of the segments that a cut crossed: block (x, r) takes row r
-// of job x, which is segment x, or where there are more segments than CTAs the
-// one that CTA x began and did not finish -- if that was cut.  The parts lie in
-// the CTAs first (its second slot) .. last (their first slots).  The offsets come
-// first, all at once, so that the sums' loads wait for nothing.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(JOIN_THREADS, 4) decode16_join_kernel(const DecArgs a) {
-  constexpr int LANES = D / 4;                 // threads that cover a row, four elements each
-  constexpr int PARTS = JOIN_THREADS / LANES;  // parts read at once
-  __shared__ float4 sh_y[PARTS][LANES];
-  __shared__ float2 sh_ml[JOIN_THREADS / 32];
-  __shared__ float sh_w[MAX_PARTS];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 job = a.joins[blockIdx.x];
-  if (job.x < 0) return;
-  const int b = job.x, kvh = job.y / a.row_tiles;
-  const int r = blockIdx.y, row = (job.y - kvh * a.row_tiles) * ROWS + r;
-  if (row >= a.rows) return;
-  const int first = job.z, count = job.w - first + 1;  // at most the CTAs, so MAX_PARTS
-  const int tid = threadIdx.x;
-  auto slot = [&](int p) { return 2LL * (first + p) + (p == 0 ? 1 : 0); };
-
-  float2 mine[MAX_PARTS / JOIN_THREADS];
-  float m = -NO_SCORE;
-#pragma unroll
-  for (int x = 0; x < MAX_PARTS / JOIN_THREADS; ++x) {
-    const int p = tid + x * JOIN_THREADS;
-    mine[x] = p < count ? a.part_ml[slot(p) * ROWS + r] : make_float2(-NO_SCORE, 0.f);
-    m = fmaxf(m, mine[x].x);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((tid & 31) == 0) sh_ml[tid >> 5].x = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < JOIN_THREADS / 32; ++w) m = fmaxf(m, sh_ml[w].x);
-  float l = 0.f;
-#pragma unroll
-  for (int x = 0; x < MAX_PARTS / JOIN_THREADS; ++x) {
-    const float w = ex2_approx(mine[x].x - m);
-    l += mine[x].y * w;
-    sh_w[tid + x * JOIN_THREADS] = w;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if ((tid & 31) == 0) sh_ml[tid >> 5].y = l;
-  __syncthreads();
-  l = 0.f;
-#pragma unroll
-  for (int w = 0; w < JOIN_THREADS / 32; ++w) l += sh_ml[w].y;
-
-  const int lane = tid % LANES, p0 = tid / LANES;
-  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int p = p0; p < count; p += PARTS) {
-    const float4 x = reinterpret_cast<const float4*>(a.part_o + (slot(p) * ROWS + r) * D)[lane];
-    const float w = sh_w[p];
-    y.x += x.x * w, y.y += x.y * w, y.z += x.z * w, y.w += x.w * w;
-  }
-  sh_y[p0][lane] = y;
-  __syncthreads();
-  if (p0 != 0) return;
-#pragma unroll
-  for (int p = 1; p < PARTS; ++p) {
-    const float4 x = sh_y[p][lane];
-    y.x += x.x, y.y += x.y, y.z += x.z, y.w += x.w;
-  }
-  store_row4(a, b, kvh, row, 4 * lane, m, l, y);
-}
-
-// The same where segments have few parts: a warp takes a row of job x by itself,
-// 32 parts' offsets at a time.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(JOIN_THREADS) decode16_join_rows_kernel(const DecArgs a) {
-  constexpr int E = D / 32;  // elements of a lane
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 job = a.joins[blockIdx.x];
-  if (job.x < 0) return;
-  const int lane = threadIdx.x & 31;
-  const int r = blockIdx.y * (JOIN_THREADS / 32) + (threadIdx.x >> 5);
-  const int b = job.x, kvh = job.y / a.row_tiles;
-  const int row = (job.y - kvh * a.row_tiles) * ROWS + r;
-  if (r >= ROWS || row >= a.rows) return;
-  const int first = job.z, count = job.w - first + 1;
-  auto slot = [&](int p) { return 2LL * (first + p) + (p == 0 ? 1 : 0); };
-  float m = -NO_SCORE, l = 0.f, y[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) y[e] = 0.f;
-  for (int p0 = 0; p0 < count; p0 += 32) {
-    const float2 ml = p0 + lane < count ? a.part_ml[slot(p0 + lane) * ROWS + r]
-                                        : make_float2(-NO_SCORE, 0.f);
-    float m1 = fmaxf(m, ml.x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
-    const float f = ex2_approx(m - m1), w = ex2_approx(ml.x - m1);
-    float sum = ml.y * w;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    m = m1;
-    l = l * f + sum;
-#pragma unroll
-    for (int e = 0; e < E; ++e) y[e] *= f;
-#pragma unroll 4
-    for (int p = p0; p < min(count, p0 + 32); ++p) {
-      const float wp = __shfl_sync(0xffffffffu, w, p - p0);
-      const float* x = a.part_o + (slot(p) * ROWS + r) * D + lane * E;
-      if constexpr (E == 4) {
-        const float4 z = *reinterpret_cast<const float4*>(x);
-        y[0] += z.x * wp, y[1] += z.y * wp, y[2] += z.z * wp, y[3] += z.w * wp;
-      } else {
-        const float2 z = *reinterpret_cast<const float2*>(x);
-        y[0] += z.x * wp, y[1] += z.y * wp;
-      }
-    }
-  }
-  if constexpr (E == 4) {
-    store_row4(a, b, kvh, row, 4 * lane, m, l, make_float4(y[0], y[1], y[2], y[3]));
-  } else {  // two lanes' elements to one store
-    const float z0 = __shfl_down_sync(0xffffffffu, y[0], 1);
-    const float z1 = __shfl_down_sync(0xffffffffu, y[1], 1);
-    if ((lane & 1) == 0)
-      store_row4(a, b, kvh, row, 2 * lane, m, l, make_float4(y[0], y[1], z0, z1));
-  }
-}
+using namespace decode16;
 
 // Query row tiles of a call: as few tensor-core columns as hold its rows, up
 // to 32 to a CTA, and equal shares where one CTA does not hold them.
-struct Plan {
-  int nt, row_tiles, units, cluster;
-  long long segments, all_units;
-  bool split;
-};
-
 Plan plan_of(const bsfa_cache16* c, const bsfa_decode4_params* p) {
   Plan pl;
   const long long rows = static_cast<long long>(p->num_heads_q / c->num_heads_kv) * p->q_len;
@@ -847,14 +37,29 @@ Plan plan_of(const bsfa_cache16* c, const bsfa_decode4_params* p) {
   // (Beyond 2^31 segments, which are refused, the product could overflow.)
   pl.all_units =
       pl.segments >> 31 ? pl.segments : pl.segments * (pl.units + SEGMENT_UNITS);
-  // A segment gets as many CTAs as keep all resident at once.
+  constexpr int grids[2][4] = {
+      {Shape<64, 1>::MAX_GRID, Shape<64, 2>::MAX_GRID, Shape<64, 3>::MAX_GRID,
+       Shape<64, 4>::MAX_GRID},
+      {Shape<128, 1>::MAX_GRID, Shape<128, 2>::MAX_GRID, Shape<128, 3>::MAX_GRID,
+       Shape<128, 4>::MAX_GRID}};
+  pl.max_grid = grids[c->head_dim == 128][pl.nt - 1];
+  // A segment gets as many CTAs as keep all resident at once; where one each is too
+  // many for that, short ones get CTAs of one warp.  Clusters of sixteen only where
+  // few are met: each has to find its place within one GPC.
+  const int resident = pl.max_grid / MAX_SMS * SMS;
+  const bool small = pl.segments > resident && pl.nt <= SMALL_NT && pl.units <= SMALL_UNITS;
+  pl.warps = small ? SMALL_WARPS : WARPS;
   pl.cluster = 1;
-  while (pl.cluster < MAX_CLUSTER && pl.units >= 2 * pl.cluster &&
-         pl.segments * 2 * pl.cluster <= MAX_GRID)
-    pl.cluster *= 2;
-  // Longer segments are cut.
-  pl.split = pl.units > CLUSTER_UNITS * pl.cluster;
-  if (pl.split) pl.cluster = 1;
+  while (pl.cluster < MAX_CLUSTER && pl.units >= 2 * pl.cluster) {
+    const int next = 2 * pl.cluster;
+    if (pl.segments * next > (next == MAX_CLUSTER ? GRID_OF_16 : resident)) break;
+    pl.cluster = next;
+  }
+  // Longer segments are cut; those that fill most of the GPU as they are, at twice the
+  // length.
+  const bool full = 2 * pl.segments * pl.cluster > resident;
+  pl.split = pl.units > (full ? 2 : 1) * CLUSTER_UNITS * pl.cluster;
+  if (pl.split) pl.cluster = 1, pl.warps = WARPS;
   return pl;
 }
 
@@ -865,7 +70,7 @@ struct Carve {
 Carve carve(const Plan& pl, int d) {
   Carve c{};
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t grid = pl.split ? static_cast<size_t>(MAX_GRID) : 0, rows = 8 * pl.nt;
+  const size_t grid = pl.split ? static_cast<size_t>(pl.max_grid) : 0, rows = 8 * pl.nt;
   c.part_o = 0;
   c.part_ml = up(c.part_o + grid * 2 * rows * d * sizeof(float));
   c.joins = up(c.part_ml + grid * 2 * rows * sizeof(float2));
@@ -890,72 +95,6 @@ bsfa_status validate_sizes(const bsfa_cache16* c, const bsfa_decode4_params* p) 
   if (pl.all_units > 0x7fffffffLL - 4096 || pl.segments * pl.cluster > 0x7fffffffLL)
     return BSFA_ERR_UNSUPPORTED;
   return BSFA_OK;
-}
-
-// The status of a runtime call.  The runtime keeps the error of one that failed
-// until it is asked for it: asked here, a later launch does not report it as its
-// own.
-bsfa_status status_of(cudaError_t e) {
-  if (e == cudaSuccess) return BSFA_OK;
-  cudaGetLastError();
-  return BSFA_ERR_CUDA;
-}
-
-// Sets a kernel's shared-memory size, once per device.
-template <int D, int NT, bool F16, int W>
-bsfa_status prepare(int dev) {
-  static std::atomic<uint64_t> ready{0};
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (ready.load(std::memory_order_relaxed) & bit) return BSFA_OK;
-  const bsfa_status v = status_of(cudaFuncSetAttribute(decode16_kernel<D, NT, F16, W>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       smem_bytes<D, NT, W>(true)));
-  if (v == BSFA_OK) ready.fetch_or(bit, std::memory_order_relaxed);
-  return v;
-}
-
-template <int D, int NT, bool F16, int W = WARPS>
-bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaStream_t stream) {
-  static_assert(MAX_GRID <= MAX_PARTS && MAX_PARTS % JOIN_THREADS == 0, "the join's weights");
-  const bsfa_status v = prepare<D, NT, F16, W>(dev);
-  if (v != BSFA_OK) return v;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr{};
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  cfg.blockDim = dim3(32 * W);
-  cfg.dynamicSmemBytes = smem_bytes<D, NT, W>(pl.cluster > 1);
-  if (!pl.split) {
-    cfg.gridDim = dim3(static_cast<unsigned>(pl.segments * pl.cluster));
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = pl.cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    return status_of(cudaLaunchKernelEx(&cfg, decode16_kernel<D, NT, F16, W>, args));
-  }
-  const long long full = static_cast<long long>(sms) * CTAS;
-  int grid = static_cast<int>(full < MAX_GRID ? full : MAX_GRID);
-  const long long most = (pl.all_units + MIN_UNITS - 1) / MIN_UNITS;
-  if (most < grid) grid = static_cast<int>(most);
-  DecArgs a = args;
-  a.join_by_segment = pl.segments <= grid;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.numAttrs = 0;
-  const bsfa_status first = status_of(cudaLaunchKernelEx(&cfg, decode16_kernel<D, NT, F16, W>, a));
-  if (first != BSFA_OK) return first;
-  // About grid / segments parts to a segment.
-  const bool by_rows = grid < JOIN_ROWS_PARTS * pl.segments;
-  constexpr int ROWS = 8 * NT;
-  const int rows = a.rows < ROWS ? a.rows : ROWS, per_block = by_rows ? JOIN_THREADS / 32 : 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(a.join_by_segment ? pl.segments : grid),
-                     (rows + per_block - 1) / per_block);
-  cfg.blockDim = dim3(JOIN_THREADS);
-  cfg.dynamicSmemBytes = 0;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.numAttrs = 1;
-  return status_of(by_rows ? cudaLaunchKernelEx(&cfg, decode16_join_rows_kernel<D, ROWS>, a)
-                           : cudaLaunchKernelEx(&cfg, decode16_join_kernel<D, ROWS>, a));
 }
 
 }  // namespace
@@ -1034,15 +173,9 @@ bsfa_status bsfa_decode16(const bsfa_cache16* cache, const bsfa_decode4_params* 
   if (v != BSFA_OK) return v;
   v = status_of(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   if (v != BSFA_OK || sms <= 0) return BSFA_ERR_CUDA;
-  using Launch = bsfa_status (*)(const DecArgs&, const Plan&, int, int, cudaStream_t);
-#define BSFA_LAUNCHES(D, F16) \
-  {launch<D, 1, F16>, launch<D, 2, F16>, launch<D, 3, F16>, launch<D, 4, F16>}
-  static const Launch launches[2][2][4] = {  // [d = 128][fp16][tiles of 8 query rows]
-      {BSFA_LAUNCHES(64, false), BSFA_LAUNCHES(64, true)},
-      {BSFA_LAUNCHES(128, false), BSFA_LAUNCHES(128, true)}};
-#undef BSFA_LAUNCHES
-  return launches[cache->head_dim == 128][a.f16][pl.nt - 1](a, pl, sms, dev,
-                                                           reinterpret_cast<cudaStream_t>(stream_));
+  const auto run_call = cache->head_dim == 128 ? (a.f16 ? run<128, true> : run<128, false>)
+                                               : (a.f16 ? run<64, true> : run<64, false>);
+  return run_call(a, pl, sms, dev, reinterpret_cast<cudaStream_t>(stream_));
 }
 
 }  // extern "C"

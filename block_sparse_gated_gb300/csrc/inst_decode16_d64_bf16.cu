@@ -1,0 +1,8 @@
+// Attention over the 16-bit cache: head dimension 64, bf16.
+#include "bsfa_decode16.cuh"
+
+namespace bsfa::decode16 {
+
+template bsfa_status run<64, false>(const DecArgs&, const Plan&, int, int, cudaStream_t);
+
+}  // namespace bsfa::decode16

@@ -484,8 +484,8 @@ typedef struct {
 /* Rows of a call.  Layouts as in bsfa_fwd_params: batched (cu_seqlens == NULL,
  * `seqlen` rows of each of `batch` sequences) or varlen (`seqlen` packed rows,
  * sequence b owns [cu_seqlens[b], cu_seqlens[b+1]); rows outside every sequence
- * are neither read nor written; offsets need not be checked by the caller: a row
- * belongs to the last sequence that begins at or before it, if that one reaches
+ * play no part and are not written; offsets need not be checked by the caller: a
+ * row belongs to the last sequence that begins at or before it, if that one reaches
  * it).  Row i of sequence b has position start[b] + i.  Strides are {batch, head,
  * token} in ELEMENTS, multiples of 8. */
 typedef struct {

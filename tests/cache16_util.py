@@ -19,12 +19,12 @@ def rotated(x: torch.Tensor, pos, freq: torch.Tensor, *, axes=None, interleaved=
             inverse=False):
     """(fp64 rows, error bound) of rotating x [.., L, d] at pos [A, L].
 
-    The kernel's sines and cosines are off by less than 2^-22: one unit in the last place of a
-    number up to 1 (2^-24), twice that for the function's own bound, the reduced angle's rounding
-    (2^-25 of at most pi / 4) and 2 pi * (2^-33 + (1 + f) |p| 2^-64) of the reduction, which is
-    below 2^-29 for |p| < 2^31 and f <= 1.  A product and a sum add 2^-24 of (|a| + |b|) each.
-    Together less than 2^-21 of |a| + |b|; then the one rounding to the type, half a step of the
-    result, or of its least subnormal."""
+    The kernel's sines and cosines are off by less than 2^-22: the reduced angle, at most pi / 4, by
+    three roundings (2^-24 of it each), their polynomials by the two last roundings (2^-24 of a
+    number up to 1 each) and 2^-29 of what they leave out, and 2 pi * (2^-33 + (1 + f) |p| 2^-64)
+    of the reduction, which is below 2^-29 for |p| < 2^31 and f <= 1.  A product and a sum add
+    2^-24 of (|a| + |b|) each.  Together less than 2^-21 of |a| + |b|; then the one rounding to
+    the type, half a step of the result, or of its least subnormal."""
     y = x.cpu().double().numpy()
     f = freq.double().numpy()
     want = ro.rotate(y, pos, f, axes=axes, interleaved=interleaved, inverse=inverse)

@@ -245,7 +245,8 @@ def test_rows_that_are_refused(lib):
         assert _write(lib, _cache(), None, r) == OK
 
 
-@pytest.mark.parametrize("source", ["bsfa_cache16", "bsfa_decode16"])
+@pytest.mark.parametrize("source", ["bsfa_cache16", "inst_decode16_d64_bf16", "inst_decode16_d64_f16",
+                                    "inst_decode16_d128_bf16", "inst_decode16_d128_f16"])
 def test_kernels_do_not_spill(lib, source):
     """The compiler warns of registers that it spills to local memory."""
     from block_sparse_gated_gb300 import build
@@ -373,7 +374,8 @@ def test_binding_checks_what_the_library_cannot_see(monkeypatch):
 
     def decode(*a, **kw):
         kw = dict(dict(layout=None, max_seqlen=None, softmax_scale=None, causal=True), **kw)
-        return n.Decode4Params.from_buffer_copy(m._decode_fields(*a, dev, **kw)[1](4096, 77))
+        _, fields, code = m._decode_fields(*a, dev, **kw)
+        return n.Decode4Params.from_buffer_copy(n.DECODE4.pack(*fields, 4096, 77, code))
 
     d = decode(q1, cache, table, lens, q1, lse=512, softmax_scale=0.5)
     assert (d.batch, d.num_heads_q, d.q_len, d.max_seqlen, d.dtype, d.causal) == (3, 8, 1, 64, 0, 1)
