@@ -6,11 +6,15 @@ there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import struct
+import sysconfig
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbsfa.so")
+BINDING_PATH = os.path.join(_HERE, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 c_int, c_float, c_void_p, c_size_t = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 c_int64 = ctypes.c_int64
@@ -102,13 +106,10 @@ class Rows16(ctypes.Structure):
     ]
 
 
-# The same as struct formats, fields in the same order.
+# The first three as struct formats, fields in the same order.
 CACHE4 = struct.Struct("@6P12q4iP2i")
 CACHE4_ROWS = struct.Struct("@2P6q2i2Pi0P")
 DECODE4 = struct.Struct("@2P6q3iPifiPPNi0P")
-CACHE16 = struct.Struct("@2P6q4iP3i0P")
-ROPE = struct.Struct("@2P2q4i64s")
-ROWS16 = struct.Struct("@5P15q5i2Pi0P")
 
 
 # bsfa_dtype
@@ -162,3 +163,25 @@ def lib() -> ctypes.CDLL:
             fn.argtypes = args
         _lib = L
     return _lib
+
+
+_binding = None
+
+
+def binding():
+    """The compiled marshalling of the 16-bit cache's calls (csrc/binding.cpp)."""
+    global _binding
+    if _binding is None:
+        import torch
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(
+                f"{BINDING_PATH} is not built: run `python -m block_sparse_gated_gb300.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_binding", BINDING_PATH)
+        m = importlib.util.module_from_spec(
+            importlib.util.spec_from_file_location("_binding", BINDING_PATH, loader=loader))
+        loader.exec_module(m)
+        if m.torch_version != torch.__version__.split("+")[0]:
+            raise RuntimeError(f"{BINDING_PATH} was built with torch {m.torch_version}: run "
+                               "`python -m block_sparse_gated_gb300.build --force`")
+        _binding = m
+    return _binding

@@ -1,18 +1,22 @@
-"""Build libbsfa.so in-tree for sm_103a with nvcc (no cmake, no torch).
+"""Build libbsfa.so in-tree for sm_103a with nvcc (no cmake, no torch), and the
+torch binding of the 16-bit cache with the host compiler.
 
     python -m block_sparse_gated_gb300.build [--force] [--jobs N]
 
-Translation units are compiled in parallel; the shared library lands next to
-this file, where the ctypes binding loads it from.
+Translation units are compiled in parallel; the shared libraries land next to
+this file, where the package loads them from.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbsfa.so")
+BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+BINDING_STAMP = os.path.join(OBJDIR, "binding.torch")  # the torch that it was built with
 
 SOURCES = ["bsfa_api.cu", "inst_fwd_d128.cu", "inst_fwd_d64.cu", "inst_fwd_vall.cu",
            "inst_calib.cu", "inst_fwd_paged_d128.cu", "inst_fwd_paged_d64.cu", "inst_fwd_corr.cu",
@@ -60,11 +66,54 @@ def _compile(src: str, verbose_ptxas: bool) -> tuple[str, str]:
     return obj, r.stdout + r.stderr
 
 
+def _torch_place() -> tuple[str, str]:
+    """Where torch lies and its version, without importing it."""
+    spec = importlib.util.find_spec("torch")
+    root = os.path.dirname(spec.origin)
+    with open(os.path.join(root, "version.py")) as f:
+        return root, re.search(r"__version__ = '([^']*)'", f.read()).group(1)
+
+
+def _build_binding(root: str, version: str) -> None:
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = BINDING + ".tmp"
+    inc = [INCLUDE, os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], cuda]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           *[x for i in inc for x in ("-isystem", i)], os.path.join(CSRC, "binding.cpp"),
+           "-o", tmp, "-L", PKG, "-l:libbsfa.so", "-L", os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(version)
+
+
+def _binding_is_current(version: str) -> bool:
+    if not os.path.exists(BINDING) or os.path.getmtime(BINDING) < _deps_mtime() or \
+            not os.path.exists(BINDING_STAMP):
+        return False
+    with open(BINDING_STAMP) as f:
+        return f.read() == version
+
+
 def build(force: bool = False, jobs: int | None = None, verbose_ptxas: bool = False) -> str:
-    """Compile every translation unit and link libbsfa.so; returns its path."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
-        return LIB
+    """Compile every translation unit, link libbsfa.so and build the torch
+    binding; returns the library's path."""
     os.makedirs(OBJDIR, exist_ok=True)
+    if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < _deps_mtime():
+        _build_library(jobs, verbose_ptxas)
+    root, version = _torch_place()
+    if force or not _binding_is_current(version):
+        _build_binding(root, version)
+    return LIB
+
+
+def _build_library(jobs: int | None, verbose_ptxas: bool) -> None:
     jobs = jobs or min(len(SOURCES), os.cpu_count() or 1)
     with cf.ThreadPoolExecutor(jobs) as ex:
         results = list(ex.map(lambda s: _compile(s, verbose_ptxas), SOURCES))
@@ -77,7 +126,6 @@ def build(force: bool = False, jobs: int | None = None, verbose_ptxas: bool = Fa
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

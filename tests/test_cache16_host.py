@@ -89,14 +89,12 @@ int main(void) {
         subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), c, "-o", exe], check=True)
         got = tuple(map(int, subprocess.run([exe], capture_output=True, text=True,
                                             check=True).stdout.split()))
-    from block_sparse_gated_gb300 import cache16
     n = _native()
     C, P, R = n.Cache16, n.Rope, n.Rows16
-    assert (n.CACHE16.size, n.ROPE.size, n.ROWS16.size) == tuple(map(ctypes.sizeof, (C, P, R)))
     assert got == (ctypes.sizeof(C), C.num_pages.offset, C.block_table.offset, C.dtype.offset,
                    ctypes.sizeof(P), P.position_stride.offset, P.num_axes.offset, P.axis.offset,
                    ctypes.sizeof(R), R.k_out_stride.offset, R.cu_seqlens.offset, R.dtype.offset,
-                   cache16.MAX_AXES)
+                   4)
 
 
 def _write(lib, c, rope, r):
@@ -257,148 +255,193 @@ def test_kernels_do_not_spill(lib, source):
         assert "are spilled" not in f.read()
 
 
-def test_binding_refuses_host_tensors():
+@pytest.fixture(scope="module")
+def b(lib):
+    import block_sparse_gated_gb300 as b
+    return b
+
+
+# The binding looks at shapes, types and strides first and at the device last: a call on host
+# tensors that is right in all else is refused for that, and nothing is launched.
+HOST = "CUDA"
+
+
+def _args():
+    """A right call's tensors, on the host."""
     b = _bsfa()
-    cache = b.cache16_empty(2, 2, 16, 64, device="cpu")
-    x = torch.zeros(1, 2, 16, 64, dtype=BF)
-    table = torch.zeros(1, 2, dtype=torch.int32)
-    rope = b.Rope(cu.inv_freq(32))
-    with pytest.raises(ValueError, match="CUDA"):
-        b.cache16_write(cache, x, x, table)
-    with pytest.raises(ValueError, match="CUDA"):
-        b.rotary(rope, x, x)
-    with pytest.raises(ValueError, match="CUDA"):
-        b.decode16(x, cache, table, torch.zeros(1, dtype=torch.int32))
+    z = torch.zeros
+    return dict(cache=b.cache16_empty(4, 2, 32, 128, device="cpu"), rope=b.Rope(cu.inv_freq(64)),
+                table=z(3, 2, dtype=torch.int32), q=z(3, 8, 10, 128, dtype=BF),
+                k=z(3, 2, 10, 128, dtype=BF), q1=z(3, 8, 1, 128, dtype=BF),
+                lens=z(3, dtype=torch.int32))
 
 
-class Cuda:  # stands for the host tensors' device
-    type, index = "cuda", -1  # get_device() of a host tensor
-
-
-def test_binding_checks_what_the_library_cannot_see(monkeypatch):
-    """Shapes, types and extents, on host tensors with the residency check
-    taken out (no call reaches the library)."""
-    from block_sparse_gated_gb300 import cache16 as m
-    b, n, dev = _bsfa(), _native(), Cuda()
-    monkeypatch.setattr(m, "_on_device", lambda *a, **k: None)
-    cache = b.cache16_empty(4, 2, 32, 128, device="cpu")
-    table = torch.zeros(3, 2, dtype=torch.int32)
-
-    packed, *rest = m._cache_fields(cache, table, dev, 3)
-    c = n.Cache16.from_buffer_copy(packed)
-    assert rest == [2, 128, 0, 64]
-    assert (c.num_pages, c.num_heads_kv, c.page_size, c.head_dim, c.dtype) == (4, 2, 32, 128, 0)
-    assert (c.k, c.v, c.block_table) == (cache.k.data_ptr(), cache.v.data_ptr(), table.data_ptr())
-    assert tuple(c.k_stride) == (2 * 32 * 128, 32 * 128, 128)
-    other = b.cache16_empty(4, 2, 32, 128, layout="pthd", dtype=HF, device="cpu")
-    c = n.Cache16.from_buffer_copy(m._cache_fields(other, table, dev, 3)[0])
-    assert (tuple(c.v_stride), c.page_size, c.dtype) == ((32 * 2 * 128, 128, 2 * 128), 32, 1)
-    wide = torch.zeros(3, 9, dtype=torch.int32)[:, :2]
-    c = n.Cache16.from_buffer_copy(m._cache_fields(cache, wide, dev, 3)[0])
-    assert (c.block_table_stride, c.block_table_width) == (9, 2)
-    for bad in (cache._replace(v=cache.v[:2]), cache._replace(k=cache.k[0]),
-                cache._replace(layout="thpd"),
-                cache._replace(k=cache.k.transpose(2, 3).contiguous().transpose(2, 3))):
-        with pytest.raises(ValueError):
-            m._cache_fields(bad, table, dev, 3)
-    for bad in (cache._replace(k=cache.k.half()), cache._replace(v=cache.v.float())):
-        with pytest.raises(TypeError):
-            m._cache_fields(bad, table, dev, 3)
-    for bad in (table.long(), table[0], torch.zeros(2, 3, dtype=torch.int32).t()):
-        with pytest.raises(ValueError, match="block_table"):
-            m._cache_fields(cache, bad, dev, 3)
-    with pytest.raises(ValueError, match="fewer rows"):
-        m._cache_fields(cache, table, dev, 4)
-
-    q, k = torch.zeros(3, 8, 10, 128, dtype=BF), torch.zeros(3, 2, 10, 128, dtype=BF)
-    packed, *rest = m._rows_fields(q, k, k, q, None, None, None, None, dev)
-    r = n.Rows16.from_buffer_copy(packed)
-    assert rest == [3, 10, 2, 128, 0, False]
-    assert (r.batch, r.num_heads_q, r.num_heads_kv, r.seqlen, r.head_dim) == (3, 8, 2, 10, 128)
-    assert (r.q, r.k, r.v, r.q_out, r.k_out) == (q.data_ptr(), k.data_ptr(), k.data_ptr(),
-                                                 q.data_ptr(), None)
-    assert tuple(r.q_out_stride) == (8 * 10 * 128, 10 * 128, 128)
-    assert tuple(r.k_out_stride) == (0, 0, 0)
-    at, off = torch.zeros(3, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)
-    t = torch.zeros(10, 8, 128, dtype=HF)
-    packed, *rest = m._rows_fields(t, t[:, :2], None, t, t[:, :2], "thd", off, at, dev)
-    r = n.Rows16.from_buffer_copy(packed)
-    assert rest == [3, 10, 2, 128, 1, True]
-    assert (tuple(r.k_stride), r.start, r.cu_seqlens) == ((0, 128, 8 * 128), at.data_ptr(),
-                                                         off.data_ptr())
-    for args in ((q, k[:, :, :9], None, q, None), (q, k[:2], None, q, None),
-                 (q, k[..., :64], None, q, None), (q, k, k[:, :1], q, None),
-                 (q, k, None, q[:, :4], None), (q, k[0], None, q, None)):
-        with pytest.raises(ValueError):
-            m._rows_fields(*args, None, None, None, dev)
-    for args in ((q, k.half(), None, q, None), (q.float(), None, None, q.float(), None)):
-        with pytest.raises(TypeError):
-            m._rows_fields(*args, None, None, None, dev)
-    with pytest.raises(ValueError, match="start"):
-        m._rows_fields(q, k, k, q, None, None, None, at[:2], dev)
-    with pytest.raises(ValueError, match="cu_seqlens"):
-        m._rows_fields(t, None, None, t, None, "thd", off.long(), None, dev)
-    with pytest.raises(ValueError, match="layout|bhdl"):
-        m._rows_fields(q, k, k, q, None, "bhdl", None, None, dev)
-
-    f = cu.inv_freq(64)
+def test_right_calls_reach_the_device_check(b):
+    x = _args()
+    cache, rope, table, q, k, lens = (x[n] for n in ("cache", "rope", "table", "q", "k", "lens"))
+    t = torch.zeros(10, 12, 128, dtype=BF)  # queries, keys and values of packed tokens
+    off, p = torch.zeros(4, dtype=torch.int32), torch.zeros(3, 3, 10, dtype=torch.int32)
     axes = (0,) * 20 + (1,) * 20 + (2,) * 24
+    q0 = q[:, :, :0]
+    for call in (
+            lambda: b.rotary(rope, q), lambda: b.rotary(rope, q, k, start=lens),
+            lambda: b.rotary(rope, q[0], k[0]), lambda: b.rotary(rope, q, k, out=(q, k)),
+            lambda: b.rotary(rope, q, out=(q, None), inverse=True),
+            lambda: b.rotary(rope, t[:, :8], t[:, 8:10], layout="thd", cu_seqlens=off, start=lens),
+            lambda: b.rotary(rope, t[:8], t[8:10], cu_seqlens=off),
+            lambda: b.rotary(rope._replace(axes=axes), q, positions=p),
+            lambda: b.rotary(rope._replace(axes=list(axes)), q, positions=p[:, :1].expand(3, 3, 10)),
+            lambda: b.rotary(rope, q, positions=p[0]), lambda: b.rotary(rope, q, positions=p),
+            lambda: b.rotary(rope, q0, positions=p[0, :, :0]),
+            lambda: b.rotary(rope._replace(axes=axes), t[:, :8], layout="thd", cu_seqlens=off,
+                             positions=p[:, 0]),
+            lambda: b.cache16_write(cache, k, k, table),
+            lambda: b.cache16_write(cache, k, k, table, rope=rope, q=q, q_out=q, start=lens),
+            lambda: b.cache16_write(cache, k.transpose(1, 2), k.transpose(1, 2), table,
+                                    layout="blhd", rope=rope),
+            lambda: b.decode16(x["q1"], cache, table, lens, return_lse=True),
+            lambda: b.decode16(q, cache, table, lens, max_seqlen=64, softmax_scale=0.5,
+                               causal=False, out=q),
+            lambda: b.decode16(q[0], cache, table, lens[:1])):
+        with pytest.raises(ValueError, match=HOST):
+            call()
+    cache = b.cache16_empty(4, 2, 32, 128, layout="pthd", dtype=HF, device="cpu")
+    with pytest.raises(ValueError, match=HOST):
+        b.cache16_write(cache, k.half(), k.half(), table, rope=rope, q=q.half())
+    # the workspace's size is a matter of shapes alone
+    assert b.decode16_workspace_bytes(x["q1"], x["cache"], table, lens) == 0
+    wide = torch.zeros(3, 4000, dtype=torch.int32)
+    assert b.decode16_workspace_bytes(x["q1"], x["cache"], wide, lens) > 0
+    assert b.decode16_workspace_bytes(x["q1"], x["cache"], wide, lens, max_seqlen=64) == 0
 
-    def rope(r, positions=None, varlen=False, batch=3, rows=10, inverse=False):
-        return n.Rope.from_buffer_copy(m._rope_fields(r, positions, inverse, varlen, batch, rows,
-                                                      dev))
 
-    x = rope(b.Rope(f))
-    assert (x.inv_freq, x.positions, x.pairs, x.num_axes) == (f.data_ptr(), None, 64, 1)
-    assert (x.interleaved, x.inverse, bytes(x.axis)) == (0, 0, bytes(64))
-    p = torch.zeros(3, 3, 10, dtype=torch.int32)
-    x = rope(b.Rope(f, axes, True), p, inverse=True)
-    assert (x.num_axes, x.interleaved, x.inverse, x.positions) == (3, 1, 1, p.data_ptr())
-    assert tuple(x.position_stride) == (30, 10) and bytes(x.axis) == bytes(axes)
-    x = rope(b.Rope(f), p[0])
-    assert tuple(x.position_stride) == (0, 10)
-    x = rope(b.Rope(f, axes), p[:, :1].expand(3, 3, 10))  # one sequence's positions for all
-    assert tuple(x.position_stride) == (30, 0)
-    x = rope(b.Rope(f, axes), p[:, 0], varlen=True)
-    assert tuple(x.position_stride) == (30, 0)
-    for r, kw in ((b.Rope(f[::2]), {}), (b.Rope(f.double()), {}), (b.Rope(f[:0]), {}),
-                  (b.Rope(torch.zeros(65)), {}), (b.Rope(f, axes[:63]), {}),
-                  (b.Rope(f, (4,) * 64), {}), (b.Rope(f, (-1,) * 64), {}),
-                  (b.Rope(f, axes), dict(positions=p[:2])), (b.Rope(f, axes), dict(positions=p[0])),
-                  (b.Rope(f), dict(positions=p[0].long())), (b.Rope(f), dict(positions=p[0, :2])),
-                  (b.Rope(f), dict(positions=torch.zeros(10, 3, dtype=torch.int32).t())),
-                  (b.Rope(f), dict(positions=torch.zeros(5, 3, 10, dtype=torch.int32)))):
-        with pytest.raises(ValueError):
-            rope(r, **kw)
-    q1, lens = torch.zeros(3, 8, 1, 128, dtype=BF), torch.zeros(3, dtype=torch.int32)
+def test_caches_that_the_binding_refuses(b):
+    x = _args()
+    cache, table, k, q1, lens = (x[n] for n in ("cache", "table", "k", "q1", "lens"))
 
-    def decode(*a, **kw):
-        kw = dict(dict(layout=None, max_seqlen=None, softmax_scale=None, causal=True), **kw)
-        _, fields, code = m._decode_fields(*a, dev, **kw)
-        return n.Decode4Params.from_buffer_copy(n.DECODE4.pack(*fields, 4096, 77, code))
+    def both(cache, table, kind, what):
+        with pytest.raises(kind, match=what):
+            b.cache16_write(cache, k, k, table)
+        with pytest.raises(kind, match=what):
+            b.decode16(q1, cache, table, lens)
 
-    d = decode(q1, cache, table, lens, q1, lse=512, softmax_scale=0.5)
-    assert (d.batch, d.num_heads_q, d.q_len, d.max_seqlen, d.dtype, d.causal) == (3, 8, 1, 64, 0, 1)
-    assert (d.q, d.o, d.seqlens, d.lse) == (q1.data_ptr(), q1.data_ptr(), lens.data_ptr(), 512)
-    assert (d.workspace, d.workspace_bytes, d.softmax_scale) == (4096, 77, 0.5)
-    for bad, what in (((q1[:, :7], cache, table, lens, q1[:, :7]), "heads"),
-                      ((q1, cache, table, lens, q1.half()), "shape and type"),
-                      ((q1.half(), cache, table, lens, q1.half()), "type"),
-                      ((q1, cache, table, lens.long(), q1), "seqlens")):
-        with pytest.raises(ValueError, match=what):
-            decode(*bad)
-    with pytest.raises(ValueError, match="pages"):
-        decode(q1, cache, table, lens, q1, max_seqlen=65)
+    turned = cache.k.transpose(2, 3).contiguous().transpose(2, 3)
+    for bad in (cache._replace(v=cache.v[:2]), cache._replace(k=turned), cache._replace(v=turned)):
+        both(bad, table, ValueError, "one shape, with the head dimension contiguous")
+    both(cache._replace(k=cache.k[0]), table, ValueError, "4-D")
+    both(cache._replace(layout="thpd"), table, ValueError, "thpd")
+    both(cache._replace(layout="bhld"), table, ValueError, "pthd")
+    for bad in (cache._replace(k=cache.k.half()), cache._replace(v=cache.v.float())):
+        both(bad, table, TypeError, "one type")
+    both(b.KVCache16(cache.k.float(), cache.v.float()), table, TypeError, "float16")
+    both(cache._replace(k=None), table, TypeError, "cache.k must be a tensor")
+    for bad in (table.long(), table[0], torch.zeros(2, 3, dtype=torch.int32).t()):
+        both(cache, bad, ValueError, "block_table must be")
+    both(cache, table[:2], ValueError, "fewer rows")
+    both(cache, 3, TypeError, "block_table must be a tensor")
+
+
+def test_rows_that_the_binding_refuses(b):
+    x = _args()
+    cache, rope, table, q, k, lens = (x[n] for n in ("cache", "rope", "table", "q", "k", "lens"))
+    t, off = torch.zeros(10, 8, 128, dtype=HF), torch.zeros(4, dtype=torch.int32)
+    shapes = "disagree|one shape|contiguous"
+    for args in ((q, k[:, :, :9]), (q, k[:2]), (q, k[..., :64]), (q, k[0]),
+                 (q, k.transpose(2, 3).contiguous().transpose(2, 3))):
+        with pytest.raises(ValueError, match=shapes):
+            b.rotary(rope, *args)
+        with pytest.raises(ValueError, match=shapes):
+            b.cache16_write(cache, args[1], args[1], table, rope=rope, q=q)
+    for out in ((q[:, :4], k), (q, k[:, :, :3]), (q[:2], k)):
+        with pytest.raises(ValueError, match=shapes):
+            b.rotary(rope, q, k, out=out)
+    with pytest.raises(ValueError, match=shapes):
+        b.cache16_write(cache, k, k[:, :1], table)
+    with pytest.raises(ValueError, match=shapes):
+        b.cache16_write(cache, k, k, table, rope=rope, q=q, q_out=q[:, :4])
+    for args in ((q, k.half()), (q.float(), None), (q, k.float())):
+        with pytest.raises(TypeError):
+            b.rotary(rope, *args)
+    with pytest.raises(TypeError, match="element type"):
+        b.rotary(rope, q, out=(q.half(), None))
+    with pytest.raises(TypeError, match="element type"):
+        b.cache16_write(cache, k, k.half(), table)
+    with pytest.raises(TypeError, match="q must be a tensor"):
+        b.rotary(rope, None)
+    for bad in (lens[:2], lens.long(), lens[None], torch.zeros(6, dtype=torch.int32)[::2]):
+        with pytest.raises(ValueError, match="start"):
+            b.rotary(rope, q, start=bad)
+    for bad in (off.long(), off[None], off[:0]):
+        with pytest.raises(ValueError, match="cu_seqlens"):
+            b.rotary(rope, t, layout="thd", cu_seqlens=bad)
+    for layout, kw in (("bhdl", {}), ("thd", {}), ("phtd", {}), ("bhld", dict(cu_seqlens=off))):
+        y = t if kw else q
+        with pytest.raises(ValueError, match="bhdl|batched rows|packed rows"):
+            b.rotary(rope, y, layout=layout, **kw)
+    with pytest.raises(ValueError, match="3-D"):
+        b.rotary(rope, q, cu_seqlens=off)
+    with pytest.raises(ValueError, match="4-D"):
+        b.rotary(rope, q[0, 0])
+    with pytest.raises(ValueError, match="pair"):
+        b.rotary(rope, q, out=(q, k))
+    with pytest.raises(ValueError, match="pair"):
+        b.rotary(rope, q, k, out=(q, None))
+    with pytest.raises(ValueError, match="two tensors"):
+        b.rotary(rope, k, k, out=(k, k))
     with pytest.raises(ValueError, match="rope"):
         b.cache16_write(cache, k, k, table, q=q)
     with pytest.raises(ValueError, match="rope"):
-        b.cache16_write(cache, k, k, table, positions=p[0])
+        b.cache16_write(cache, k, k, table, positions=torch.zeros(3, 10, dtype=torch.int32))
     with pytest.raises(ValueError, match="q_out"):
-        b.cache16_write(cache, k, k, table, rope=b.Rope(f), q_out=q)
-    with pytest.raises(ValueError, match="pair"):
-        b.rotary(b.Rope(f), q, out=(q, k))
-    with pytest.raises(ValueError, match="cache's"):
-        m.cache16_write(cache, q, q, table, rope=b.Rope(f))
+        b.cache16_write(cache, k, k, table, rope=rope, q_out=q)
+    for bad in (q, k[..., :64], k.half()):
+        with pytest.raises(ValueError, match="cache's"):
+            b.cache16_write(cache, bad, bad, table)
+
+
+def test_ropes_that_the_binding_refuses(b):
+    x = _args()
+    f, q = x["rope"].inv_freq, x["q"]
+    axes = (0,) * 20 + (1,) * 20 + (2,) * 24
+    p = torch.zeros(3, 3, 10, dtype=torch.int32)
+    for bad in (f[::2], f.double(), f[:0], torch.zeros(65), f[None]):
+        with pytest.raises(ValueError, match="inv_freq"):
+            b.rotary(b.Rope(bad), q)
+    for bad in (axes[:63], (4,) * 64, (-1,) * 64, (1 << 40,) * 64):
+        with pytest.raises(ValueError, match="axes"):
+            b.rotary(b.Rope(f, bad), q)
+    for bad in (3, (0.5,) * 64):
+        with pytest.raises(TypeError):
+            b.rotary(b.Rope(f, bad), q)
+    for rope, bad in ((b.Rope(f, axes), p[:2]), (b.Rope(f, axes), p[0]), (b.Rope(f), p[0].long()),
+                      (b.Rope(f), p[0, :2]), (b.Rope(f), p[0, 0]), (b.Rope(f), p[:, :, :9]),
+                      (b.Rope(f), torch.zeros(10, 3, dtype=torch.int32).t()),
+                      (b.Rope(f), torch.zeros(5, 3, 10, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="positions"):
+            b.rotary(rope, q, positions=bad)
+    with pytest.raises(ValueError, match="positions"):
+        b.rotary(b.Rope(f), q[0], cu_seqlens=torch.zeros(2, dtype=torch.int32), positions=p)
+
+
+def test_decode_calls_that_the_binding_refuses(b):
+    x = _args()
+    cache, table, q1, lens = (x[n] for n in ("cache", "table", "q1", "lens"))
+    for bad, what in (((q1[:, :7], lens), "heads"), ((q1.half(), lens), "type"),
+                      ((q1[..., :64], lens), "head dimension"), ((q1, lens.long()), "seqlens"),
+                      ((q1, lens[:2]), "seqlens"), ((q1[0, 0], lens), "4-D")):
+        with pytest.raises(ValueError, match=what):
+            b.decode16(bad[0], cache, table, bad[1])
+    for bad in (q1.half(), q1[:2], x["q"]):
+        with pytest.raises(ValueError, match="shape and type"):
+            b.decode16(q1, cache, table, lens, out=bad)
+    with pytest.raises(ValueError, match="pages"):
+        b.decode16(q1, cache, table, lens, max_seqlen=65)
+    with pytest.raises(TypeError):
+        b.decode16(q1, cache, table, lens, max_seqlen="64")
+    with pytest.raises(ValueError, match="contiguous"):
+        b.decode16(q1, cache, table, lens, workspace=torch.zeros(8, 8)[:, 1])
+    with pytest.raises(ValueError, match="batched rows"):
+        b.decode16(q1, cache, table, lens, layout="thd")
 
 
 def test_cache_allocation_checks():
