@@ -31,7 +31,8 @@ SOURCES = ["bsfa_api.cu", "inst_fwd_d128.cu", "inst_fwd_d64.cu", "inst_fwd_vall.
            "inst_calib.cu", "inst_fwd_paged_d128.cu", "inst_fwd_paged_d64.cu", "inst_fwd_corr.cu",
            "bsfa_noalloc.cu", "inst_xs.cu", "inst_xs224.cu", "bsfa_cache4.cu", "bsfa_decode4.cu",
            "bsfa_cache16.cu", "bsfa_decode16.cu", "inst_decode16_d64_bf16.cu",
-           "inst_decode16_d64_f16.cu", "inst_decode16_d128_bf16.cu", "inst_decode16_d128_f16.cu"]
+           "inst_decode16_d64_f16.cu", "inst_decode16_d128_bf16.cu", "inst_decode16_d128_f16.cu",
+           "inst_decode16_wide_d64.cu", "inst_decode16_wide_d128.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]

@@ -218,9 +218,8 @@ static EncodeTiled get_encoder() {
 
 // 4-D map of 16-bit elements (bf16 or fp16) {d, tokens, heads, batch}, box {64, box_rows,
 // 1, 1} (128 rows, or 224 for the keys and values of the 128 x 224 tile), 128-byte swizzle.
-static bool make_map(CUtensorMap* m, const void* ptr, bool f16, int d, long long tokens, int heads,
-                     int batch, long long st_tok, long long st_head, long long st_batch,
-                     int box_rows = TILE) {
+bool make_map(CUtensorMap* m, const void* ptr, bool f16, int d, long long tokens, int heads,
+              int batch, long long st_tok, long long st_head, long long st_batch, int box_rows) {
   EncodeTiled enc = get_encoder();
   if (enc == nullptr) return false;
   cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)tokens, (cuuint64_t)heads, (cuuint64_t)batch};
@@ -245,6 +244,8 @@ static unsigned* error_word() {
   if (cudaGetSymbolAddress(&ptr, g_device_error) != cudaSuccess) return nullptr;
   return static_cast<unsigned*>(ptr);
 }
+
+unsigned* device_error_word() { return error_word(); }
 
 template <bool CALIB, bool F16, bool G, bool VA, bool PG, bool CR>
 static cudaError_t dispatch_dn(int d, int nq, const Maps& m, const DevParams& p, int grid,

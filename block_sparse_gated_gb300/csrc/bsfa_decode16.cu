@@ -8,7 +8,8 @@
 #include "bsfa.h"
 #include "bsfa_cache16.h"
 #include "bsfa_cache4.h"
-#include "bsfa_decode16.cuh"
+#include "bsfa_decode16_wide.cuh"
+#include "bsfa_launch.h"
 
 namespace bsfa {
 
@@ -17,6 +18,14 @@ extern template bsfa_status run<64, false>(const DecArgs&, const Plan&, int, int
 extern template bsfa_status run<64, true>(const DecArgs&, const Plan&, int, int, cudaStream_t);
 extern template bsfa_status run<128, false>(const DecArgs&, const Plan&, int, int, cudaStream_t);
 extern template bsfa_status run<128, true>(const DecArgs&, const Plan&, int, int, cudaStream_t);
+#define BSFA_WIDE(D, F16)                                                                  \
+  extern template bsfa_status run_wide<D, F16>(const CUtensorMap&, const CUtensorMap&,      \
+                                               const DecArgs&, const Plan&, int, int, cudaStream_t);
+BSFA_WIDE(64, false)
+BSFA_WIDE(64, true)
+BSFA_WIDE(128, false)
+BSFA_WIDE(128, true)
+#undef BSFA_WIDE
 }  // namespace decode16
 
 namespace {
@@ -29,6 +38,19 @@ Plan plan_of(const bsfa_cache16* c, const bsfa_decode4_params* p) {
   Plan pl;
   const long long rows = static_cast<long long>(p->num_heads_q / c->num_heads_kv) * p->q_len;
   const long long eights = rows > 0 ? (rows + 7) / 8 : 1;
+  pl.row_tiles = static_cast<int>((rows + 127) / 128);
+  pl.segments = static_cast<long long>(p->batch) * c->num_heads_kv * pl.row_tiles;
+  pl.wide = rows > WIDE_ROWS && p->max_seqlen >= WIDE_LEAST && pl.segments <= WIDE_SEGMENTS;
+  if (pl.wide) {
+    pl.nt = 16;
+    pl.units = (p->max_seqlen + WIDE_UNIT - 1) / WIDE_UNIT;
+    pl.all_units = pl.segments * (pl.units + WIDE_SEGMENT_UNITS);
+    pl.max_grid = MAX_SMS;
+    pl.warps = WARPS;
+    pl.cluster = 1;
+    pl.split = true;
+    return pl;
+  }
   pl.row_tiles = static_cast<int>((eights + 3) / 4);
   pl.nt = static_cast<int>((eights + pl.row_tiles - 1) / pl.row_tiles);
   pl.units = (p->max_seqlen + UNIT - 1) / UNIT;
@@ -63,6 +85,16 @@ Plan plan_of(const bsfa_cache16* c, const bsfa_decode4_params* p) {
   return pl;
 }
 
+// The tensor map of a pool: copies of `box` tokens of one head and page.
+bool map_pool(CUtensorMap* m, const bsfa_cache16* c, const void* pool, const int64_t (&stride)[3],
+              int box) {
+  // The stride of a dimension of one element may be anything, but not in a map.
+  const long long head = c->num_heads_kv > 1 ? stride[1] : c->head_dim;
+  const long long page = c->num_pages > 1 ? stride[0] : c->head_dim;
+  return make_map(m, pool, c->dtype == BSFA_DTYPE_F16, c->head_dim, c->page_size, c->num_heads_kv,
+                  c->num_pages, stride[2], head, page, box);
+}
+
 struct Carve {
   size_t part_o, part_ml, joins, bytes;
 };
@@ -70,11 +102,12 @@ struct Carve {
 Carve carve(const Plan& pl, int d) {
   Carve c{};
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t grid = pl.split ? static_cast<size_t>(pl.max_grid) : 0, rows = 8 * pl.nt;
+  const size_t grid = pl.split ? static_cast<size_t>(pl.max_grid) : 0;
+  const size_t rows = 2 * grid * 8 * pl.nt * (pl.wide ? WIDE_PARTS : 1);
   c.part_o = 0;
-  c.part_ml = up(c.part_o + grid * 2 * rows * d * sizeof(float));
-  c.joins = up(c.part_ml + grid * 2 * rows * sizeof(float2));
-  c.bytes = up(c.joins + grid * sizeof(int4));
+  c.part_ml = up(c.part_o + rows * d * sizeof(float));
+  c.joins = up(c.part_ml + rows * sizeof(float2));
+  c.bytes = up(c.joins + (pl.wide ? pl.segments : grid) * sizeof(int4));
   return c;
 }
 
@@ -173,9 +206,23 @@ bsfa_status bsfa_decode16(const bsfa_cache16* cache, const bsfa_decode4_params* 
   if (v != BSFA_OK) return v;
   v = status_of(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   if (v != BSFA_OK || sms <= 0) return BSFA_ERR_CUDA;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (pl.wide) {
+    // A copy lies within a page: the largest power of two that divides one.
+    a.box = cache->page_size & -cache->page_size;
+    if (a.box > WIDE_UNIT) a.box = WIDE_UNIT;
+    a.err = device_error_word();
+    CUtensorMap k, v;
+    if (a.err == nullptr || !map_pool(&k, cache, cache->k, cache->k_stride, a.box) ||
+        !map_pool(&v, cache, cache->v, cache->v_stride, a.box))
+      return BSFA_ERR_CUDA;
+    const auto call = cache->head_dim == 128 ? (a.f16 ? run_wide<128, true> : run_wide<128, false>)
+                                             : (a.f16 ? run_wide<64, true> : run_wide<64, false>);
+    return call(k, v, a, pl, sms, dev, stream);
+  }
   const auto run_call = cache->head_dim == 128 ? (a.f16 ? run<128, true> : run<128, false>)
                                                : (a.f16 ? run<64, true> : run<64, false>);
-  return run_call(a, pl, sms, dev, reinterpret_cast<cudaStream_t>(stream_));
+  return run_call(a, pl, sms, dev, stream);
 }
 
 }  // extern "C"

@@ -48,6 +48,9 @@ constexpr float SHIFT = 10.f;       // log2 of the factor that a weight carries
 constexpr float NO_SCORE = 3e38f;   // a row's offset before its first score
 constexpr int MIN_UNITS = 4;        // shortest piece of the line worth a CTA
 constexpr int SEGMENT_UNITS = 3;    // a segment's fixed cost, in units
+constexpr int WIDE_ROWS = 32;       // query rows of a KV head beyond which a call may be wide
+constexpr int WIDE_LEAST = 512;     // ... from that bound on the lengths
+constexpr int WIDE_SEGMENTS = 1 << 16;  // ... and up to so many segments
 constexpr int JOIN_THREADS = 256;   // of the kernel that joins parts
 constexpr int JOIN_ROWS_PARTS = 8;  // a warp to a row below, a block above
 constexpr int MAX_PARTS = 768;      // parts of a segment, at most: CTAs of a cut call
@@ -118,6 +121,8 @@ struct DecArgs {
   long long lse_pitch;
   float* part_o;    // [grid][2][rows of a CTA][d]
   float2* part_ml;  // [grid][2][rows of a CTA]
+  unsigned* err;    // the device error word (wide calls)
+  int box;          // tokens of a copy (wide calls)
   int4* joins;      // [jobs]: {sequence, kvh * row_tiles + row tile, first, last CTA}, or x < 0
 };
 
@@ -127,7 +132,10 @@ __device__ __forceinline__ int clamp_len(const DecArgs& a, int b) {
 }
 // Units of a segment on the line: its tokens', and what a CTA spends on any segment
 // (queries, the first copies' latency, the join of its warps).
-__device__ __forceinline__ int units_of(int len) { return SEGMENT_UNITS + (len + UNIT - 1) / UNIT; }
+template <int U = UNIT, int FIXED = SEGMENT_UNITS>
+__device__ __forceinline__ int units_of(int len) {
+  return FIXED + (len + U - 1) / U;
+}
 
 // Where a CTA's piece of the line begins.
 struct Piece {
@@ -138,13 +146,15 @@ struct Piece {
 
 // Cuts the line.  Every CTA adds up the lengths by itself: a few loads per
 // thread, no extra launch.
+template <int U, int FIXED, int WARPS>
 __device__ __forceinline__ Piece cut(const DecArgs& a, int* sh) {
+  constexpr int THREADS = 32 * WARPS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int chunk = (a.batch + THREADS - 1) / THREADS;
   const int b0 = min(a.batch, tid * chunk), b1 = min(a.batch, b0 + chunk);
   const int per_unit = a.heads_kv * a.row_tiles;
   int sum = 0;
-  for (int b = b0; b < b1; ++b) sum += units_of(clamp_len(a, b));
+  for (int b = b0; b < b1; ++b) sum += units_of<U, FIXED>(clamp_len(a, b));
   int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -169,7 +179,7 @@ __device__ __forceinline__ Piece cut(const DecArgs& a, int* sh) {
   if (at >= before && at < before + sum) {
     int base = before;
     for (int b = b0; b < b1; ++b) {
-      const int n = units_of(clamp_len(a, b));
+      const int n = units_of<U, FIXED>(clamp_len(a, b));
       if (at < base + n) {
         sh[WARPS] = b;
         sh[WARPS + 1] = base * per_unit;
@@ -279,11 +289,11 @@ __global__ void __launch_bounds__(32 * W, Shape<D, NT>::CTAS * decode16::WARPS /
     // Lets the join's blocks take their places, where they wait for this kernel's end.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0 && !a.join_by_segment) a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    piece = cut(a, sh_cut);
+    piece = cut<UNIT, SEGMENT_UNITS, WARPS>(a, sh_cut);
   } else {  // one segment per cluster; u walks over it once
     const int seg = static_cast<int>(blockIdx.x) / a.cluster, per_b = a.heads_kv * a.row_tiles;
     piece.b = seg / per_b;
-    const int n = units_of(clamp_len(a, piece.b));
+    const int n = units_of<>(clamp_len(a, piece.b));
     piece.base = 0;
     piece.begin = (seg - piece.b * per_b) * n;
     piece.end = piece.begin + n;
@@ -294,7 +304,7 @@ __global__ void __launch_bounds__(32 * W, Shape<D, NT>::CTAS * decode16::WARPS /
   int u = piece.begin, b = piece.b, base = piece.base;
   while (u < piece.end) {
     const int len = clamp_len(a, b);
-    const int n_units = units_of(len);
+    const int n_units = units_of<>(len);
     const int seg = (u - base) / n_units;  // kvh * row_tiles + row tile
     const int u0 = u - base - seg * n_units;
     const int u1 = min(n_units, u0 + piece.end - u);
@@ -723,12 +733,19 @@ __global__ void __launch_bounds__(32 * W, Shape<D, NT>::CTAS * decode16::WARPS /
   }
 }
 
+// Place of part p of a segment that began in CTA `first`.
+template <int PER>
+__device__ __forceinline__ long long slot_of(int first, int p) {
+  const int c = p / PER;
+  return (2LL * (first + c) + (c == 0 ? 1 : 0)) * PER + (p - c * PER);
+}
+
 // Joins the parts of the segments that a cut crossed: block (x, r) takes row r
 // of job x, which is segment x, or where there are more segments than CTAs the
 // one that CTA x began and did not finish -- if that was cut.  The parts lie in
-// the CTAs first (its second slot) .. last (their first slots).  The offsets come
-// first, all at once, so that the sums' loads wait for nothing.
-template <int D, int ROWS>
+// the CTAs first (its second slot) .. last (their first slots), PER in each.  The
+// offsets come first, all at once, so that the sums' loads wait for nothing.
+template <int D, int ROWS, int PER>
 __global__ void __launch_bounds__(JOIN_THREADS, 4) decode16_join_kernel(const DecArgs a) {
   constexpr int LANES = D / 4;                 // threads that cover a row, four elements each
   constexpr int PARTS = JOIN_THREADS / LANES;  // parts read at once
@@ -741,9 +758,9 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) decode16_join_kernel(const De
   const int b = job.x, kvh = job.y / a.row_tiles;
   const int r = blockIdx.y, row = (job.y - kvh * a.row_tiles) * ROWS + r;
   if (row >= a.rows) return;
-  const int first = job.z, count = job.w - first + 1;  // at most the CTAs, so MAX_PARTS
+  const int first = job.z, count = PER * (job.w - first + 1);  // at most MAX_PARTS
   const int tid = threadIdx.x;
-  auto slot = [&](int p) { return 2LL * (first + p) + (p == 0 ? 1 : 0); };
+  auto slot = [&](int p) { return slot_of<PER>(first, p); };
 
   float2 mine[MAX_PARTS / JOIN_THREADS];
   float m = -NO_SCORE;
@@ -795,7 +812,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) decode16_join_kernel(const De
 
 // The same where segments have few parts: a warp takes a row of job x by itself,
 // 32 parts' offsets at a time.
-template <int D, int ROWS>
+template <int D, int ROWS, int PER>
 __global__ void __launch_bounds__(JOIN_THREADS) decode16_join_rows_kernel(const DecArgs a) {
   constexpr int E = D / 32;  // elements of a lane
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -806,8 +823,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) decode16_join_rows_kernel(const 
   const int b = job.x, kvh = job.y / a.row_tiles;
   const int row = (job.y - kvh * a.row_tiles) * ROWS + r;
   if (r >= ROWS || row >= a.rows) return;
-  const int first = job.z, count = job.w - first + 1;
-  auto slot = [&](int p) { return 2LL * (first + p) + (p == 0 ? 1 : 0); };
+  const int first = job.z, count = PER * (job.w - first + 1);
+  auto slot = [&](int p) { return slot_of<PER>(first, p); };
   float m = -NO_SCORE, l = 0.f, y[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) y[e] = 0.f;
@@ -853,6 +870,7 @@ struct Plan {
   int nt, row_tiles, units, warps, cluster, max_grid;
   long long segments, all_units;
   bool split;
+  bool wide;  // bsfa_decode16_wide.cuh
 };
 
 // The status of a runtime call.  The runtime keeps the error of one that failed
@@ -878,6 +896,26 @@ bsfa_status prepare(int dev) {
                                        cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
   if (v == BSFA_OK) ready.fetch_or(bit, std::memory_order_relaxed);
   return v;
+}
+
+// The join of what `grid` CTAs left of `segments` segments, in `jobs` jobs.
+template <int D, int ROWS, int PER>
+bsfa_status launch_join(const DecArgs& a, long long segments, int grid, long long jobs,
+                        cudaStream_t stream) {
+  // About grid / segments parts to a segment.
+  const bool by_rows = grid * PER < JOIN_ROWS_PARTS * segments;
+  const int rows = a.rows < ROWS ? a.rows : ROWS, per_block = by_rows ? JOIN_THREADS / 32 : 1;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(jobs), (rows + per_block - 1) / per_block);
+  cfg.blockDim = dim3(JOIN_THREADS);
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  return status_of(by_rows ? cudaLaunchKernelEx(&cfg, decode16_join_rows_kernel<D, ROWS, PER>, a)
+                           : cudaLaunchKernelEx(&cfg, decode16_join_kernel<D, ROWS, PER>, a));
 }
 
 template <int D, int NT, bool F16, int W = WARPS>
@@ -910,19 +948,8 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
     cfg.numAttrs = 0;
     const bsfa_status first = status_of(cudaLaunchKernelEx(&cfg, decode16_kernel<D, NT, F16, W>, a));
     if (first != BSFA_OK) return first;
-    // About grid / segments parts to a segment.
-    const bool by_rows = grid < JOIN_ROWS_PARTS * pl.segments;
-    constexpr int ROWS = 8 * NT;
-    const int rows = a.rows < ROWS ? a.rows : ROWS, per_block = by_rows ? JOIN_THREADS / 32 : 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(a.join_by_segment ? pl.segments : grid),
-                       (rows + per_block - 1) / per_block);
-    cfg.blockDim = dim3(JOIN_THREADS);
-    cfg.dynamicSmemBytes = 0;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 1;
-    return status_of(by_rows ? cudaLaunchKernelEx(&cfg, decode16_join_rows_kernel<D, ROWS>, a)
-                             : cudaLaunchKernelEx(&cfg, decode16_join_kernel<D, ROWS>, a));
+    return launch_join<D, 8 * NT, 1>(a, pl.segments, grid,
+                                     a.join_by_segment ? pl.segments : grid, stream);
   }
   return BSFA_ERR_CUDA;
 }

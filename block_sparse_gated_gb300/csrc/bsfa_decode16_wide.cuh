@@ -1,0 +1,619 @@
+// bsfa_decode16_wide.cuh -- attention over the 16-bit cache for calls of many query
+// rows per KV head (several tokens of many heads): up to 128 rows to a CTA on the
+// fifth-generation tensor cores, so that each key and value is read once for all of
+// them.
+//
+// Mathematics and work split are those of bsfa_decode16.cuh; query rows are the rows
+// (M = 128) of S = Q K^T and O = P V here, and a tile is 128 tokens.  A weight goes
+// into the products as two 16-bit numbers, as there.
+//
+// Two softmax warpgroups take the tiles in turn, each with a score buffer, an O and a
+// row offset of its own: neither waits for the other, and their results are two parts
+// of the segment, which the join adds along with those of other CTAs.  Of a segment
+// that lies within one CTA the second warpgroup adds them.
+//
+// Roles (384 threads, one CTA per SM):
+//   warp 0      copies K and V tiles through TMA, one box per lane: a box lies within
+//               a page.
+//   warp 1      issues the products, owns TMEM.
+//   warps 4-7   softmax of the even tiles, a thread to a row.
+//   warps 8-11  ... of the odd ones.
+// TMEM: scores at columns 0 and 128, O at 256 and 384.  The weights of 32 keys take
+// the columns of their scores: 16 for the first numbers, 16 for the second.
+#pragma once
+#include "bsfa_decode16.cuh"
+#include "bsfa_fwd.cuh"
+
+namespace bsfa {
+
+namespace decode16 {
+
+constexpr int WIDE_UNIT = TILE;        // tokens of a work unit
+constexpr int WIDE_SEGMENT_UNITS = 6;  // a segment's fixed cost, in units
+constexpr int WIDE_THREADS = 384;
+constexpr int WIDE_RUN = 64;           // tiles that a warpgroup sums in TMEM, at most
+constexpr int WIDE_STAGES = 3;         // of the key and of the value ring
+constexpr int WIDE_PARTS = 2;          // that a CTA leaves of a segment
+
+struct WideCtrl {
+  uint64_t q_full, q_empty;
+  uint64_t k_full[WIDE_STAGES], k_empty[WIDE_STAGES];
+  uint64_t v_full[WIDE_STAGES], v_empty[WIDE_STAGES];
+  uint64_t s_full[2], p_full[2], pv_done[2];  // of each warpgroup
+  uint64_t x_full, x_empty;  // the first warpgroup's part of a segment: there, read
+  float2 part[TILE];         // ... its offsets and sums
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  int cut[WIDE_THREADS / 32 + 2];
+};
+
+template <int D>
+struct WideLayout {
+  static constexpr int TB = TILE * D * 2;  // bytes of a tile
+  static constexpr int K_OFF = TB, V_OFF = K_OFF + WIDE_STAGES * TB;
+  static constexpr int C_OFF = V_OFF + WIDE_STAGES * TB;
+  static constexpr int RAW = C_OFF + static_cast<int>(sizeof(WideCtrl)) + 1024;
+  // At least 120 KB, so that one CTA is resident per SM (it takes all of TMEM).
+  static constexpr int BYTES = RAW > 120 * 1024 ? RAW : 120 * 1024;
+  static_assert(BYTES <= 227 * 1024, "shared memory");
+};
+
+// One segment's part in a CTA's piece.
+struct WideWork {
+  int b, kvh, seg, r0, n_rows, len, min_lim, max_lim;
+  int t0, n;            // first tile, tiles
+  bool began, whole;    // the segment begins in this CTA, and ends there as well
+  int last_cta;         // ... or in that one
+};
+
+struct WideWalk {
+  const DecArgs& a;
+  Piece p;
+  int u, b, base;
+  __device__ __forceinline__ WideWalk(const DecArgs& a_, const Piece& p_)
+      : a(a_), p(p_), u(p_.begin), b(p_.b), base(p_.base) {}
+  __device__ __forceinline__ bool next(WideWork& w) {
+    if (u >= p.end) return false;
+    const int per_b = a.heads_kv * a.row_tiles;
+    w.b = b;
+    w.len = clamp_len(a, b);
+    const int n_units = units_of<WIDE_UNIT, WIDE_SEGMENT_UNITS>(w.len);
+    w.seg = (u - base) / n_units;
+    const int u0 = u - base - w.seg * n_units, u1 = min(n_units, u0 + p.end - u);
+    w.kvh = w.seg / a.row_tiles;
+    w.r0 = (w.seg - w.kvh * a.row_tiles) * TILE;
+    w.n_rows = min(TILE, a.rows - w.r0);
+    const int first_i = w.r0 / a.group, last_i = (w.r0 + w.n_rows - 1) / a.group;
+    w.min_lim = a.causal ? max(0, w.len - a.q_len + first_i + 1) : w.len;
+    w.max_lim = a.causal ? max(0, w.len - a.q_len + last_i + 1) : w.len;
+    w.t0 = max(0, u0 - WIDE_SEGMENT_UNITS);
+    w.n = max(0, min(max(0, u1 - WIDE_SEGMENT_UNITS), (w.max_lim + TILE - 1) / TILE) - w.t0);
+    w.began = u0 == 0;
+    w.whole = w.began && u1 == n_units;
+    w.last_cta = (u + n_units - 1) / p.per_cta;
+    u += u1 - u0;
+    if (u1 == n_units && w.seg == per_b - 1) {
+      base += n_units * per_b;
+      ++b;
+    }
+    return true;
+  }
+};
+
+// 16 elements of a row, as fp32.
+template <bool F16>
+__device__ __forceinline__ void load16(const void* p, float (&f)[16]) {
+  const uint4* q = reinterpret_cast<const uint4*>(p);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint4 x = __ldg(q + h);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 y = x2_to_f32(w[e], F16);
+      f[8 * h + 2 * e] = y.x, f[8 * h + 2 * e + 1] = y.y;
+    }
+  }
+}
+
+// The elements of one row's O over a warpgroup's tiles that are not finite, which may
+// be due to a value that the row does not see, once more: from global memory in fp32.
+// Sixteen elements take a walk over the tokens of their own.
+template <int D, bool F16>
+__device__ __noinline__ void wide_exact_row(const DecArgs& a, const WideWork& w, int row, int wg,
+                                            float z, float* dst) {
+  const int i = row / a.group, h = w.kvh * a.group + (row - i * a.group);
+  const uint16_t* q = a.q + w.b * a.q_s[0] + h * a.q_s[1] + i * a.q_s[2];
+  const int lim = a.causal ? w.len - a.q_len + i + 1 : w.len;
+  const int page_size = a.tiles_per_page * TOK;
+  const int32_t* table = a.table + static_cast<long long>(w.b) * a.table_stride;
+  for (int d0 = 0; d0 < D; d0 += 16) {
+    bool finite = true;
+    for (int j = 0; j < 16; ++j) finite = finite && fabsf(dst[d0 + j]) < INFINITY;
+    if (finite) continue;
+    float o[16] = {};
+    for (int t = wg; t < w.n; t += 2) {
+      const int begin = (w.t0 + t) * TILE, end = min(begin + TILE, lim);
+      for (int tok = begin; tok < end; ++tok) {
+        const int page = __ldg(table + tok / page_size), at = tok % page_size;
+        const bool ok = page >= 0 && page < a.num_pages;
+        float s = 0.f, v[16] = {};
+        if (ok) {
+          const uint8_t* k = a.k + page * a.k_sp + w.kvh * a.k_sh + at * a.k_st;
+          for (int e = 0; e < D; e += 16) {
+            float x[16], y[16];
+            load16<F16>(q + e, x);
+            load16<F16>(k + 2 * e, y);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s = fmaf(x[j], y[j], s);
+          }
+          load16<F16>(a.v + page * a.v_sp + w.kvh * a.v_sh + at * a.v_st + 2 * d0, v);
+        }
+        const float p = ex2_approx(fmaf(s, a.sigma_log2, z));
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[j] = fmaf(p, v[j], o[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (!(fabsf(dst[d0 + j]) < INFINITY)) dst[d0 + j] = o[j];
+  }
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(WIDE_THREADS, 1)
+    decode16_wide_kernel(const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV,
+                         const __grid_constant__ DecArgs a) {
+  using LY = WideLayout<D>;
+  constexpr int TB = LY::TB, NHALF = D / 64, HB = TILE * 128;  // 64-column halves of a tile
+  constexpr int ST = WIDE_STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t *sQ = base, *sK = base + LY::K_OFF, *sV = base + LY::V_OFF;
+  WideCtrl* c = reinterpret_cast<WideCtrl*>(base + LY::C_OFF);
+  volatile int* abort = &c->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&c->q_full, 256);
+    mbar_init(&c->q_empty, 1);
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&c->k_full[i], 1);
+      mbar_init(&c->k_empty[i], 1);
+      mbar_init(&c->v_full[i], 1);
+      mbar_init(&c->v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c->s_full[i], 1);
+      mbar_init(&c->p_full[i], 128);
+      mbar_init(&c->pv_done[i], 1);
+    }
+    mbar_init(&c->x_full, 128);
+    mbar_init(&c->x_empty, 128);
+    mbar_init(&c->drain, 1);
+    c->abort = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(&c->tmem_base, 512);
+    tmem_relinquish();
+  }
+  const Piece piece = cut<WIDE_UNIT, WIDE_SEGMENT_UNITS, WIDE_THREADS / 32>(a, c->cut);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c->tmem_base;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ copies
+    const int box = a.box, boxes = TILE / box;
+    uint32_t kc = 0;  // tiles so far
+    bool ok = true;
+    WideWork w;
+    for (WideWalk walk(a, piece); ok && walk.next(w);) {
+      const int32_t* table = a.table + static_cast<long long>(w.b) * a.table_stride;
+      const int page_size = a.tiles_per_page * TOK;
+      for (int t = 0; t < w.n; ++t, ++kc) {
+        // This lane's box; those past what any row sees stay as they are: their scores
+        // are masked and their values zeroed.
+        const int pos = (w.t0 + t) * TILE + lane * box;
+        const bool mine = lane < boxes && pos < w.max_lim;
+        const int loaded = __popc(__ballot_sync(0xffffffffu, mine));
+        int page = a.num_pages, at = 0;  // a page that is none reads as zeros
+        if (mine) {
+          const int entry = __ldg(table + pos / page_size);
+          at = pos % page_size;
+          if (entry >= 0 && entry < a.num_pages) page = entry;
+        }
+        const uint32_t st = kc % ST, par = ((kc / ST) & 1) ^ 1;
+        auto copy = [&](uint64_t* full, uint8_t* tile, const CUtensorMap* map) {
+          if (lane == 0) mbar_arrive_expect_tx(full, loaded * box * D * 2);
+          __syncwarp();
+          if (mine)
+            for (int hf = 0; hf < NHALF; ++hf)
+              tma_load_4d(tile + hf * HB + lane * box * 128, map, full, hf * 64, at, w.kvh, page);
+          __syncwarp();
+        };
+        if (!(ok = wait_all(&c->k_empty[st], par, abort, a.err, ERR_WAIT_K_EMPTY))) break;
+        copy(&c->k_full[st], sK + st * TB, &tmK);
+        if (!(ok = wait_all(&c->v_empty[st], par, abort, a.err, ERR_WAIT_V_EMPTY))) {
+          drain_wait(&c->k_full[st], (kc / ST) & 1);
+          break;
+        }
+        copy(&c->v_full[st], sV + st * TB, &tmV);
+      }
+    }
+    if (!ok) {  // let every copy already issued land before the CTA can exit
+      for (uint32_t i = 0; i < ST && i < kc; ++i) {
+        const uint32_t f = kc - 1 - i;
+        drain_wait(&c->k_full[f % ST], (f / ST) & 1);
+        drain_wait(&c->v_full[f % ST], (f / ST) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products
+    constexpr uint32_t IDESC_QK = idesc_f32acc<F16>(128, TILE, false, false);
+    constexpr uint32_t IDESC_PV = idesc_f32acc<F16>(128, D, false, true);
+    const uint64_t dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t dK = smem_desc_sw128(smem_u32(sK), 16, 1024);
+    const uint64_t dV = smem_desc_sw128(smem_u32(sV), HB, 1024);
+    uint32_t kc = 0, vc = 0, uc = 0, pc[2] = {0, 0};
+    bool ok = true;
+    WideWork w;
+    for (WideWalk walk(a, piece); ok && walk.next(w);) {
+      if (w.n == 0) continue;
+      if (!(ok = wait_all(&c->q_full, uc & 1, abort, a.err, ERR_WAIT_Q_FULL))) break;
+      ++uc;
+      auto scores = [&](int t) -> bool {  // S of tile t
+        const uint32_t st = kc % ST;
+        if (!wait_all(&c->k_full[st], (kc / ST) & 1, abort, a.err, ERR_WAIT_K_FULL)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_qk<D, 1>(tmem + (t & 1) * 128, dQ, dK + ((st * TB) >> 4), IDESC_QK);
+          umma_commit(&c->s_full[t & 1]);
+          umma_commit(&c->k_empty[st]);
+          if (t == w.n - 1) umma_commit(&c->q_empty);
+        }
+        __syncwarp();
+        ++kc;
+        return true;
+      };
+      for (int t = 0; t < 2 && t < w.n; ++t)
+        if (!(ok = scores(t))) break;
+      for (int t = 0; ok && t < w.n; ++t, ++vc) {
+        const int wg = t & 1;
+        const uint32_t st = vc % ST;
+        if (!(ok = wait_all(&c->v_full[st], (vc / ST) & 1, abort, a.err, ERR_WAIT_V_FULL))) break;
+        const int seen = w.max_lim - (w.t0 + t) * TILE;  // a hidden value may be anything
+        if (seen < TILE) zero_tile_rows<D>(sV + st * TB, seen, lane);
+        if (!(ok = wait_all(&c->p_full[wg], pc[wg] & 1, abort, a.err, ERR_WAIT_P_FULL))) break;
+        ++pc[wg];
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t d_o = tmem + 256 + wg * 128, d_p = tmem + wg * 128;
+          const uint64_t dv = dV + ((st * TB) >> 4);
+          const bool fresh = (t >> 1) % WIDE_RUN == 0;  // a run begins
+#pragma unroll
+          for (int kk = 0; kk < TILE / 16; ++kk) {
+            const uint32_t p = d_p + 32 * (kk >> 1) + 8 * (kk & 1);
+            umma_ts(d_o, p + 16, dv + ((kk * 2048) >> 4), IDESC_PV, fresh && kk == 0 ? 0u : 1u);
+            umma_ts(d_o, p, dv + ((kk * 2048) >> 4), IDESC_PV, 1u);
+          }
+          umma_commit(&c->pv_done[wg]);
+          umma_commit(&c->v_empty[st]);
+        }
+        __syncwarp();
+        if (t + 2 < w.n && !(ok = scores(t + 2))) break;
+      }
+    }
+    // Drain: every issued product completes before TMEM is given back.
+    if (elect_one()) umma_commit(&c->drain);
+    __syncwarp();
+    drain_wait(&c->drain, 0);
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax
+    const int wg = (warp - 4) >> 2, wq = warp & 3, row = wq * 32 + lane;
+    const uint32_t tlane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+    const uint32_t tS = tlane + wg * 128, tO = tlane + 256 + wg * 128;
+    const float sc = a.sigma_log2;
+    uint32_t sc_n = 0, pv_n = 0;  // tiles of this warpgroup, its products
+    uint32_t uc = 0, xc = 0;      // queries so far, segments within this CTA
+    bool ok = true;
+    WideWork w;
+    for (WideWalk walk(a, piece); ok && walk.next(w);) {
+      const int r = w.r0 + row;
+      const bool real = row < w.n_rows;
+      const int i = real ? r / a.group : 0;
+      const int lim = !real ? 0 : a.causal ? w.len - a.q_len + i + 1 : w.len;
+      const int slot = WIDE_PARTS * (2 * static_cast<int>(blockIdx.x) + (w.began ? 1 : 0)) + wg;
+      const long long at = static_cast<long long>(slot) * TILE + row;
+      if (w.began && threadIdx.x == 128)
+        a.joins[w.b * a.heads_kv * a.row_tiles + w.seg] =
+            make_int4(w.whole ? -1 : w.b, w.seg, static_cast<int>(blockIdx.x), w.last_cta);
+      if (w.n > 0) {
+        // ---- this thread's half of a query row, swizzled as TMA would
+        const int h = w.kvh * a.group + (r - i * a.group);
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + w.b * a.q_s[0] + h * a.q_s[1] +
+                                                          i * a.q_s[2]) + wg * (D / 16);
+        uint4 y[D / 16];
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) y[x] = real ? __ldg(src + x) : make_uint4(0u, 0u, 0u, 0u);
+        if (uc > 0 &&
+            !(ok = wait_all(&c->q_empty, (uc - 1) & 1, abort, a.err, ERR_WAIT_Q_EMPTY)))
+          break;
+        ++uc;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          const int at16 = wg * (D / 16) + x;
+          *reinterpret_cast<uint4*>(sQ + (at16 >> 3) * HB + row * 128 +
+                                    (((at16 & 7) ^ (row & 7)) << 4)) = y[x];
+        }
+        fence_proxy_async_shared();
+        mbar_arrive(&c->q_full);
+      }
+      // The other warpgroup may have yet to read this one's part of the segment before.
+      if (wg == 0 && xc > 0 &&
+          !(ok = wait_all(&c->x_empty, (xc - 1) & 1, abort, a.err, ERR_WAIT_WG)))
+        break;
+      float z = NO_SCORE, l = 0.f;        // of the run
+      float z_c = NO_SCORE, l_c = 0.f;    // of the runs before it
+      bool carried = false;
+      int in_run = 0;                     // tiles of the run so far
+      bool finite = true;
+      // Adds the run's O to what the part holds.
+      auto flush = [&](bool any) -> bool {
+        if (any && !wait_all(&c->pv_done[wg], (pv_n - 1) & 1, abort, a.err, ERR_WAIT_O_FULL))
+          return false;
+        tc_fence_after();
+        const float both = fminf(z, z_c);
+        const float f = ex2_approx(both - z), f_c = ex2_approx(both - z_c);
+        float4* dst = reinterpret_cast<float4*>(a.part_o + at * D);
+#pragma unroll 1
+        for (int x = 0; x < D / 32; ++x) {
+          uint32_t o[32];
+          if (any) {
+            tmem_ld32(tO + 32 * x, o);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          if (!real) continue;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float4 y = make_float4(__uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
+                                   __uint_as_float(o[4 * e + 2]) * f,
+                                   __uint_as_float(o[4 * e + 3]) * f);
+            if (carried) {
+              const float4 old = dst[8 * x + e];
+              y.x = fmaf(old.x, f_c, y.x), y.y = fmaf(old.y, f_c, y.y);
+              y.z = fmaf(old.z, f_c, y.z), y.w = fmaf(old.w, f_c, y.w);
+            }
+            finite = finite && fabsf(y.x) < INFINITY && fabsf(y.y) < INFINITY &&
+                     fabsf(y.z) < INFINITY && fabsf(y.w) < INFINITY;
+            dst[8 * x + e] = y;
+          }
+        }
+        tc_fence_before();
+        l_c = fmaf(l_c, f_c, l * f);
+        z_c = both;
+        l = 0.f;
+        carried = true;
+        in_run = 0;
+        return true;
+      };
+
+      for (int t = wg; t < w.n; t += 2) {
+        if (in_run == WIDE_RUN && !(ok = flush(true))) break;
+        if (!(ok = wait_all(&c->s_full[wg], sc_n & 1, abort, a.err, ERR_WAIT_S_FULL))) break;
+        ++sc_n;
+        tc_fence_after();
+        const int tok0 = (w.t0 + t) * TILE;
+        const bool masked = tok0 + TILE > w.min_lim;
+        const int seen = lim - tok0;  // keys of the tile that this row sees
+        // ---- the largest score
+        float m = -INFINITY;
+#pragma unroll 2
+        for (int x = 0; x < 4; ++x) {
+          uint32_t s[32];
+          float mx;
+          tmem_ld32_max(tS + 32 * x, s, mx);
+          tmem_wait_ld();
+          if (masked) {
+            mx = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * x + e < seen) mx = fmaxf(mx, __uint_as_float(s[e]));
+          }
+          m = fmaxf(m, mx);
+        }
+        m *= sc;
+        const bool over = m + z > SHIFT + HEADROOM;
+        if (__any_sync(0xffffffffu, over)) {
+          const float z1 = over ? fminf(z, SHIFT - m) : z;
+          const float f = ex2_approx(z1 - z);
+          z = z1;
+          l *= f;
+          if (in_run > 0) {  // O of the run's tiles before
+            if (!(ok = wait_all(&c->pv_done[wg], (pv_n - 1) & 1, abort, a.err, ERR_WAIT_O_FULL)))
+              break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = 0; x < D / 32; ++x) {
+              uint32_t o[32];
+              tmem_ld32(tO + 32 * x, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(tO + 32 * x, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        // ---- weights, in place of their scores
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+        for (int x = 0; x < 4; ++x) {
+          uint32_t s[32], hi[16], lo[16];
+          tmem_ld32(tS + 32 * x, s);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float p0 = ex2_approx(fmaf(__uint_as_float(s[2 * e]), sc, z));
+            float p1 = ex2_approx(fmaf(__uint_as_float(s[2 * e + 1]), sc, z));
+            if (masked) {
+              if (32 * x + 2 * e >= seen) p0 = 0.f;
+              if (32 * x + 2 * e + 1 >= seen) p1 = 0.f;
+            }
+            l4[2 * (e & 1)] += p0;
+            l4[2 * (e & 1) + 1] += p1;
+            hi[e] = pack_x2<F16>(p0, p1);
+            const float2 q = x2_to_f32(hi[e], F16);
+            lo[e] = pack_x2<F16>(p0 - q.x, p1 - q.y);
+          }
+          tmem_st16(tS + 32 * x, hi);
+          tmem_st16(tS + 32 * x + 16, lo);
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&c->p_full[wg]);
+        ++pv_n;
+        ++in_run;
+      }
+      if (!ok) break;
+      if (!w.whole || carried) {
+        if (!(ok = flush(in_run > 0))) break;
+        if (real && !finite && l_c < INFINITY)
+          wide_exact_row<D, F16>(a, w, r, wg, z_c, a.part_o + at * D);
+        if (!w.whole) {
+          if (real) a.part_ml[at] = make_float2(-z_c, l_c);
+          continue;
+        }
+      }
+      // ---- a segment within this CTA: both parts from where they are, TMEM or (after
+      // more than one run) global memory
+      const bool any = in_run > 0;
+      if (any && !(ok = wait_all(&c->pv_done[wg], (pv_n - 1) & 1, abort, a.err, ERR_WAIT_O_FULL)))
+        break;
+      if (wg == 0) {
+        c->part[row] = carried ? make_float2(z_c, l_c) : make_float2(z, l);
+        tc_fence_before();
+        mbar_arrive(&c->x_full);
+      } else {
+        if (!(ok = wait_all(&c->x_full, xc & 1, abort, a.err, ERR_WAIT_WG))) break;
+        tc_fence_after();
+        const float2 other = c->part[row];
+        const int tiles0 = (w.n + 1) / 2;  // of the other warpgroup
+        const float my_z = carried ? z_c : z, my_l = carried ? l_c : l;
+        const float both = fminf(my_z, other.x);
+        const float f = ex2_approx(both - my_z), f0 = ex2_approx(both - other.x);
+        const float sum = fmaf(my_l, f, other.y * f0);
+        float4 *own = reinterpret_cast<float4*>(a.part_o + at * D), *first = own - TILE * D / 4;
+        bool sums_finite = true;
+        // The O's of 32 elements.
+        auto parts = [&](int x, float (&o)[32], float (&o0)[32]) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = o0[e] = 0.f;
+          auto load = [&](uint32_t from, const float4* held, bool in_memory, bool there,
+                          float (&to)[32]) {
+            if (in_memory) {
+#pragma unroll
+              for (int e = 0; e < 8 && real; ++e)
+                *reinterpret_cast<float4*>(to + 4 * e) = __ldcg(held + 8 * x + e);
+            } else if (there) {
+              uint32_t v[32];
+              tmem_ld32(from + 32 * x, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) to[e] = __uint_as_float(v[e]);
+            }
+          };
+          load(tO, own, carried, any, o);
+          load(tO - 128, first, tiles0 > WIDE_RUN, tiles0 > 0, o0);
+        };
+        auto store = [&](int x, const float (&o)[32], const float (&o0)[32]) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 y = make_float4(fmaf(o[e], f, o0[e] * f0),
+                                         fmaf(o[e + 1], f, o0[e + 1] * f0),
+                                         fmaf(o[e + 2], f, o0[e + 2] * f0),
+                                         fmaf(o[e + 3], f, o0[e + 3] * f0));
+            sums_finite = sums_finite && fabsf(y.x) < INFINITY && fabsf(y.y) < INFINITY &&
+                          fabsf(y.z) < INFINITY && fabsf(y.w) < INFINITY;
+            store_row4(a, w.b, w.kvh, r, 32 * x + e, -both, sum, y);
+          }
+        };
+#pragma unroll 1
+        for (int x = 0; x < D / 32; ++x) {
+          float o[32], o0[32];
+          parts(x, o, o0);
+          if (real) store(x, o, o0);
+        }
+        if (__any_sync(0xffffffffu, real && !sums_finite && sum < INFINITY)) {
+          // As for parts that go to the join: into memory, and what is not finite anew.
+#pragma unroll 1
+          for (int x = 0; x < D / 32; ++x) {
+            float o[32], o0[32];
+            parts(x, o, o0);
+            for (int e = 0; e < 32 && real; e += 4) {
+              own[8 * x + e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              first[8 * x + e / 4] = make_float4(o0[e], o0[e + 1], o0[e + 2], o0[e + 3]);
+            }
+          }
+          if (real) {
+            wide_exact_row<D, F16>(a, w, r, 1, my_z, a.part_o + at * D);
+            wide_exact_row<D, F16>(a, w, r, 0, other.x, a.part_o + (at - TILE) * D);
+            for (int x = 0; x < D / 4; ++x) {
+              const float4 y = own[x], y0 = first[x];
+              store_row4(a, w.b, w.kvh, r, 4 * x, -both, sum,
+                         make_float4(fmaf(y.x, f, y0.x * f0), fmaf(y.y, f, y0.y * f0),
+                                     fmaf(y.z, f, y0.z * f0), fmaf(y.w, f, y0.w * f0)));
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&c->x_empty);
+      }
+      ++xc;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// One call: the kernel and the join of its parts.
+template <int D, bool F16>
+bsfa_status run_wide(const CUtensorMap& tmK, const CUtensorMap& tmV, const DecArgs& a,
+                     const Plan& pl, int sms, int dev, cudaStream_t stream) {
+  static std::atomic<uint64_t> ready{0};
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    const bsfa_status v = status_of(cudaFuncSetAttribute(
+        decode16_wide_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        WideLayout<D>::BYTES));
+    if (v != BSFA_OK) return v;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  int grid = sms < MAX_SMS ? sms : MAX_SMS;
+  const long long most = (pl.all_units + MIN_UNITS - 1) / MIN_UNITS;
+  if (most < grid) grid = static_cast<int>(most);
+  decode16_wide_kernel<D, F16>
+      <<<static_cast<unsigned>(grid), WIDE_THREADS, WideLayout<D>::BYTES, stream>>>(tmK, tmV, a);
+  const bsfa_status first = status_of(cudaGetLastError());
+  if (first != BSFA_OK) return first;
+  return launch_join<D, TILE, WIDE_PARTS>(a, pl.segments, grid, pl.segments, stream);
+}
+
+}  // namespace decode16
+
+}  // namespace bsfa

@@ -24,4 +24,11 @@ template <int D, int BK, bool GATING, bool CALIB, bool F16, bool VALL, bool PAGE
           bool CORR = false>
 cudaError_t launch_xs(const Maps& m, const DevParams& p, int grid, cudaStream_t stream);
 
+// bsfa_api.cu: a 4-D tensor map of 16-bit elements {d, tokens, heads, batch} in boxes of
+// box_rows tokens, strides in elements, and the device error word (nullptr: not found).
+bool make_map(CUtensorMap* m, const void* ptr, bool f16, int d, long long tokens, int heads,
+              int batch, long long st_tok, long long st_head, long long st_batch,
+              int box_rows = TILE);
+unsigned* device_error_word();
+
 }  // namespace bsfa
