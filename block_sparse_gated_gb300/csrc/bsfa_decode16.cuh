@@ -146,7 +146,7 @@ struct Piece {
 
 // Cuts the line.  Every CTA adds up the lengths by itself: a few loads per
 // thread, no extra launch.
-template <int U, int FIXED, int WARPS>
+template <int U, int FIXED, int LEAST, int WARPS>
 __device__ __forceinline__ Piece cut(const DecArgs& a, int* sh) {
   constexpr int THREADS = 32 * WARPS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -171,7 +171,7 @@ __device__ __forceinline__ Piece cut(const DecArgs& a, int* sh) {
   }
   Piece p;
   const int all = total * per_unit;
-  p.per_cta = max(MIN_UNITS, (all + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+  p.per_cta = max(LEAST, (all + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
   p.begin = static_cast<int>(min(static_cast<long long>(all),
                                  static_cast<long long>(blockIdx.x) * p.per_cta));
   p.end = min(all, p.begin + p.per_cta);
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(32 * W, Shape<D, NT>::CTAS * decode16::WARPS /
     // Lets the join's blocks take their places, where they wait for this kernel's end.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0 && !a.join_by_segment) a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    piece = cut<UNIT, SEGMENT_UNITS, WARPS>(a, sh_cut);
+    piece = cut<UNIT, SEGMENT_UNITS, MIN_UNITS, WARPS>(a, sh_cut);
   } else {  // one segment per cluster; u walks over it once
     const int seg = static_cast<int>(blockIdx.x) / a.cluster, per_b = a.heads_kv * a.row_tiles;
     piece.b = seg / per_b;

@@ -30,6 +30,7 @@ namespace decode16 {
 
 constexpr int WIDE_UNIT = TILE;        // tokens of a work unit
 constexpr int WIDE_SEGMENT_UNITS = 6;  // a segment's fixed cost, in units
+constexpr int WIDE_MIN_UNITS = 1;      // shortest piece of the line worth a CTA
 constexpr int WIDE_THREADS = 384;
 constexpr int WIDE_RUN = 64;           // tiles that a warpgroup sums in TMEM, at most
 constexpr int WIDE_STAGES = 3;         // of the key and of the value ring
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     tmem_alloc(&c->tmem_base, 512);
     tmem_relinquish();
   }
-  const Piece piece = cut<WIDE_UNIT, WIDE_SEGMENT_UNITS, WIDE_THREADS / 32>(a, c->cut);
+  const Piece piece = cut<WIDE_UNIT, WIDE_SEGMENT_UNITS, WIDE_MIN_UNITS, WIDE_THREADS / 32>(a, c->cut);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -421,19 +422,25 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         const int seen = lim - tok0;  // keys of the tile that this row sees
         // ---- the largest score
         float m = -INFINITY;
-#pragma unroll 2
-        for (int x = 0; x < 4; ++x) {
-          uint32_t s[32];
-          float mx;
-          tmem_ld32_max(tS + 32 * x, s, mx);
-          tmem_wait_ld();
-          if (masked) {
-            mx = -INFINITY;
+        if (!masked) {
+#pragma unroll 1
+          for (int x = 0; x < 4; ++x) {
+            uint32_t s[32];  // not looked at: the load gives their maximum
+            float mx;
+            tmem_ld32_max(tS + 32 * x, s, mx);
+            tmem_wait_ld();
+            m = fmaxf(m, mx);
+          }
+        } else {
+#pragma unroll 1
+          for (int x = 0; x < 4; ++x) {
+            uint32_t s[32];
+            tmem_ld32(tS + 32 * x, s);
+            tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (32 * x + e < seen) mx = fmaxf(mx, __uint_as_float(s[e]));
+              if (32 * x + e < seen) m = fmaxf(m, __uint_as_float(s[e]));
           }
-          m = fmaxf(m, mx);
         }
         m *= sc;
         const bool over = m + z > SHIFT + HEADROOM;
@@ -459,30 +466,43 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
           }
         }
         // ---- weights, in place of their scores
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-        for (int x = 0; x < 4; ++x) {
-          uint32_t s[32], hi[16], lo[16];
-          tmem_ld32(tS + 32 * x, s);
-          tmem_wait_ld();
+        const uint64_t sc2 = f2_pack(sc, sc), z2 = f2_pack(z, z);
+        uint64_t sum2[2] = {0, 0};
+        auto weights = [&](auto masked_tag) {
+#pragma unroll 1
+          for (int x = 0; x < 4; ++x) {
+            uint32_t s[32], hi[16], lo[16];
+            tmem_ld32(tS + 32 * x, s);
+            tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float p0 = ex2_approx(fmaf(__uint_as_float(s[2 * e]), sc, z));
-            float p1 = ex2_approx(fmaf(__uint_as_float(s[2 * e + 1]), sc, z));
-            if (masked) {
-              if (32 * x + 2 * e >= seen) p0 = 0.f;
-              if (32 * x + 2 * e + 1 >= seen) p1 = 0.f;
+            for (int e = 0; e < 16; ++e) {
+              float p0, p1;
+              f2_unpack(
+                  f2_fma(f2_pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), sc2, z2),
+                  p0, p1);
+              p0 = ex2_approx(p0), p1 = ex2_approx(p1);
+              if constexpr (decltype(masked_tag)::value) {
+                if (32 * x + 2 * e >= seen) p0 = 0.f;
+                if (32 * x + 2 * e + 1 >= seen) p1 = 0.f;
+              }
+              const uint64_t p = f2_pack(p0, p1);
+              sum2[e & 1] = f2_add(sum2[e & 1], p);
+              hi[e] = pack_x2<F16>(p0, p1);
+              const float2 q = x2_to_f32(hi[e], F16);
+              f2_unpack(f2_add(p, f2_pack(-q.x, -q.y)), p0, p1);
+              lo[e] = pack_x2<F16>(p0, p1);
             }
-            l4[2 * (e & 1)] += p0;
-            l4[2 * (e & 1) + 1] += p1;
-            hi[e] = pack_x2<F16>(p0, p1);
-            const float2 q = x2_to_f32(hi[e], F16);
-            lo[e] = pack_x2<F16>(p0 - q.x, p1 - q.y);
+            tmem_st16(tS + 32 * x, hi);
+            tmem_st16(tS + 32 * x + 16, lo);
           }
-          tmem_st16(tS + 32 * x, hi);
-          tmem_st16(tS + 32 * x + 16, lo);
-        }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        };
+        if (masked)
+          weights(std::true_type{});
+        else
+          weights(std::false_type{});
+        float l0, l1;
+        f2_unpack(f2_add(sum2[0], sum2[1]), l0, l1);
+        l += l0 + l1;
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&c->p_full[wg]);
@@ -605,7 +625,7 @@ bsfa_status run_wide(const CUtensorMap& tmK, const CUtensorMap& tmV, const DecAr
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   int grid = sms < MAX_SMS ? sms : MAX_SMS;
-  const long long most = (pl.all_units + MIN_UNITS - 1) / MIN_UNITS;
+  const long long most = (pl.all_units + WIDE_MIN_UNITS - 1) / WIDE_MIN_UNITS;
   if (most < grid) grid = static_cast<int>(most);
   decode16_wide_kernel<D, F16>
       <<<static_cast<unsigned>(grid), WIDE_THREADS, WideLayout<D>::BYTES, stream>>>(tmK, tmV, a);

@@ -244,7 +244,8 @@ def test_rows_that_are_refused(lib):
 
 
 @pytest.mark.parametrize("source", ["bsfa_cache16", "inst_decode16_d64_bf16", "inst_decode16_d64_f16",
-                                    "inst_decode16_d128_bf16", "inst_decode16_d128_f16"])
+                                    "inst_decode16_d128_bf16", "inst_decode16_d128_f16",
+                                    "inst_decode16_wide_d64", "inst_decode16_wide_d128"])
 def test_kernels_do_not_spill(lib, source):
     """The compiler warns of registers that it spills to local memory."""
     from block_sparse_gated_gb300 import build
