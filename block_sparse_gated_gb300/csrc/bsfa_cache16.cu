@@ -9,7 +9,9 @@
 // One thread owns eight pairs of a row: 16 elements in two 16-byte pieces, so that
 // the threads of a row read and write whole lines.  It forms its eight sines and
 // cosines once and walks over the heads it is given, of the queries, the keys or
-// the values.  Both calls move each byte once and are bound by HBM.
+// the values.  Both calls move each byte once and are bound by HBM: 32 query and 8 KV
+// heads of 32768 tokens, d = 128 (671 MB), are rotated in 100 us, 6.7 TB/s (a copy runs
+// at 6.79); 131072 tokens of them rotated and written to pages (3.22 GB) in 459 us, 7.0.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -25,8 +27,14 @@ namespace {
 
 constexpr int THREADS = 128;
 constexpr int CHUNK = 16;  // elements of a row that a thread owns: eight pairs
-constexpr int AHEAD = 3;   // heads whose loads a thread issues at once
-constexpr int FILL = 600;  // blocks that a call with few rows is spread over
+// Heads whose loads a thread issues at once (that prompt, a gradient of 15009 tokens,
+// 10396 packed tokens of 32 heads of d = 64: 99.6, 49.0 and 18.5 us; at 4 100.2, 50.1
+// and 18.1, at 2 100.1, 50.6 and 19.0).
+constexpr int AHEAD = 3;
+// Blocks that a call with few rows is spread over.  More of them form the same angles
+// more often, fewer leave SMs idle (the packed tokens, and one token of 256 sequences:
+// 18.1 and 4.3 us; at 2048 20.9 and 5.1).
+constexpr int FILL = 600;
 
 enum Kind { QUERIES, KEYS, VALUES };
 

@@ -23,7 +23,12 @@
 // right as they grow.  A segment that a cut crosses leaves partial sums in the
 // workspace, which a second kernel joins in a fixed order.
 //
-// Bound.  512 bytes per (token, KV head) at d = 128: HBM.
+// Bound.  512 bytes per (token, KV head) at d = 128, and 4 flops of a query row to
+// each two of them: HBM.  64 ragged sequences to 16K (2.25 GB) take 321 us, 7.0 TB/s
+// where a copy runs at 6.79; the issue slots are 18% used there, the tensor pipe 14%.
+// Twenty rows leave 255 registers to a thread and eight warps to an SM, so that fixed
+// latencies show: five tokens over 16 ragged sequences to 32K 226 us, 6.2 TB/s.  More
+// than 32 rows are bsfa_decode16_wide.cuh's.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -47,10 +52,17 @@ constexpr float HEADROOM = 5.f;     // log2 a weight may pass 2^SHIFT by
 constexpr float SHIFT = 10.f;       // log2 of the factor that a weight carries
 constexpr float NO_SCORE = 3e38f;   // a row's offset before its first score
 constexpr int MIN_UNITS = 4;        // shortest piece of the line worth a CTA
-constexpr int SEGMENT_UNITS = 3;    // a segment's fixed cost, in units
-constexpr int WIDE_ROWS = 32;       // query rows of a KV head beyond which a call may be wide
-constexpr int WIDE_LEAST = 512;     // ... from that bound on the lengths
-constexpr int WIDE_SEGMENTS = 1 << 16;  // ... and up to so many segments
+// A segment's fixed cost, in units (128 ragged sequences to 2K, cut, and 1 x 128K: 90.2
+// and 84.0 us; at 1 96.4 and 85.5, at 5 89.6 and 84.7).
+constexpr int SEGMENT_UNITS = 3;
+// A call is wide from that many query rows of a KV head on, if the lengths' bound and
+// the segments allow (64 ragged sequences to 16K with 16 rows 335 us, wide 347; five
+// tokens of four heads over 16 to 32K, 20 rows, 227 and 232; 32 rows 224 and 226; 33
+// rows, two row tiles, 172 and 102; 128 rows over 4 x 300 tokens 21.9 and 23.3, over
+// 16 x 600 35.0 and 32.5).
+constexpr int WIDE_ROWS = 32;
+constexpr int WIDE_LEAST = 512;
+constexpr int WIDE_SEGMENTS = 1 << 16;
 constexpr int JOIN_THREADS = 256;   // of the kernel that joins parts
 constexpr int JOIN_ROWS_PARTS = 8;  // a warp to a row below, a block above
 constexpr int MAX_PARTS = 768;      // parts of a segment, at most: CTAs of a cut call
@@ -65,7 +77,10 @@ constexpr int SMALL_UNITS = 4;      // ... and units of a segment
 
 // Per head dimension and row-tile width: CTAs of four warps on an SM, tiles in a
 // warp's ring, and the most CTAs a cut call has (the workspace holds two partial
-// results each).
+// results each).  At d = 64 two CTAs with rings of six tiles leave 256 sequences of 600
+// tokens on two heads a second wave, 15.8 us, four with three tiles 12.3.  At d = 128 a
+// third CTA with rings of two tiles gains nothing (64 ragged sequences to 16K 320 us
+// both), and two with them lose (324).
 template <int CTAS_, int STAGES_>
 struct ShapeOf {
   static constexpr int CTAS = CTAS_, STAGES = STAGES_, MAX_GRID = MAX_SMS * CTAS;
@@ -286,7 +301,8 @@ __global__ void __launch_bounds__(32 * W, Shape<D, NT>::CTAS * decode16::WARPS /
   if (a.cluster > 1) cluster_arrive();
   Piece piece;
   if (W == decode16::WARPS && a.split) {
-    // Lets the join's blocks take their places, where they wait for this kernel's end.
+    // Lets the join's blocks take their places, where they wait for this kernel's end
+    // (1 x 16K, cut: 19.2 -> 18.5 us).
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0 && !a.join_by_segment) a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
     piece = cut<UNIT, SEGMENT_UNITS, MIN_UNITS, WARPS>(a, sh_cut);
@@ -503,7 +519,9 @@ __global__ void __launch_bounds__(32 * W, Shape<D, NT>::CTAS * decode16::WARPS /
       }
       // The products take 16-bit factors: a weight goes in as two, itself rounded and
       // the remainder rounded, which leaves 2^-16 of it (bf16; fp16 2^-22) and makes
-      // O as good as its own rounding.
+      // O as good as its own rounding.  The second product costs nothing at one or two
+      // row tiles and 1.5% at three (five tokens over 16 ragged sequences to 32K: 218 us
+      // without it, 221).
       uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {

@@ -523,10 +523,11 @@ bsfa_status bsfa_cache16_write(const bsfa_cache16* cache, const bsfa_rope* rope,
 
 /* Attention of q_len new tokens of each sequence over its cached keys and values:
  * bsfa_decode4 over 16-bit pages, with the same parameters (dtype must be the
- * cache's) and the same limits.  Products run on the tensor cores in that type with
- * fp32 accumulation; weights take part as the sum of two 16-bit numbers, so O is off
- * by little more than its one rounding.  A token that a query does not see has no
- * part in its result, whatever its rows hold. */
+ * cache's, the workspace of bsfa_decode16_workspace_size) and the same limits.
+ * Products run on the tensor cores in that type with fp32 accumulation; weights take
+ * part as the sum of two 16-bit numbers, so O is off by little more than its one
+ * rounding.  A token that a query does not see has no part in its result, whatever its
+ * rows hold.  Scores below -3e38 weigh nothing. */
 size_t bsfa_decode16_workspace_size(const bsfa_cache16* cache, const bsfa_decode4_params* p);
 bsfa_status bsfa_decode16(const bsfa_cache16* cache, const bsfa_decode4_params* p,
                           bsfa_stream_t stream);
