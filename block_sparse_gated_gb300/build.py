@@ -67,9 +67,11 @@ def _compile(src: str, verbose_ptxas: bool) -> tuple[str, str]:
     return obj, r.stdout + r.stderr
 
 
-def _torch_place() -> tuple[str, str]:
-    """Where torch lies and its version, without importing it."""
+def _torch_place() -> tuple[str, str] | None:
+    """Where torch lies and its version, without importing it; None without torch."""
     spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
     root = os.path.dirname(spec.origin)
     with open(os.path.join(root, "version.py")) as f:
         return root, re.search(r"__version__ = '([^']*)'", f.read()).group(1)
@@ -108,9 +110,9 @@ def build(force: bool = False, jobs: int | None = None, verbose_ptxas: bool = Fa
     os.makedirs(OBJDIR, exist_ok=True)
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < _deps_mtime():
         _build_library(jobs, verbose_ptxas)
-    root, version = _torch_place()
-    if force or not _binding_is_current(version):
-        _build_binding(root, version)
+    place = _torch_place()  # the library itself does not need it
+    if place is not None and (force or not _binding_is_current(place[1])):
+        _build_binding(*place)
     return LIB
 
 

@@ -576,25 +576,29 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
           load(tO, own, carried, any, o);
           load(tO - 128, first, tiles0 > WIDE_RUN, tiles0 > 0, o0);
         };
-        auto store = [&](int x, const float (&o)[32], const float (&o0)[32]) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 y = make_float4(fmaf(o[e], f, o0[e] * f0),
-                                         fmaf(o[e + 1], f, o0[e + 1] * f0),
-                                         fmaf(o[e + 2], f, o0[e + 2] * f0),
-                                         fmaf(o[e + 3], f, o0[e + 3] * f0));
-            sums_finite = sums_finite && fabsf(y.x) < INFINITY && fabsf(y.y) < INFINITY &&
-                          fabsf(y.z) < INFINITY && fabsf(y.w) < INFINITY;
-            store_row4(a, w.b, w.kvh, r, 32 * x + e, -both, sum, y);
-          }
-        };
+        // Whether all is finite comes before the first store: the output may be the queries
+        // themselves, which are needed once more where it is not.
 #pragma unroll 1
         for (int x = 0; x < D / 32; ++x) {
           float o[32], o0[32];
           parts(x, o, o0);
-          if (real) store(x, o, o0);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            sums_finite = sums_finite && fabsf(fmaf(o[e], f, o0[e] * f0)) < INFINITY;
         }
-        if (__any_sync(0xffffffffu, real && !sums_finite && sum < INFINITY)) {
+        if (!__any_sync(0xffffffffu, real && !sums_finite && sum < INFINITY)) {
+#pragma unroll 1
+          for (int x = 0; x < D / 32; ++x) {
+            float o[32], o0[32];
+            parts(x, o, o0);
+#pragma unroll
+            for (int e = 0; e < 32 && real; e += 4)
+              store_row4(a, w.b, w.kvh, r, 32 * x + e, -both, sum,
+                         make_float4(fmaf(o[e], f, o0[e] * f0), fmaf(o[e + 1], f, o0[e + 1] * f0),
+                                     fmaf(o[e + 2], f, o0[e + 2] * f0),
+                                     fmaf(o[e + 3], f, o0[e + 3] * f0)));
+          }
+        } else {
           // As for parts that go to the join: into memory, and what is not finite anew.
 #pragma unroll 1
           for (int x = 0; x < D / 32; ++x) {

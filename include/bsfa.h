@@ -517,7 +517,7 @@ bsfa_status bsfa_rotary(const bsfa_rope* rope, const bsfa_rows16* rows, bsfa_str
  * be NULL.  num_heads_kv, head_dim and dtype must be the cache's.  Rows whose
  * position names no cache row are dropped, and their queries rotated all the same.
  * Positions of one call must differ: where two rows share one, it holds some
- * mixture of the two. */
+ * mixture of the two.  The rows must not overlap the pools. */
 bsfa_status bsfa_cache16_write(const bsfa_cache16* cache, const bsfa_rope* rope,
                                const bsfa_rows16* rows, bsfa_stream_t stream);
 
@@ -527,7 +527,8 @@ bsfa_status bsfa_cache16_write(const bsfa_cache16* cache, const bsfa_rope* rope,
  * Products run on the tensor cores in that type with fp32 accumulation; weights take
  * part as the sum of two 16-bit numbers, so O is off by little more than its one
  * rounding.  A token that a query does not see has no part in its result, whatever its
- * rows hold.  Scores below -3e38 weigh nothing. */
+ * rows hold.  Scores below -3e38 weigh nothing.  o may be q itself, with the same
+ * strides. */
 size_t bsfa_decode16_workspace_size(const bsfa_cache16* cache, const bsfa_decode4_params* p);
 bsfa_status bsfa_decode16(const bsfa_cache16* cache, const bsfa_decode4_params* p,
                           bsfa_stream_t stream);

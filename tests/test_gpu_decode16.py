@@ -715,6 +715,87 @@ def test_many_query_rows_in_graphs_with_strides_and_two_streams(cuda_device):
         b.decode16(q[0], cache, table, n32[0], workspace=ws[0][:need - 256])
 
 
+@pytest.mark.parametrize("heads", [(8, 2, 2), (40, 1, 2)])
+@pytest.mark.parametrize("cut", [True, False])
+def test_results_in_place_of_the_queries(cuda_device, heads, cut):
+    """Also beside a value that is not a number and that some queries do not see."""
+    b = _bsfa()
+    Hq, Hkv, n = heads
+    lens = [700, 3, 0, 1200]
+    cache, table, rows = cu.random_cache(b, lens, 32, Hkv, 64, BF, 6, cuda_device)
+    table = widen(table, 32) if cut else table
+    q = _queries(4, Hq, n, 64, BF, 6, cuda_device)
+    n32 = _i32(lens, cuda_device)
+    for bad in (None, float("nan")):
+        if bad is not None:  # in the last token of the first sequence
+            cache.v[table[0, 699 // 32].item(), :, 699 % 32, 3] = bad
+        want = b.decode16(q, cache, table, n32, return_lse=True)
+        mine = q.clone()
+        got = b.decode16(mine, cache, table, n32, out=mine, return_lse=True)
+        assert got["out"] is mine
+        for x, y in zip(want.values(), got.values()):
+            assert torch.equal(torch.nan_to_num(x.float(), nan=1e9), torch.nan_to_num(y.float(), nan=1e9))
+        if bad is None:
+            cu.check_decode(got, q, rows, lens, BF, 64)
+    assert bool(torch.isnan(want["out"][0, :, 1, 3]).all())
+    assert bool(torch.isfinite(want["out"][0, :, 0]).all())
+
+
+def test_first_calls_within_a_capture(cuda_device):
+    """A process whose first call of each kernel is captured."""
+    import subprocess
+    import sys
+    code = """
+import torch, block_sparse_gated_gb300 as b
+dev = torch.device("cuda:0")
+x = torch.randn(2, 48, 1, 64, device=dev).bfloat16()
+k = torch.randn(2, 1, 600, 64, device=dev).bfloat16()
+cache = b.cache16_empty(20, 1, 64, 64)
+table = torch.arange(20, dtype=torch.int32, device=dev).view(2, 10)
+n = torch.full((2,), 600, dtype=torch.int32, device=dev)
+rope = b.Rope(torch.rand(32, device=dev))
+def calls():
+    b.cache16_write(cache, k, k, table, rope=rope)
+    q, _ = b.rotary(rope, x, start=n - 1)
+    return [b.decode16(q[:, :h], cache, table, n)["out"] for h in (1, 16, 48)]
+g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    got = calls()
+g.replay()
+want = calls()
+torch.cuda.synchronize()
+assert all(torch.equal(a, c) for a, c in zip(got, want)) and bool(got[2].any())
+print("same")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.stdout.strip() == "same", r.stdout + r.stderr
+
+
+def test_calls_from_several_threads(cuda_device):
+    """Each thread on a stream of its own, the same caches read by all."""
+    from concurrent.futures import ThreadPoolExecutor
+    b = _bsfa()
+    lens = [900, 50]
+    cache, table, rows = cu.random_cache(b, lens, 32, 2, 64, HF, 6, cuda_device)
+    table = widen(table, 32)
+    n32 = _i32(lens, cuda_device)
+    qs = [_queries(2, 8 * (1 + 9 * (i % 2)), 1, 64, HF, i, cuda_device) for i in range(6)]
+    torch.cuda.synchronize()
+
+    def work(q):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                r = b.decode16(q, cache, table, n32, return_lse=True)
+        s.synchronize()
+        return r
+
+    with ThreadPoolExecutor(6) as ex:
+        for q, r in zip(qs, ex.map(work, qs)):
+            cu.check_decode(r, q, rows, lens, HF, 64)
+
+
 def test_the_waits_of_many_query_rows_did_not_run_out(cuda_device):
     from block_sparse_gated_gb300 import api
     assert api.device_error() == 0
