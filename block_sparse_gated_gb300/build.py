@@ -86,7 +86,7 @@ def _build_binding(root: str, version: str) -> None:
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            *[x for i in inc for x in ("-isystem", i)], os.path.join(CSRC, "binding.cpp"),
            "-o", tmp, "-L", PKG, "-l:libbsfa.so", "-L", os.path.join(root, "lib"),
-           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
            "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

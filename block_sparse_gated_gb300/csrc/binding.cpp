@@ -9,7 +9,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty_like.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -111,9 +111,11 @@ class Place {
     return t;
   }
   Tensor empty(at::IntArrayRef size, at::ScalarType type) const {
-    return fresh([&] { return at::empty(size, at::TensorOptions(type).device(device_)); });
+    return fresh(
+        [&] { return Tensor(at::detail::empty_cuda(size, type, device_, std::nullopt)); });
   }
   Tensor like(const Tensor& t) const {
+    if (t.is_contiguous()) return empty(t.sizes(), t.scalar_type());
     return fresh([&] { return at::empty_like(t); });
   }
 
