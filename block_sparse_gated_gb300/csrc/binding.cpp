@@ -110,6 +110,7 @@ class Place {
     t.record_stream(mine);
     return t;
   }
+  // (Straight from the allocator: a fifth of a short call's time was torch's dispatch.)
   Tensor empty(at::IntArrayRef size, at::ScalarType type) const {
     return fresh(
         [&] { return Tensor(at::detail::empty_cuda(size, type, device_, std::nullopt)); });

@@ -144,6 +144,8 @@ __device__ __forceinline__ void turn(float f, long long position, float& c, floa
 template <int D, bool F16, bool INTERLEAVED>
 __global__ void __launch_bounds__(THREADS) rows16_kernel(const __grid_constant__ RowsArgs a) {
   constexpr int GROUPS = D / CHUNK;  // threads of a row
+  allow_next_kernel();
+  wait_for_kernels_before();
   const int g = threadIdx.x & (GROUPS - 1);
   const long long t =
       static_cast<long long>(blockIdx.x) * (THREADS / GROUPS) + threadIdx.x / GROUPS;
@@ -353,11 +355,21 @@ bsfa_status launch_rows(const bsfa_cache16* c, const bsfa_rope* rope, const bsfa
        {rows16_kernel<128, false, false>, rows16_kernel<128, false, true>}},
       {{rows16_kernel<64, true, false>, rows16_kernel<64, true, true>},
        {rows16_kernel<128, true, false>, rows16_kernel<128, true, true>}}};
-  kernels[r->dtype == BSFA_DTYPE_F16][r->head_dim == 128][interleaved]
-      <<<dim3(static_cast<unsigned>(blocks), y), THREADS, 0,
-         reinterpret_cast<cudaStream_t>(stream_)>>>(a);
-  // Asked here, so that a later launch does not report this one's error.
-  return cudaGetLastError() == cudaSuccess ? BSFA_OK : BSFA_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), y);
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream_);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg,
+                         kernels[r->dtype == BSFA_DTYPE_F16][r->head_dim == 128][interleaved],
+                         a) == cudaSuccess)
+    return BSFA_OK;
+  cudaGetLastError();  // taken here, so that a later launch does not report it as its own
+  return BSFA_ERR_CUDA;
 }
 
 }  // namespace

@@ -298,12 +298,13 @@ __global__ void __launch_bounds__(32 * W, Shape<D, NT>::CTAS * decode16::WARPS /
   // The query row (of the CTA's) of this lane's column e of tile nt.
   auto col_row = [&](int nt, int e) { return nt * 8 + 2 * c + e; };
 
+  // The next kernel's blocks (the join's, after a cut) take their places and wait there
+  // for this kernel's end (1 x 16K, cut: 19.2 -> 18.5 us).
+  allow_next_kernel();
   if (a.cluster > 1) cluster_arrive();
+  wait_for_kernels_before();
   Piece piece;
   if (W == decode16::WARPS && a.split) {
-    // Lets the join's blocks take their places, where they wait for this kernel's end
-    // (1 x 16K, cut: 19.2 -> 18.5 us).
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0 && !a.join_by_segment) a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
     piece = cut<UNIT, SEGMENT_UNITS, MIN_UNITS, WARPS>(a, sh_cut);
   } else {  // one segment per cluster; u walks over it once
@@ -770,7 +771,8 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) decode16_join_kernel(const De
   __shared__ float4 sh_y[PARTS][LANES];
   __shared__ float2 sh_ml[JOIN_THREADS / 32];
   __shared__ float sh_w[MAX_PARTS];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  allow_next_kernel();
+  wait_for_kernels_before();
   const int4 job = a.joins[blockIdx.x];
   if (job.x < 0) return;
   const int b = job.x, kvh = job.y / a.row_tiles;
@@ -833,7 +835,8 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) decode16_join_kernel(const De
 template <int D, int ROWS, int PER>
 __global__ void __launch_bounds__(JOIN_THREADS) decode16_join_rows_kernel(const DecArgs a) {
   constexpr int E = D / 32;  // elements of a lane
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  allow_next_kernel();
+  wait_for_kernels_before();
   const int4 job = a.joins[blockIdx.x];
   if (job.x < 0) return;
   const int lane = threadIdx.x & 31;
@@ -916,6 +919,14 @@ bsfa_status prepare(int dev) {
   return v;
 }
 
+// For kernels that wait by themselves for those before them.
+inline cudaLaunchAttribute after_kernels() {
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+
 // The join of what `grid` CTAs left of `segments` segments, in `jobs` jobs.
 template <int D, int ROWS, int PER>
 bsfa_status launch_join(const DecArgs& a, long long segments, int grid, long long jobs,
@@ -924,14 +935,12 @@ bsfa_status launch_join(const DecArgs& a, long long segments, int grid, long lon
   const bool by_rows = grid * PER < JOIN_ROWS_PARTS * segments;
   const int rows = a.rows < ROWS ? a.rows : ROWS, per_block = by_rows ? JOIN_THREADS / 32 : 1;
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr{};
+  cudaLaunchAttribute attr = after_kernels();
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(jobs), (rows + per_block - 1) / per_block);
   cfg.blockDim = dim3(JOIN_THREADS);
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
   return status_of(by_rows ? cudaLaunchKernelEx(&cfg, decode16_join_rows_kernel<D, ROWS, PER>, a)
                            : cudaLaunchKernelEx(&cfg, decode16_join_kernel<D, ROWS, PER>, a));
 }
@@ -942,17 +951,18 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
   const bsfa_status v = prepare<D, NT, F16, W>(dev);
   if (v != BSFA_OK) return v;
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr{};
+  cudaLaunchAttribute attrs[2] = {after_kernels(), {}};
   cfg.stream = stream;
-  cfg.attrs = &attr;
+  cfg.attrs = attrs;
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(32 * W);
   cfg.dynamicSmemBytes = smem_bytes<D, NT, W>(pl.cluster > 1);
   if (!pl.split) {
     cfg.gridDim = dim3(static_cast<unsigned>(pl.segments * pl.cluster));
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = pl.cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = pl.cluster;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
     return status_of(cudaLaunchKernelEx(&cfg, decode16_kernel<D, NT, F16, W>, args));
   }
   if constexpr (W == WARPS) {  // other CTAs never cut
@@ -963,7 +973,6 @@ bsfa_status launch(const DecArgs& args, const Plan& pl, int sms, int dev, cudaSt
     DecArgs a = args;
     a.join_by_segment = pl.segments <= grid;
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.numAttrs = 0;
     const bsfa_status first = status_of(cudaLaunchKernelEx(&cfg, decode16_kernel<D, NT, F16, W>, a));
     if (first != BSFA_OK) return first;
     return launch_join<D, 8 * NT, 1>(a, pl.segments, grid,

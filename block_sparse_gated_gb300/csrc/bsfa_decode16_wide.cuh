@@ -222,12 +222,13 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     tmem_alloc(&c->tmem_base, 512);
     tmem_relinquish();
   }
+  allow_next_kernel();
+  wait_for_kernels_before();
   const Piece piece = cut<WIDE_UNIT, WIDE_SEGMENT_UNITS, WIDE_MIN_UNITS, WIDE_THREADS / 32>(a, c->cut);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c->tmem_base;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0) {
     // ------------------------------------------------------------ copies
@@ -647,9 +648,16 @@ bsfa_status run_wide(const CUtensorMap& tmK, const CUtensorMap& tmV, const DecAr
   int grid = sms < MAX_SMS ? sms : MAX_SMS;
   const long long most = (pl.all_units + WIDE_MIN_UNITS - 1) / WIDE_MIN_UNITS;
   if (most < grid) grid = static_cast<int>(most);
-  decode16_wide_kernel<D, F16>
-      <<<static_cast<unsigned>(grid), WIDE_THREADS, WideLayout<D>::BYTES, stream>>>(tmK, tmV, a);
-  const bsfa_status first = status_of(cudaGetLastError());
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr = after_kernels();
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(WIDE_THREADS);
+  cfg.dynamicSmemBytes = WideLayout<D>::BYTES;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const bsfa_status first =
+      status_of(cudaLaunchKernelEx(&cfg, decode16_wide_kernel<D, F16>, tmK, tmV, a));
   if (first != BSFA_OK) return first;
   return launch_join<D, TILE, WIDE_PARTS>(a, pl.segments, grid, pl.segments, stream);
 }

@@ -772,6 +772,75 @@ print("same")
     assert r.stdout.strip() == "same", r.stdout + r.stderr
 
 
+def test_captures_with_copies_forks_and_joins(cuda_device):
+    """A decode step whose calls follow copies, each other, other streams' calls and other
+    kernels in one graph, replayed back to back on changing data: each sees all before it."""
+    b = _bsfa()
+    Hq, Hkv, d, page, L = 8, 2, 64, 32, 600
+    cache = b.cache16_empty(2 * 32, Hkv, page, d, device=cuda_device)
+    other = b.cache16_empty(2 * 32, Hkv, page, d, device=cuda_device)
+    table = torch.randperm(64, generator=torch.Generator().manual_seed(1)).to(
+        device=cuda_device, dtype=torch.int32).view(2, 32)
+    rope = b.Rope(cu.inv_freq(32).to(cuda_device))
+    src = [cu.rand((3, 2, h, 1, d), BF, s, cuda_device) for s, h in ((1, Hq), (2, Hkv), (3, Hkv))]
+    seen = [cu.rand((2, Hkv, L, d), BF, s, cuda_device) for s in (4, 5)]
+    q, k, v = (torch.zeros_like(x[0]) for x in src)
+    n32, step = _i32([L, L - 70], cuda_device), torch.zeros(1, dtype=torch.int64, device=cuda_device)
+    outs = [torch.zeros(4, 2, Hq, 1, d, dtype=BF, device=cuda_device) for _ in range(2)]
+    side = torch.cuda.Stream()
+
+    def body(out):
+        for x, y in zip((q, k, v), src):
+            x.copy_(y.index_select(0, step % 3)[0])
+        # A fork: the second cache on a side stream, which a copy and the first cache's call feed.
+        q1 = b.cache16_write(cache, k, v, table, q=q, rope=rope, start=n32)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            q2 = b.cache16_write(other, k, v, table, q=q, rope=rope, start=n32)
+        n32.add_(1)
+        out[0].copy_(b.decode16(q1, cache, table, n32)["out"])
+        torch.cuda.current_stream().wait_stream(side)  # a join: two calls before the next
+        back, _ = b.rotary(rope, q2, start=n32 - 1, inverse=True)
+        turned, _ = b.rotary(rope, back, start=n32 - 1)
+        b.decode16(turned, other, table, n32, max_seqlen=700, out=out[1])
+        wide = turned.repeat(1, 5, 1, 1)
+        out[2:4].copy_(b.decode16(wide, other, table, n32)["out"][:, :2 * Hq].view(2, 2, Hq, 1, d)
+                       .transpose(0, 1))
+        out.mul_(0.5)
+        step.add_(1)
+
+    def reset():
+        for c in (cache, other):
+            c.k.zero_(), c.v.zero_()
+            b.cache16_write(c, *seen, table, rope=rope)
+        n32.copy_(_i32([L, L - 70], cuda_device))
+        step.zero_()
+
+    reset()
+    want = []
+    for _ in range(9):
+        body(outs[0])
+        torch.cuda.synchronize()
+        want.append(outs[0].clone())
+    reset()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        body(outs[1])
+    reset()
+    got = []
+    for _ in range(9):  # no waits between the replays
+        g.replay()
+        got.append(outs[1].clone())
+    torch.cuda.synchronize()
+    for x, y in zip(want, got):
+        assert torch.equal(x, y) and bool(x.any())
+    reset()
+    for i in range(9):  # nor between calls
+        body(outs[0])
+        assert torch.equal(outs[0], want[i])
+
+
 def test_calls_from_several_threads(cuda_device):
     """Each thread on a stream of its own, the same caches read by all."""
     from concurrent.futures import ThreadPoolExecutor
