@@ -144,7 +144,8 @@ __device__ __forceinline__ void turn(float f, long long position, float& c, floa
 template <int D, bool F16, bool INTERLEAVED>
 __global__ void __launch_bounds__(THREADS) rows16_kernel(const __grid_constant__ RowsArgs a) {
   constexpr int GROUPS = D / CHUNK;  // threads of a row
-  allow_next_kernel();
+  // (Without allow_next_kernel(): blocks of the next call that take their places early are
+  // spread unevenly over the SMs, 14.0 -> 15.7 us for the packed rows of a chunked prompt.)
   wait_for_kernels_before();
   const int g = threadIdx.x & (GROUPS - 1);
   const long long t =

@@ -752,6 +752,11 @@ __global__ void __launch_bounds__(32 * W, Shape<D, NT>::CTAS * decode16::WARPS /
   }
 }
 
+// Whether the kernel after a join may be placed early (1 x 128K: 82.8 -> 82.0 us; at d =
+// 64, where an SM holds four of its CTAs, they are spread unevenly: 47.0 -> 50.4).
+template <int D>
+constexpr bool EARLY_AFTER_JOIN = D == 128;
+
 // Place of part p of a segment that began in CTA `first`.
 template <int PER>
 __device__ __forceinline__ long long slot_of(int first, int p) {
@@ -771,7 +776,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) decode16_join_kernel(const De
   __shared__ float4 sh_y[PARTS][LANES];
   __shared__ float2 sh_ml[JOIN_THREADS / 32];
   __shared__ float sh_w[MAX_PARTS];
-  allow_next_kernel();
+  if constexpr (EARLY_AFTER_JOIN<D>) allow_next_kernel();
   wait_for_kernels_before();
   const int4 job = a.joins[blockIdx.x];
   if (job.x < 0) return;
@@ -835,7 +840,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) decode16_join_kernel(const De
 template <int D, int ROWS, int PER>
 __global__ void __launch_bounds__(JOIN_THREADS) decode16_join_rows_kernel(const DecArgs a) {
   constexpr int E = D / 32;  // elements of a lane
-  allow_next_kernel();
+  if constexpr (EARLY_AFTER_JOIN<D>) allow_next_kernel();
   wait_for_kernels_before();
   const int4 job = a.joins[blockIdx.x];
   if (job.x < 0) return;
