@@ -183,6 +183,7 @@ bsfa_status bsfa_decode16(const bsfa_cache16* cache, const bsfa_decode4_params* 
   a.tiles_per_page = cache->page_size / TOK;
   a.q = static_cast<const uint16_t*>(p->q);
   a.o = static_cast<uint16_t*>(p->o);
+  a.in_place = p->o == p->q;
   a.seqlens = p->seqlens;
   a.batch = p->batch;
   a.heads_kv = cache->num_heads_kv;

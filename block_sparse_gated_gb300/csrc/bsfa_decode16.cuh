@@ -138,6 +138,7 @@ struct DecArgs {
   float2* part_ml;  // [grid][2][rows of a CTA]
   unsigned* err;    // the device error word (wide calls)
   int box;          // tokens of a copy (wide calls)
+  int in_place;     // o is q
   int4* joins;      // [jobs]: {sequence, kvh * row_tiles + row tile, first, last CTA}, or x < 0
 };
 

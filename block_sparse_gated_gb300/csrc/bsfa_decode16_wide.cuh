@@ -577,8 +577,16 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
           load(tO, own, carried, any, o);
           load(tO - 128, first, tiles0 > WIDE_RUN, tiles0 > 0, o0);
         };
-        // Whether all is finite comes before the first store: the output may be the queries
-        // themselves, which are needed once more where it is not.
+        auto store = [&](int x, const float (&o)[32], const float (&o0)[32]) {
+#pragma unroll
+          for (int e = 0; e < 32 && real; e += 4)
+            store_row4(a, w.b, w.kvh, r, 32 * x + e, -both, sum,
+                       make_float4(fmaf(o[e], f, o0[e] * f0), fmaf(o[e + 1], f, o0[e + 1] * f0),
+                                   fmaf(o[e + 2], f, o0[e + 2] * f0),
+                                   fmaf(o[e + 3], f, o0[e + 3] * f0)));
+        };
+        // Where the output is the queries themselves, which are needed once more for sums
+        // that are not finite, nothing is stored before that is known.
 #pragma unroll 1
         for (int x = 0; x < D / 32; ++x) {
           float o[32], o0[32];
@@ -586,18 +594,16 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             sums_finite = sums_finite && fabsf(fmaf(o[e], f, o0[e] * f0)) < INFINITY;
+          if (!a.in_place) store(x, o, o0);
         }
         if (!__any_sync(0xffffffffu, real && !sums_finite && sum < INFINITY)) {
+          if (a.in_place) {
 #pragma unroll 1
-          for (int x = 0; x < D / 32; ++x) {
-            float o[32], o0[32];
-            parts(x, o, o0);
-#pragma unroll
-            for (int e = 0; e < 32 && real; e += 4)
-              store_row4(a, w.b, w.kvh, r, 32 * x + e, -both, sum,
-                         make_float4(fmaf(o[e], f, o0[e] * f0), fmaf(o[e + 1], f, o0[e + 1] * f0),
-                                     fmaf(o[e + 2], f, o0[e + 2] * f0),
-                                     fmaf(o[e + 3], f, o0[e + 3] * f0)));
+            for (int x = 0; x < D / 32; ++x) {
+              float o[32], o0[32];
+              parts(x, o, o0);
+              store(x, o, o0);
+            }
           }
         } else {
           // As for parts that go to the join: into memory, and what is not finite anew.
