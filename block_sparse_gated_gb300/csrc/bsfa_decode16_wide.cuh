@@ -577,32 +577,35 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
           load(tO, own, carried, any, o);
           load(tO - 128, first, tiles0 > WIDE_RUN, tiles0 > 0, o0);
         };
-        auto store = [&](int x, const float (&o)[32], const float (&o0)[32]) {
+        auto joined = [&](int x, float (&y)[32]) {
+          float o0[32];
+          parts(x, y, o0);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = fmaf(y[e], f, o0[e] * f0);
+        };
+        auto store = [&](int x, const float (&y)[32]) {
 #pragma unroll
           for (int e = 0; e < 32 && real; e += 4)
             store_row4(a, w.b, w.kvh, r, 32 * x + e, -both, sum,
-                       make_float4(fmaf(o[e], f, o0[e] * f0), fmaf(o[e + 1], f, o0[e + 1] * f0),
-                                   fmaf(o[e + 2], f, o0[e + 2] * f0),
-                                   fmaf(o[e + 3], f, o0[e + 3] * f0)));
+                       make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]));
         };
         // Where the output is the queries themselves, which are needed once more for sums
         // that are not finite, nothing is stored before that is known.
 #pragma unroll 1
         for (int x = 0; x < D / 32; ++x) {
-          float o[32], o0[32];
-          parts(x, o, o0);
+          float y[32];
+          joined(x, y);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            sums_finite = sums_finite && fabsf(fmaf(o[e], f, o0[e] * f0)) < INFINITY;
-          if (!a.in_place) store(x, o, o0);
+          for (int e = 0; e < 32; ++e) sums_finite = sums_finite && fabsf(y[e]) < INFINITY;
+          if (!a.in_place) store(x, y);
         }
         if (!__any_sync(0xffffffffu, real && !sums_finite && sum < INFINITY)) {
           if (a.in_place) {
 #pragma unroll 1
             for (int x = 0; x < D / 32; ++x) {
-              float o[32], o0[32];
-              parts(x, o, o0);
-              store(x, o, o0);
+              float y[32];
+              joined(x, y);
+              store(x, y);
             }
           }
         } else {
