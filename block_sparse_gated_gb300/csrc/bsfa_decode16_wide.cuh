@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(&c->q_full, 256);
+    mbar_init(&c->q_full, 128);
     mbar_init(&c->q_empty, 1);
     for (int i = 0; i < ST; ++i) {
       mbar_init(&c->k_full[i], 1);
@@ -344,7 +344,15 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     const float sc = a.sigma_log2;
     uint32_t sc_n = 0, pv_n = 0;  // tiles of this warpgroup, its products
     uint32_t uc = 0, xc = 0;      // queries so far, segments within this CTA
+    uint32_t read = 0;            // ... and those whose first part is known to have been read
     bool ok = true;
+    // The second warpgroup may have yet to read the first one's O and part of the segment
+    // before, which are written from here on.
+    auto part_is_free = [&]() -> bool {
+      if (wg != 0 || read == xc) return true;
+      read = xc;
+      return wait_all(&c->x_empty, (xc - 1) & 1, abort, a.err, ERR_WAIT_WG);
+    };
     WideWork w;
     for (WideWalk walk(a, piece); ok && walk.next(w);) {
       const int r = w.r0 + row;
@@ -356,31 +364,26 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
       if (w.began && threadIdx.x == 128)
         a.joins[w.b * a.heads_kv * a.row_tiles + w.seg] =
             make_int4(w.whole ? -1 : w.b, w.seg, static_cast<int>(blockIdx.x), w.last_cta);
-      if (w.n > 0) {
-        // ---- this thread's half of a query row, swizzled as TMA would
+      if (w.n > 0 && wg == 0) {
+        // ---- this thread's query row, swizzled as TMA would (by the first warpgroup: the
+        // second may still be joining the segment before)
         const int h = w.kvh * a.group + (r - i * a.group);
         const uint4* src = reinterpret_cast<const uint4*>(a.q + w.b * a.q_s[0] + h * a.q_s[1] +
-                                                          i * a.q_s[2]) + wg * (D / 16);
-        uint4 y[D / 16];
+                                                          i * a.q_s[2]);
+        uint4 y[D / 8];
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) y[x] = real ? __ldg(src + x) : make_uint4(0u, 0u, 0u, 0u);
+        for (int x = 0; x < D / 8; ++x) y[x] = real ? __ldg(src + x) : make_uint4(0u, 0u, 0u, 0u);
         if (uc > 0 &&
             !(ok = wait_all(&c->q_empty, (uc - 1) & 1, abort, a.err, ERR_WAIT_Q_EMPTY)))
           break;
         ++uc;
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          const int at16 = wg * (D / 16) + x;
-          *reinterpret_cast<uint4*>(sQ + (at16 >> 3) * HB + row * 128 +
-                                    (((at16 & 7) ^ (row & 7)) << 4)) = y[x];
-        }
+        for (int x = 0; x < D / 8; ++x)
+          *reinterpret_cast<uint4*>(sQ + (x >> 3) * HB + row * 128 +
+                                    (((x & 7) ^ (row & 7)) << 4)) = y[x];
         fence_proxy_async_shared();
         mbar_arrive(&c->q_full);
       }
-      // The other warpgroup may have yet to read this one's part of the segment before.
-      if (wg == 0 && xc > 0 &&
-          !(ok = wait_all(&c->x_empty, (xc - 1) & 1, abort, a.err, ERR_WAIT_WG)))
-        break;
       float z = NO_SCORE, l = 0.f;        // of the run
       float z_c = NO_SCORE, l_c = 0.f;    // of the runs before it
       bool carried = false;
@@ -522,11 +525,12 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         l += l0 + l1;
         tmem_wait_st();
         tc_fence_before();
+        if (!(ok = part_is_free())) break;
         mbar_arrive(&c->p_full[wg]);
         ++pv_n;
         ++in_run;
       }
-      if (!ok) break;
+      if (!ok || !(ok = part_is_free())) break;
       if (!w.whole || carried) {
         if (!(ok = flush(in_run > 0))) break;
         if (real && !finite && l_c < INFINITY)
