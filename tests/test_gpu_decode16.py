@@ -794,12 +794,15 @@ def test_captures_with_copies_forks_and_joins(cuda_device):
             x.copy_(y.index_select(0, step % 3)[0])
         # A fork: the second cache on a side stream, which a copy and the first cache's call feed.
         q1 = b.cache16_write(cache, k, v, table, q=q, rope=rope, start=n32)
+        at = n32.clone()  # the side stream's own: n32 moves on meanwhile
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
-            q2 = b.cache16_write(other, k, v, table, q=q, rope=rope, start=n32)
+            q2 = b.cache16_write(other, k, v, table, q=q, rope=rope, start=at)
+        at.record_stream(side)
         n32.add_(1)
         out[0].copy_(b.decode16(q1, cache, table, n32)["out"])
         torch.cuda.current_stream().wait_stream(side)  # a join: two calls before the next
+        q2.record_stream(torch.cuda.current_stream())
         back, _ = b.rotary(rope, q2, start=n32 - 1, inverse=True)
         turned, _ = b.rotary(rope, back, start=n32 - 1)
         b.decode16(turned, other, table, n32, max_seqlen=700, out=out[1])
