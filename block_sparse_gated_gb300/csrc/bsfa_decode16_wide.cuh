@@ -21,10 +21,10 @@
 // Bound.  At 128 rows a tile's products take 1900 cycles and its 64 KB (d = 128) 2790 at
 // a copy's rate; between them stands the chain of a warpgroup (scores, weights, O), two
 // of which overlap.  16 ragged sequences to 32K on four heads (570 MB) take 103 us with
-// 64 rows and 111 with 128, 5.5 and 5.2 TB/s (by row tiles of 32 on mma.sync 173 and
+// 64 rows and 109 with 128, 5.5 and 5.2 TB/s (by row tiles of 32 on mma.sync 173 and
 // 320); d = 64, 128 rows, 70 us, bound by the weights' arithmetic.  512 new tokens of
-// four heads over 16K on eight KV heads: 159 us, 850 TFLOP/s, and half as
-// much again for the weights' second numbers.
+// four heads over 16K on eight KV heads: 156 us, 865 TFLOP/s, and half as much again
+// for the weights' second numbers.
 //
 // TMEM: scores at columns 0 and 128, O at 256 and 384.  The weights of 32 keys take
 // the columns of their scores: 16 for the first numbers, 16 for the second.
@@ -37,8 +37,8 @@ namespace bsfa {
 namespace decode16 {
 
 constexpr int WIDE_UNIT = TILE;        // tokens of a work unit
-// A segment's fixed cost, in units (100 ragged sequences to 1K, 64 rows: 89.9 us; at 3
-// 91.1, at 10 95.7).
+// A segment's fixed cost, in units (100 ragged sequences to 1K, 64 rows: 89.9 us at 6,
+// 91.1 at 3, 95.7 at 10, before segments overlapped).
 constexpr int WIDE_SEGMENT_UNITS = 6;
 constexpr int WIDE_MIN_UNITS = 1;  // shortest piece of the line worth a CTA (1 x 1K with 64
                                    // rows: 13.0 us; at 4 16.1)
