@@ -649,6 +649,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 template <int D, bool F16>
 bsfa_status run_wide(const CUtensorMap& tmK, const CUtensorMap& tmV, const DecArgs& a,
                      const Plan& pl, int sms, int dev, cudaStream_t stream) {
+  static_assert(WIDE_PARTS * MAX_SMS <= MAX_PARTS, "the join's weights");
   static std::atomic<uint64_t> ready{0};
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (!(ready.load(std::memory_order_relaxed) & bit)) {

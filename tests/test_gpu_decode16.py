@@ -586,6 +586,22 @@ def test_many_query_rows_over_long_and_many_sequences(cuda_device, d, dtype, len
                         lens[i:i + 1], dtype, d)
 
 
+def test_many_query_rows_of_the_largest_batch(cuda_device):
+    """4096 sequences of 0 to 3 tokens and one of 700, queries inside a larger tensor."""
+    b = _bsfa()
+    lens = [int(x) for x in np.random.default_rng(5).integers(0, 4, 4096)]
+    lens[2222] = 700
+    cache, table, rows = cu.random_cache(b, lens, 16, 1, 64, BF, 2, cuda_device)
+    q = _queries(4096, 42, 1, 80, BF, 2, cuda_device)[:, 1:41, :, 8:72]
+    res = b.decode16(q, cache, table, _i32(lens, cuda_device), return_lse=True)
+    lse = res["lse"].view(40, 4096, 1)
+    for i in [0, 1, 2, 2221, 2222, 2223, 4094, 4095] + list(range(100, 4000, 300)):
+        cu.check_decode({"out": res["out"][i:i + 1], "lse": lse[:, i]}, q[i:i + 1], rows[i:i + 1],
+                        lens[i:i + 1], BF, 64)
+    empty = torch.tensor([x == 0 for x in lens], device=cuda_device)
+    assert not res["out"][empty].any() and bool(res["out"][~empty].any(-1).all())
+
+
 @pytest.mark.parametrize("causal", [True, False])
 def test_many_queries_longer_than_the_cache(cuda_device, causal):
     """Tiles of rows of which some or all see nothing."""
