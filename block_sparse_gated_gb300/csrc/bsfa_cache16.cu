@@ -110,7 +110,7 @@ __device__ __forceinline__ uint64_t turns_per_position(float f) {
   if (down >= 32) return down < 96 ? high >> (down - 32) : 0;
   const uint64_t lowest = low & 0xffffffffu;
   if (down >= 0) return high << (32 - down) | lowest >> down;
-  return down > -32 ? (high << 32 | lowest) << -down : 0;
+  return down > -64 ? (high << 32 | lowest) << -down : 0;  // beyond: whole turns only
 }
 
 // cos and sin of position * f.
