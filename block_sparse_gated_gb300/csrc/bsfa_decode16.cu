@@ -199,6 +199,10 @@ bsfa_status bsfa_decode16(const bsfa_cache16* cache, const bsfa_decode4_params* 
   const float sigma =
       p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt((float)cache->head_dim);
   a.sigma_log2 = sigma * 1.4426950408889634f;
+  int log2_len = 0;
+  while ((1LL << log2_len) < p->max_seqlen) ++log2_len;
+  a.shift = -(HEADROOM + static_cast<float>(log2_len));
+  a.most = a.shift + HEADROOM;
   a.lse = p->lse;
   a.lse_pitch = static_cast<long long>(p->batch) * p->q_len;
   uint8_t* ws = static_cast<uint8_t*>(p->workspace);

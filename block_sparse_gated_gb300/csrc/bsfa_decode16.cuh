@@ -4,9 +4,11 @@
 // Mathematics.  S^T = K Q^T and O^T = V^T P^T are tensor-core products of 16-bit
 // factors with fp32 sums.  The softmax is streamed: a weight is p = 2^(y + z) with y
 // the score in log2 units and z the row's offset, which falls, with O and the sum l
-// rescaled, only when some weight would pass 2^(SHIFT + HEADROOM); the factor
-// 2^SHIFT that p carries cancels in O / l and keeps small weights out of fp16's
-// subnormals.
+// rescaled, only when some weight would pass 2^(shift + HEADROOM).  The factor 2^shift
+// that p carries cancels in O / l.  In fp16 it keeps small weights out of the
+// subnormals: 2^10, with values up to 2^16 far from fp32's end.  bf16 values reach to
+// that end: there it is 2^-(HEADROOM + log2 of the lengths' bound), so that the weights
+// of all tokens add up to one at most and O stays within the largest value.
 //
 // Layout.  Cached tokens are the rows (M) of the products and query rows
 // (Hq/Hkv heads times q_len tokens) the columns (N = 8 per tile), so that a decode
@@ -48,8 +50,8 @@ constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
 constexpr int TOK = 16;             // tokens of a warp's tile
 constexpr int UNIT = TOK * WARPS;   // tokens of a work unit
-constexpr float HEADROOM = 5.f;     // log2 a weight may pass 2^SHIFT by
-constexpr float SHIFT = 10.f;       // log2 of the factor that a weight carries
+constexpr float HEADROOM = 5.f;     // log2 a weight may pass 2^shift by
+constexpr float SHIFT_F16 = 10.f;   // log2 of the factor that a weight carries in fp16
 constexpr float NO_SCORE = 3e38f;   // a row's offset before its first score
 constexpr int MIN_UNITS = 4;        // shortest piece of the line worth a CTA
 // A segment's fixed cost, in units (128 ragged sequences to 2K, cut, and 1 x 128K: 90.2
@@ -132,6 +134,7 @@ struct DecArgs {
   int batch, heads_kv, group, q_len, rows, row_tiles, max_len;
   int causal, f16, split, cluster, join_by_segment;
   float sigma_log2;
+  float shift, most;  // log2 of the factor that a bf16 weight carries, and of the largest one
   float* lse;
   long long lse_pitch;
   float* part_o;    // [grid][2][rows of a CTA][d]
@@ -141,6 +144,17 @@ struct DecArgs {
   int in_place;     // o is q
   int4* joins;      // [jobs]: {sequence, kvh * row_tiles + row tile, first, last CTA}, or x < 0
 };
+
+// log2 of the factor that a weight carries, and of the largest weight before the
+// offset falls.
+template <bool F16>
+__device__ __forceinline__ float shift_of(const DecArgs& a) {
+  return F16 ? SHIFT_F16 : a.shift;
+}
+template <bool F16>
+__device__ __forceinline__ float most_of(const DecArgs& a) {
+  return F16 ? SHIFT_F16 + HEADROOM : a.most;
+}
 
 // The sequence length that the call sees.
 __device__ __forceinline__ int clamp_len(const DecArgs& a, int b) {
@@ -476,7 +490,7 @@ __global__ void __launch_bounds__(32 * W, Shape<D, NT>::CTAS * decode16::WARPS /
           mma_16816<F16>(SUMS == 2 && (j & 1) ? s2[SUMS == 2 ? nt : 0] : s[nt], k, q2.x, q2.y);
         }
       }
-      // ---- weights; the offset falls where one would pass 2^(SHIFT + HEADROOM)
+      // ---- weights; the offset falls where one would pass 2^(shift + HEADROOM)
       float y[NT][4];
       auto hidden = [&](int nt, int e) {
         return tok0 + g + (e & 2) * 4 >= sh_lim[col_row(nt, e & 1)];
@@ -495,7 +509,7 @@ __global__ void __launch_bounds__(32 * W, Shape<D, NT>::CTAS * decode16::WARPS /
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           y[nt][e] = s[nt][e] + zn[nt][e & 1];
-          over |= y[nt][e] > SHIFT + HEADROOM;
+          over |= y[nt][e] > most_of<F16>(a);
         }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -506,7 +520,7 @@ __global__ void __launch_bounds__(32 * W, Shape<D, NT>::CTAS * decode16::WARPS /
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-            const float z = fminf(zn[nt][e], SHIFT - m);
+            const float z = fminf(zn[nt][e], shift_of<F16>(a) - m);
             const float f = ex2_approx(z - zn[nt][e]);
             zn[nt][e] = z;
             sum[nt][e] *= f;

@@ -463,9 +463,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
           }
         }
         m *= sc;
-        const bool over = m + z > SHIFT + HEADROOM;
+        const bool over = m + z > most_of<F16>(a);
         if (__any_sync(0xffffffffu, over)) {
-          const float z1 = over ? fminf(z, SHIFT - m) : z;
+          const float z1 = over ? fminf(z, shift_of<F16>(a) - m) : z;
           const float f = ex2_approx(z1 - z);
           z = z1;
           l *= f;

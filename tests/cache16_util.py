@@ -125,3 +125,26 @@ def check_decode(res, q, rows, lens, dtype, d, *, sigma=None, causal=True):
             assert (np.isneginf(y) == ~seen).all()
             assert (np.abs(y[seen] - lse[seen]) <= tol_lse[seen]).all(), f"sequence {b}: lse"
     return worst
+
+
+def wide_pieces(lens, max_len, *, heads_kv=1, row_tiles=1, sms=152):
+    """How a call of more than 32 query rows per KV head is cut over the CTAs: (units per CTA,
+    [(sequence, KV head and row tile, first CTA, last CTA) per segment]).  A segment is its tiles
+    of 128 tokens and six units beside them."""
+    def units(n):
+        return 6 + math.ceil(max(0, min(n, max_len)) / 128)
+    per_b = heads_kv * row_tiles
+    total = per_b * sum(units(n) for n in lens)
+    grid = min(sms, len(lens) * per_b * units(max_len))
+    per_cta = max(1, math.ceil(total / grid))
+    segments, at = [], 0
+    for b, n in enumerate(lens):
+        for s in range(per_b):
+            segments.append((b, s, at // per_cta, (at + units(n) - 1) // per_cta))
+            at += units(n)
+    return per_cta, segments
+
+
+def shared(table, batch):
+    """The table of ``batch`` sequences that take turns in the pages of a few."""
+    return table.repeat(math.ceil(batch / table.shape[0]), 1)[:batch].contiguous()
