@@ -142,7 +142,9 @@ struct DecArgs {
   unsigned* err;    // the device error word (wide calls)
   int box;          // tokens of a copy (wide calls)
   int in_place;     // o is q
-  int4* joins;      // [jobs]: {sequence, kvh * row_tiles + row tile, first, last CTA}, or x < 0
+  // [jobs]: {sequence, kvh * row_tiles + row tile, first, last CTA}; x < 0: none, w < 0: the
+  // segment lies within its first CTA.
+  int4* joins;
 };
 
 // log2 of the factor that a weight carries, and of the largest weight before the
@@ -794,7 +796,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) decode16_join_kernel(const De
   if constexpr (EARLY_AFTER_JOIN<D>) allow_next_kernel();
   wait_for_kernels_before();
   const int4 job = a.joins[blockIdx.x];
-  if (job.x < 0) return;
+  if (job.x < 0 || job.w < 0) return;
   const int b = job.x, kvh = job.y / a.row_tiles;
   const int r = blockIdx.y, row = (job.y - kvh * a.row_tiles) * ROWS + r;
   if (row >= a.rows) return;
@@ -858,7 +860,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) decode16_join_rows_kernel(const 
   if constexpr (EARLY_AFTER_JOIN<D>) allow_next_kernel();
   wait_for_kernels_before();
   const int4 job = a.joins[blockIdx.x];
-  if (job.x < 0) return;
+  if (job.x < 0 || job.w < 0) return;
   const int lane = threadIdx.x & 31;
   const int r = blockIdx.y * (JOIN_THREADS / 32) + (threadIdx.x >> 5);
   const int b = job.x, kvh = job.y / a.row_tiles;

@@ -16,6 +16,7 @@
 //   warp 0      copies K and V tiles through TMA, one box per lane: a box lies within
 //               a page.
 //   warp 1      issues the products, owns TMEM.
+//   warp 2      writes what the join is to do.
 //   warps 4-7   softmax of the even tiles, a thread to a row.
 //   warps 8-11  ... of the odd ones.
 // Bound.  At 128 rows a tile's products take 1900 cycles and its 64 KB (d = 128) 2790 at
@@ -336,6 +337,15 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     if (elect_one()) umma_commit(&c->drain);
     __syncwarp();
     drain_wait(&c->drain, 0);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ the join's table
+    // Of every segment that begins in this piece, by a warp that waits for nothing: the
+    // join follows it even where a wait of the others has run out and they have left.
+    WideWork w;
+    for (WideWalk walk(a, piece); walk.next(w);)
+      if (w.began && lane == 0)
+        a.joins[w.b * a.heads_kv * a.row_tiles + w.seg] =
+            make_int4(w.b, w.seg, static_cast<int>(blockIdx.x), w.whole ? -1 : w.last_cta);
   } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax
     const int wg = (warp - 4) >> 2, wq = warp & 3, row = wq * 32 + lane;
@@ -361,9 +371,6 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
       const int lim = !real ? 0 : a.causal ? w.len - a.q_len + i + 1 : w.len;
       const int slot = WIDE_PARTS * (2 * static_cast<int>(blockIdx.x) + (w.began ? 1 : 0)) + wg;
       const long long at = static_cast<long long>(slot) * TILE + row;
-      if (w.began && threadIdx.x == 128)
-        a.joins[w.b * a.heads_kv * a.row_tiles + w.seg] =
-            make_int4(w.whole ? -1 : w.b, w.seg, static_cast<int>(blockIdx.x), w.last_cta);
       if (w.n > 0 && wg == 0) {
         // ---- this thread's query row, swizzled as TMA would (by the first warpgroup: the
         // second may still be joining the segment before)
