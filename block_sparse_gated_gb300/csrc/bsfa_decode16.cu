@@ -100,18 +100,23 @@ bool map_pool(CUtensorMap* m, const bsfa_cache16* c, const void* pool, const int
 }
 
 struct Carve {
-  size_t part_o, part_ml, joins, bytes;
+  size_t part_o, part_ml, joins, anew, kept, bytes;
 };
 
-Carve carve(const Plan& pl, int d) {
+Carve carve(const Plan& pl, const bsfa_cache16* cache, const bsfa_decode4_params* p) {
   Carve c{};
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const int d = cache->head_dim;
   const size_t grid = pl.split ? static_cast<size_t>(pl.max_grid) : 0;
   const size_t rows = 2 * grid * 8 * pl.nt * (pl.wide ? WIDE_PARTS : 1);
   c.part_o = 0;
   c.part_ml = up(c.part_o + rows * d * sizeof(float));
   c.joins = up(c.part_ml + rows * sizeof(float2));
-  c.bytes = up(c.joins + (pl.wide ? pl.segments : grid) * sizeof(int4));
+  c.anew = up(c.joins + (pl.wide ? pl.segments : grid) * sizeof(int4));
+  c.kept = up(c.anew + (pl.wide ? pl.segments * 4 * sizeof(uint32_t) : 0));
+  // (Of every wide call: whether its output is its queries is not known to all who ask.)
+  const size_t queries = static_cast<size_t>(p->batch) * p->num_heads_q * p->q_len;
+  c.bytes = c.kept + (pl.wide ? up(queries * d * sizeof(uint16_t)) : 0);
   return c;
 }
 
@@ -144,7 +149,7 @@ extern "C" {
 
 size_t bsfa_decode16_workspace_size(const bsfa_cache16* cache, const bsfa_decode4_params* p) {
   if (validate_sizes(cache, p) != BSFA_OK) return 0;
-  return carve(plan_of(cache, p), cache->head_dim).bytes;
+  return carve(plan_of(cache, p), cache, p).bytes;
 }
 
 bsfa_status bsfa_decode16(const bsfa_cache16* cache, const bsfa_decode4_params* p,
@@ -159,7 +164,7 @@ bsfa_status bsfa_decode16(const bsfa_cache16* cache, const bsfa_decode4_params* 
   if (!rows_aligned(p->q, p->q_stride, extent) || !rows_aligned(p->o, p->o_stride, extent))
     return BSFA_ERR_UNSUPPORTED;
   const Plan pl = plan_of(cache, p);
-  const Carve cv = carve(pl, cache->head_dim);
+  const Carve cv = carve(pl, cache, p);
   if (pl.split && (p->workspace == nullptr || (reinterpret_cast<uintptr_t>(p->workspace) & 255u) ||
                    p->workspace_bytes < cv.bytes))
     return BSFA_ERR_WORKSPACE;
@@ -209,6 +214,8 @@ bsfa_status bsfa_decode16(const bsfa_cache16* cache, const bsfa_decode4_params* 
   a.part_o = reinterpret_cast<float*>(ws + cv.part_o);
   a.part_ml = reinterpret_cast<float2*>(ws + cv.part_ml);
   a.joins = reinterpret_cast<int4*>(ws + cv.joins);
+  a.anew = reinterpret_cast<uint32_t*>(ws + cv.anew);
+  a.kept = reinterpret_cast<uint16_t*>(ws + cv.kept);
 
   int dev = 0, sms = 0;
   v = status_of(cudaGetDevice(&dev));

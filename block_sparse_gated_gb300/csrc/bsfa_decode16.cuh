@@ -145,6 +145,11 @@ struct DecArgs {
   // [jobs]: {sequence, kvh * row_tiles + row tile, first, last CTA}; x < 0: none, w < 0: the
   // segment lies within its first CTA.
   int4* joins;
+  // Wide calls, of segments that lie within a CTA: [segments][4], a bit for each row that is
+  // formed anew (form_anew), and where the output is the queries [batch][KV heads][rows][d],
+  // the queries of such rows.
+  uint32_t* anew;
+  uint16_t* kept;
 };
 
 // log2 of the factor that a weight carries, and of the largest weight before the
@@ -226,19 +231,31 @@ __device__ __forceinline__ Piece cut(const DecArgs& a, int* sh) {
   return p;
 }
 
+// An output row: `row` is the query row within the KV head's group.
+__device__ __forceinline__ uint16_t* output_row(const DecArgs& a, int b, int kvh, int row) {
+  const int i = row / a.group, h = kvh * a.group + (row - i * a.group);
+  return a.o + b * a.o_s[0] + h * a.o_s[1] + i * a.o_s[2];
+}
+
+// A row's log-sum-exp, where the call wants it; l is relative to 2^m.
+__device__ __forceinline__ void store_lse(const DecArgs& a, int b, int kvh, int row, float m,
+                                          float l) {
+  if (a.lse == nullptr) return;
+  const int i = row / a.group, h = kvh * a.group + (row - i * a.group);
+  a.lse[h * a.lse_pitch + static_cast<long long>(b) * a.q_len + i] =
+      l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
 // Four elements of an output row, and with the first of them its log-sum-exp:
-// `row` is the query row within the KV head's group, y and l are relative to 2^m.
+// y and l are relative to 2^m.
 __device__ __forceinline__ void store_row4(const DecArgs& a, int b, int kvh, int row, int d0,
                                            float m, float l, float4 y) {
-  const int i = row / a.group, h = kvh * a.group + (row - i * a.group);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint2 w;
   w.x = f32_to_x2(y.x * inv, y.y * inv, a.f16);
   w.y = f32_to_x2(y.z * inv, y.w * inv, a.f16);
-  *reinterpret_cast<uint2*>(a.o + b * a.o_s[0] + h * a.o_s[1] + i * a.o_s[2] + d0) = w;
-  if (a.lse != nullptr && d0 == 0)
-    a.lse[h * a.lse_pitch + static_cast<long long>(b) * a.q_len + i] =
-        l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  *reinterpret_cast<uint2*>(output_row(a, b, kvh, row) + d0) = w;
+  if (d0 == 0) store_lse(a, b, kvh, row, m, l);
 }
 
 template <bool F16>
@@ -781,13 +798,151 @@ __device__ __forceinline__ long long slot_of(int first, int p) {
   return (2LL * (first + c) + (c == 0 ? 1 : 0)) * PER + (p - c * PER);
 }
 
+// A row whose sums are not finite though its weights are, which may be due to a value
+// that the row does not see, once more: y takes the place of the elements that are not
+// finite in it.  Scores and sums are formed in fp32, in two walks over the tokens (the
+// largest score and the sum of weights, then O), 32 of them at a time to a warp and by
+// WARPS warps in turn, whose sums are added in order; weights are divided by their sum
+// first, so that O cannot overflow.  (Rows of wide calls alone, and here, where nobody
+// waits for them: 160 histories of 2^18 tokens, 40 rows each, all formed anew: 0.28 s.)
+//
+// Lane x of a warp holds elements E x on, E = D / 32, of what it is given and returns.
+template <int D, int WARPS>
+__device__ __noinline__ void form_anew(const DecArgs& a, int b, int kvh, int row, bool from_kept,
+                                       int warp, float (*sh)[D], float (&y)[D / 32]) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int i = row / a.group, h = kvh * a.group + (row - i * a.group);
+  const uint16_t* q = from_kept
+                          ? a.kept + ((static_cast<long long>(b) * a.heads_kv + kvh) * a.rows + row) * D
+                          : a.q + b * a.q_s[0] + h * a.q_s[1] + i * a.q_s[2];
+  const uint4* q4 = reinterpret_cast<const uint4*>(q);
+  const int len = clamp_len(a, b), lim = a.causal ? len - a.q_len + i + 1 : len;
+  const int page_size = a.tiles_per_page * TOK;
+  const int32_t* table = a.table + static_cast<long long>(b) * a.table_stride;
+  const uint8_t *k = a.k + kvh * a.k_sh, *v = a.v + kvh * a.v_sh;
+  // The score of a token, in log2 units, and where its value lies (no page: zeros).
+  auto score = [&](int tok, const uint8_t*& value) {
+    const int col = tok / page_size, at = tok - col * page_size, page = __ldg(table + col);
+    value = nullptr;
+    if (page < 0 || page >= a.num_pages) return 0.f;
+    value = v + (page * a.v_sp + static_cast<long long>(at) * a.v_st);
+    const uint4* k4 = reinterpret_cast<const uint4*>(k + (page * a.k_sp +
+                                                          static_cast<long long>(at) * a.k_st));
+    float s = 0.f;
+#pragma unroll 2
+    for (int e = 0; e < D / 8; ++e) {
+      const uint4 x = q4[e], z = __ldg(k4 + e);
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, zs[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float2 f = x2_to_f32(xs[w], a.f16), g = x2_to_f32(zs[w], a.f16);
+        s = fmaf(f.x, g.x, s);
+        s = fmaf(f.y, g.y, s);
+      }
+    }
+    return s * a.sigma_log2;
+  };
+  auto of_warps = [&](float x, bool largest) {  // the largest, or the sum, over all tokens
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float z = __shfl_xor_sync(0xffffffffu, x, o);
+      x = largest ? fmaxf(x, z) : x + z;
+    }
+    if constexpr (WARPS > 1) {
+      __syncthreads();
+      if (lane == 0) sh[warp][0] = x;
+      __syncthreads();
+      x = sh[0][0];
+      for (int w = 1; w < WARPS; ++w) x = largest ? fmaxf(x, sh[w][0]) : x + sh[w][0];
+    }
+    return x;
+  };
+
+  const uint8_t* value;
+  float m = -NO_SCORE, l = 0.f;
+  for (int tok = 32 * warp + lane; tok < lim; tok += 32 * WARPS) {
+    const float s = score(tok, value), m1 = fmaxf(m, s);
+    l = fmaf(l, ex2_approx(m - m1), ex2_approx(s - m1));
+    m = m1;
+  }
+  const float most = of_warps(m, true);
+  const float inv = 1.f / of_warps(l * ex2_approx(m - most), false);
+  float o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  for (int t0 = 32 * warp; t0 < lim; t0 += 32 * WARPS) {
+    value = nullptr;
+    float p = 0.f;
+    if (t0 + lane < lim) p = ex2_approx(score(t0 + lane, value) - most) * inv;
+#pragma unroll 2
+    for (int t = 0; t < 32; ++t) {
+      const float pt = __shfl_sync(0xffffffffu, p, t);
+      const uint8_t* vt = reinterpret_cast<const uint8_t*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(value), t));
+      if (vt == nullptr) continue;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 f =
+            x2_to_f32(__ldg(reinterpret_cast<const uint32_t*>(vt) + (lane * E + e) / 2), a.f16);
+        o[e] = fmaf(pt, f.x, o[e]);
+        o[e + 1] = fmaf(pt, f.y, o[e + 1]);
+      }
+    }
+  }
+  if constexpr (WARPS > 1) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e) sh[warp][lane * E + e] = o[e];
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      o[e] = sh[0][lane * E + e];
+      for (int w = 1; w < WARPS; ++w) o[e] += sh[w][lane * E + e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (!(fabsf(y[e]) < INFINITY)) y[e] = o[e];
+}
+
+// Stores such a row; its log-sum-exp is of the weights alone, and stored with the rest.
+template <int D>
+__device__ __forceinline__ void store_anew(const DecArgs& a, int b, int kvh, int row,
+                                           const float (&y)[D / 32]) {
+  uint32_t* o = reinterpret_cast<uint32_t*>(output_row(a, b, kvh, row));
+#pragma unroll
+  for (int e = 0; e < D / 32; e += 2)
+    o[((threadIdx.x & 31) * (D / 32) + e) / 2] = f32_to_x2(y[e], y[e + 1], a.f16);
+}
+
+// A stored row, as fp32.
+template <int D>
+__device__ __forceinline__ void load_stored(const DecArgs& a, int b, int kvh, int row,
+                                            float (&y)[D / 32]) {
+  const uint32_t* o = reinterpret_cast<const uint32_t*>(output_row(a, b, kvh, row));
+#pragma unroll
+  for (int e = 0; e < D / 32; e += 2) {
+    const float2 f = x2_to_f32(o[((threadIdx.x & 31) * (D / 32) + e) / 2], a.f16);
+    y[e] = f.x, y[e + 1] = f.y;
+  }
+}
+
+// Whether row r of segment x, which lies within a CTA, is to be formed anew.  (Of other
+// segments it says nothing; read all the same, so that the load waits for no other.)
+template <int PER>
+__device__ __forceinline__ bool is_anew(const DecArgs& a, int x, int r) {
+  return PER > 1 && (a.anew[4 * x + (r >> 5)] >> (r & 31) & 1u);
+}
+
 // Joins the parts of the segments that a cut crossed: block (x, r) takes row r
 // of job x, which is segment x, or where there are more segments than CTAs the
 // one that CTA x began and did not finish -- if that was cut.  The parts lie in
 // the CTAs first (its second slot) .. last (their first slots), PER in each.  The
 // offsets come first, all at once, so that the sums' loads wait for nothing.
 template <int D, int ROWS, int PER>
-__global__ void __launch_bounds__(JOIN_THREADS, 4) decode16_join_kernel(const DecArgs a) {
+__global__ void __launch_bounds__(JOIN_THREADS, 4)
+    decode16_join_kernel(const __grid_constant__ DecArgs a) {
   constexpr int LANES = D / 4;                 // threads that cover a row, four elements each
   constexpr int PARTS = JOIN_THREADS / LANES;  // parts read at once
   __shared__ float4 sh_y[PARTS][LANES];
@@ -796,12 +951,26 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) decode16_join_kernel(const De
   if constexpr (EARLY_AFTER_JOIN<D>) allow_next_kernel();
   wait_for_kernels_before();
   const int4 job = a.joins[blockIdx.x];
-  if (job.x < 0 || job.w < 0) return;
+  const int r = blockIdx.y;
+  const bool anew = is_anew<PER>(a, blockIdx.x, r);
+  if (job.x < 0 || (job.w < 0 && !anew)) return;
   const int b = job.x, kvh = job.y / a.row_tiles;
-  const int r = blockIdx.y, row = (job.y - kvh * a.row_tiles) * ROWS + r;
+  const int row = (job.y - kvh * a.row_tiles) * ROWS + r;
   if (row >= a.rows) return;
-  const int first = job.z, count = PER * (job.w - first + 1);  // at most MAX_PARTS
   const int tid = threadIdx.x;
+  constexpr int JOIN_WARPS = JOIN_THREADS / 32;
+  float(*sh_o)[D] = reinterpret_cast<float(*)[D]>(sh_y);  // of each warp, in form_anew
+  static_assert(JOIN_WARPS * D * 4 <= sizeof(sh_y), "shared memory");
+  if constexpr (PER > 1) {
+    if (job.w < 0) {
+      float y[D / 32];
+      load_stored<D>(a, b, kvh, row, y);
+      form_anew<D, JOIN_WARPS>(a, b, kvh, row, a.in_place, tid >> 5, sh_o, y);
+      if (tid < 32) store_anew<D>(a, b, kvh, row, y);
+      return;
+    }
+  }
+  const int first = job.z, count = PER * (job.w - first + 1);  // at most MAX_PARTS
   auto slot = [&](int p) { return slot_of<PER>(first, p); };
 
   float2 mine[MAX_PARTS / JOIN_THREADS];
@@ -843,11 +1012,32 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) decode16_join_kernel(const De
   }
   sh_y[p0][lane] = y;
   __syncthreads();
-  if (p0 != 0) return;
+  if (PER == 1 && p0 != 0) return;
+  if (p0 == 0) {
 #pragma unroll
-  for (int p = 1; p < PARTS; ++p) {
-    const float4 x = sh_y[p][lane];
-    y.x += x.x, y.y += x.y, y.z += x.z, y.w += x.w;
+    for (int p = 1; p < PARTS; ++p) {
+      const float4 x = sh_y[p][lane];
+      y.x += x.x, y.y += x.y, y.z += x.z, y.w += x.w;
+    }
+  }
+  if constexpr (PER > 1) {
+    const bool finite = fabsf(y.x) < INFINITY && fabsf(y.y) < INFINITY && fabsf(y.z) < INFINITY &&
+                        fabsf(y.w) < INFINITY;
+    if (__syncthreads_or(p0 == 0 && !finite && l < INFINITY)) {
+      const float inv = 1.f / l;
+      if (p0 == 0)
+        reinterpret_cast<float4*>(sh_o[0])[lane] =
+            make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+      __syncthreads();
+      float z[D / 32];
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) z[e] = sh_o[0][(tid & 31) * (D / 32) + e];
+      form_anew<D, JOIN_WARPS>(a, b, kvh, row, false, tid >> 5, sh_o, z);
+      if (tid < 32) store_anew<D>(a, b, kvh, row, z);
+      if (tid == 0) store_lse(a, b, kvh, row, m, l);
+      return;
+    }
+    if (p0 != 0) return;
   }
   store_row4(a, b, kvh, row, 4 * lane, m, l, y);
 }
@@ -855,17 +1045,28 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) decode16_join_kernel(const De
 // The same where segments have few parts: a warp takes a row of job x by itself,
 // 32 parts' offsets at a time.
 template <int D, int ROWS, int PER>
-__global__ void __launch_bounds__(JOIN_THREADS) decode16_join_rows_kernel(const DecArgs a) {
+__global__ void __launch_bounds__(JOIN_THREADS)
+    decode16_join_rows_kernel(const __grid_constant__ DecArgs a) {
   constexpr int E = D / 32;  // elements of a lane
   if constexpr (EARLY_AFTER_JOIN<D>) allow_next_kernel();
   wait_for_kernels_before();
   const int4 job = a.joins[blockIdx.x];
-  if (job.x < 0 || job.w < 0) return;
   const int lane = threadIdx.x & 31;
   const int r = blockIdx.y * (JOIN_THREADS / 32) + (threadIdx.x >> 5);
+  const bool anew = r < ROWS && is_anew<PER>(a, blockIdx.x, r);
+  if (job.x < 0 || (job.w < 0 && !anew)) return;
   const int b = job.x, kvh = job.y / a.row_tiles;
   const int row = (job.y - kvh * a.row_tiles) * ROWS + r;
   if (r >= ROWS || row >= a.rows) return;
+  if constexpr (PER > 1) {
+    if (job.w < 0) {
+      float y[E];
+      load_stored<D>(a, b, kvh, row, y);
+      form_anew<D, 1>(a, b, kvh, row, a.in_place, 0, nullptr, y);
+      store_anew<D>(a, b, kvh, row, y);
+      return;
+    }
+  }
   const int first = job.z, count = PER * (job.w - first + 1);
   auto slot = [&](int p) { return slot_of<PER>(first, p); };
   float m = -NO_SCORE, l = 0.f, y[E];
@@ -896,6 +1097,20 @@ __global__ void __launch_bounds__(JOIN_THREADS) decode16_join_rows_kernel(const 
         const float2 z = *reinterpret_cast<const float2*>(x);
         y[0] += z.x * wp, y[1] += z.y * wp;
       }
+    }
+  }
+  if constexpr (PER > 1) {
+    bool finite = true;
+#pragma unroll
+    for (int e = 0; e < E; ++e) finite = finite && fabsf(y[e]) < INFINITY;
+    if (l < INFINITY && !__all_sync(0xffffffffu, finite)) {
+      const float inv = 1.f / l;
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] *= inv;
+      form_anew<D, 1>(a, b, kvh, row, false, 0, nullptr, y);
+      store_anew<D>(a, b, kvh, row, y);
+      if (lane == 0) store_lse(a, b, kvh, row, m, l);
+      return;
     }
   }
   if constexpr (E == 4) {

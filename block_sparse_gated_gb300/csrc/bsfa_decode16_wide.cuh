@@ -119,66 +119,6 @@ struct WideWalk {
   }
 };
 
-// 16 elements of a row, as fp32.
-template <bool F16>
-__device__ __forceinline__ void load16(const void* p, float (&f)[16]) {
-  const uint4* q = reinterpret_cast<const uint4*>(p);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint4 x = __ldg(q + h);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 y = x2_to_f32(w[e], F16);
-      f[8 * h + 2 * e] = y.x, f[8 * h + 2 * e + 1] = y.y;
-    }
-  }
-}
-
-// The elements of one row's O over a warpgroup's tiles that are not finite, which may
-// be due to a value that the row does not see, once more: from global memory in fp32.
-// Sixteen elements take a walk over the tokens of their own.
-template <int D, bool F16>
-__device__ __noinline__ void wide_exact_row(const DecArgs& a, const WideWork& w, int row, int wg,
-                                            float z, float* dst) {
-  const int i = row / a.group, h = w.kvh * a.group + (row - i * a.group);
-  const uint16_t* q = a.q + w.b * a.q_s[0] + h * a.q_s[1] + i * a.q_s[2];
-  const int lim = a.causal ? w.len - a.q_len + i + 1 : w.len;
-  const int page_size = a.tiles_per_page * TOK;
-  const int32_t* table = a.table + static_cast<long long>(w.b) * a.table_stride;
-  for (int d0 = 0; d0 < D; d0 += 16) {
-    bool finite = true;
-    for (int j = 0; j < 16; ++j) finite = finite && fabsf(dst[d0 + j]) < INFINITY;
-    if (finite) continue;
-    float o[16] = {};
-    for (int t = wg; t < w.n; t += 2) {
-      const int begin = (w.t0 + t) * TILE, end = min(begin + TILE, lim);
-      for (int tok = begin; tok < end; ++tok) {
-        const int page = __ldg(table + tok / page_size), at = tok % page_size;
-        const bool ok = page >= 0 && page < a.num_pages;
-        float s = 0.f, v[16] = {};
-        if (ok) {
-          const uint8_t* k = a.k + page * a.k_sp + w.kvh * a.k_sh + at * a.k_st;
-          for (int e = 0; e < D; e += 16) {
-            float x[16], y[16];
-            load16<F16>(q + e, x);
-            load16<F16>(k + 2 * e, y);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) s = fmaf(x[j], y[j], s);
-          }
-          load16<F16>(a.v + page * a.v_sp + w.kvh * a.v_sh + at * a.v_st + 2 * d0, v);
-        }
-        const float p = ex2_approx(fmaf(s, a.sigma_log2, z));
-#pragma unroll
-        for (int j = 0; j < 16; ++j) o[j] = fmaf(p, v[j], o[j]);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (!(fabsf(dst[d0 + j]) < INFINITY)) dst[d0 + j] = o[j];
-  }
-}
-
 template <int D, bool F16>
 __global__ void __launch_bounds__(WIDE_THREADS, 1)
     decode16_wide_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -395,7 +335,6 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
       float z_c = NO_SCORE, l_c = 0.f;    // of the runs before it
       bool carried = false;
       int in_run = 0;                     // tiles of the run so far
-      bool finite = true;
       // Adds the run's O to what the part holds.
       auto flush = [&](bool any) -> bool {
         if (any && !wait_all(&c->pv_done[wg], (pv_n - 1) & 1, abort, a.err, ERR_WAIT_O_FULL))
@@ -425,8 +364,6 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
               y.x = fmaf(old.x, f_c, y.x), y.y = fmaf(old.y, f_c, y.y);
               y.z = fmaf(old.z, f_c, y.z), y.w = fmaf(old.w, f_c, y.w);
             }
-            finite = finite && fabsf(y.x) < INFINITY && fabsf(y.y) < INFINITY &&
-                     fabsf(y.z) < INFINITY && fabsf(y.w) < INFINITY;
             dst[8 * x + e] = y;
           }
         }
@@ -540,8 +477,6 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
       if (!ok || !(ok = part_is_free())) break;
       if (!w.whole || carried) {
         if (!(ok = flush(in_run > 0))) break;
-        if (real && !finite && l_c < INFINITY)
-          wide_exact_row<D, F16>(a, w, r, wg, z_c, a.part_o + at * D);
         if (!w.whole) {
           if (real) a.part_ml[at] = make_float2(-z_c, l_c);
           continue;
@@ -565,12 +500,12 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         const float both = fminf(my_z, other.x);
         const float f = ex2_approx(both - my_z), f0 = ex2_approx(both - other.x);
         const float sum = fmaf(my_l, f, other.y * f0);
-        float4 *own = reinterpret_cast<float4*>(a.part_o + at * D), *first = own - TILE * D / 4;
-        bool sums_finite = true;
-        // The O's of 32 elements.
-        auto parts = [&](int x, float (&o)[32], float (&o0)[32]) {
+        const float4 *own = reinterpret_cast<const float4*>(a.part_o + at * D),
+                     *first = own - TILE * D / 4;
+        auto joined = [&](int x, float (&y)[32]) {  // 32 elements
+          float o0[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = o0[e] = 0.f;
+          for (int e = 0; e < 32; ++e) y[e] = o0[e] = 0.f;
           auto load = [&](uint32_t from, const float4* held, bool in_memory, bool there,
                           float (&to)[32]) {
             if (in_memory) {
@@ -585,12 +520,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
               for (int e = 0; e < 32; ++e) to[e] = __uint_as_float(v[e]);
             }
           };
-          load(tO, own, carried, any, o);
+          load(tO, own, carried, any, y);
           load(tO - 128, first, tiles0 > WIDE_RUN, tiles0 > 0, o0);
-        };
-        auto joined = [&](int x, float (&y)[32]) {
-          float o0[32];
-          parts(x, y, o0);
 #pragma unroll
           for (int e = 0; e < 32; ++e) y[e] = fmaf(y[e], f, o0[e] * f0);
         };
@@ -600,47 +531,36 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             store_row4(a, w.b, w.kvh, r, 32 * x + e, -both, sum,
                        make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]));
         };
-        // Where the output is the queries themselves, which are needed once more for sums
-        // that are not finite, nothing is stored before that is known.
+        bool finite = true;
 #pragma unroll 1
         for (int x = 0; x < D / 32; ++x) {
           float y[32];
           joined(x, y);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) sums_finite = sums_finite && fabsf(y[e]) < INFINITY;
+          for (int e = 0; e < 32; ++e) finite = finite && fabsf(y[e]) < INFINITY;
           if (!a.in_place) store(x, y);
         }
-        if (!__any_sync(0xffffffffu, real && !sums_finite && sum < INFINITY)) {
-          if (a.in_place) {
-#pragma unroll 1
-            for (int x = 0; x < D / 32; ++x) {
-              float y[32];
-              joined(x, y);
-              store(x, y);
-            }
+        // What is not finite is formed anew by the join, from the queries: where the output
+        // takes their place, nothing is stored before they have been kept.
+        const bool anew = real && !finite && sum < INFINITY;
+        if (a.in_place) {
+          if (anew) {
+            const uint4* src = reinterpret_cast<const uint4*>(output_row(a, w.b, w.kvh, r));
+            uint4* dst = reinterpret_cast<uint4*>(
+                a.kept + ((static_cast<long long>(w.b) * a.heads_kv + w.kvh) * a.rows + r) * D);
+#pragma unroll
+            for (int x = 0; x < D / 8; ++x) dst[x] = src[x];
           }
-        } else {
-          // As for parts that go to the join: into memory, and what is not finite anew.
 #pragma unroll 1
           for (int x = 0; x < D / 32; ++x) {
-            float o[32], o0[32];
-            parts(x, o, o0);
-            for (int e = 0; e < 32 && real; e += 4) {
-              own[8 * x + e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-              first[8 * x + e / 4] = make_float4(o0[e], o0[e + 1], o0[e + 2], o0[e + 3]);
-            }
-          }
-          if (real) {
-            wide_exact_row<D, F16>(a, w, r, 1, my_z, a.part_o + at * D);
-            wide_exact_row<D, F16>(a, w, r, 0, other.x, a.part_o + (at - TILE) * D);
-            for (int x = 0; x < D / 4; ++x) {
-              const float4 y = own[x], y0 = first[x];
-              store_row4(a, w.b, w.kvh, r, 4 * x, -both, sum,
-                         make_float4(fmaf(y.x, f, y0.x * f0), fmaf(y.y, f, y0.y * f0),
-                                     fmaf(y.z, f, y0.z * f0), fmaf(y.w, f, y0.w * f0)));
-            }
+            float y[32];
+            joined(x, y);
+            store(x, y);
           }
         }
+        const uint32_t rows_anew = __ballot_sync(0xffffffffu, anew);
+        if (lane == 0)
+          a.anew[4 * (w.b * a.heads_kv * a.row_tiles + w.seg) + wq] = rows_anew;
         tc_fence_before();
         mbar_arrive(&c->x_empty);
       }

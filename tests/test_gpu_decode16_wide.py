@@ -62,6 +62,112 @@ def _bad_in(cache, table, seq, token, element, number, page=64):
     return at, was
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("d,dtype", [(64, HF), (128, BF)])
+@pytest.mark.parametrize("few,batch", [([1000, 700], 200), ([16800], 160)])
+def test_values_that_are_not_finite_within_a_cta(cuda_device, bad, d, dtype, few, batch):
+    """A value poisons its element of the queries that see the token, in every sequence that holds
+    it, and nothing else, down to the bit, in whole segments and in cut ones, with results in a
+    tensor of their own or in place of the queries."""
+    b = _bsfa()
+    n, L = 3, few[0]
+    q, cache, table, n32, lens, rows, (per_cta, segments) = _call(
+        few, batch, (18, 1, n), d, dtype, cuda_device, block=4000 if L > 4000 else None)
+    holds = torch.tensor([i % len(few) == 0 for i in range(batch)], device=cuda_device)
+    mine = [s for s in segments if s[0] % len(few) == 0]
+    assert len(_whole(mine)) >= 5 and len(mine) > len(_whole(mine))
+    clean = b.decode16(q, cache, table, n32, return_lse=True)
+    for token, first in ((L - 2, 1), (L - 1, 2), (100, 0)):  # seen by queries `first` and later
+        at, was = _bad_in(cache, table, 0, token, 37, bad)
+        got = b.decode16(q, cache, table, n32, return_lse=True)
+        place = q.clone()
+        b.decode16(place, cache, table, n32, out=place)
+        cache.v[at] = was
+        hit = torch.zeros_like(got["out"], dtype=torch.bool)
+        hit[holds, :, first:, 37] = True
+        x = got["out"][hit]
+        assert bool((torch.isnan(x) if math.isnan(bad) else x == bad).all())
+        assert torch.equal(got["lse"], clean["lse"])
+        again = hit.clone()
+        again[holds, :, :, 37] = True  # formed anew, from weights in fp32
+        assert torch.equal(got["out"][~again], clean["out"][~again])
+        same = torch.equal(torch.nan_to_num(got["out"].float(), nan=1e9),
+                           torch.nan_to_num(place.float(), nan=1e9))
+        assert same
+        got["out"][hit] = clean["out"][hit]
+        _check(got, q, rows, lens, dtype, d, range(0, batch, 23))
+
+
+def test_pages_and_lengths_of_rows_that_are_formed_anew(cuda_device):
+    """Beside a value that is not a number and not seen by all: entries outside the pool read as
+    zero keys and values there too, and both orders of tokens and heads, two KV heads and three
+    tiles of rows are walked right."""
+    b = _bsfa()
+    for layout, d, dtype in (("pthd", 64, BF), ("phtd", 128, HF)):
+        few = [900, 300, 120]
+        Hq, n = 10, 60
+        q, cache, table, n32, lens, rows, (_, segments) = _call(
+            few, 120, (Hq, 2, n), d, dtype, cuda_device, page=48, layout=layout)
+        for i, L in enumerate(few):
+            token = L - 2
+            page = table[i, token // 48].item()
+            at = (page, slice(None), token % 48) if layout == "phtd" else (page, token % 48)
+            cache.v[at][..., 5] = float("nan")
+        for i in range(0, 120, 3):  # the third page of the first one's histories
+            table[i, 2] = -1
+        rows[0] = tuple(x.copy() for x in rows[0])
+        for x in rows[0]:
+            x[:, 96:144] = 0.0
+        assert _whole(segments)
+        got = b.decode16(q, cache, table, n32, return_lse=True)
+        out = got["out"]
+        seen = torch.zeros_like(out, dtype=torch.bool)
+        seen[:, :, n - 2:, 5] = True
+        assert bool(torch.isnan(out[seen]).all()) and bool(torch.isfinite(out[~seen]).all())
+        for x in rows:  # the rows that see it are compared in their other elements alone
+            x[1][:, -2, 5] = 0.0
+        for i in (0, 1, 2, 60, 61, 62, 117, 118, 119):
+            part = {"out": out[i:i + 1].clone(),
+                    "lse": got["lse"].view(Hq, 120, n)[:, i]}
+            clean = rows[i % 3]
+            exact = co.attend(q[i].cpu().double().numpy(), *clean, sigma=1 / math.sqrt(d))[0]
+            part["out"][0, :, n - 2:, 5] = torch.from_numpy(exact[:, n - 2:, 5]).to(out)
+            cu.check_decode(part, q[i:i + 1], [clean], [lens[i]], dtype, d)
+
+
+def test_values_that_are_not_finite_in_long_histories(cuda_device):
+    """Hundreds of thousands of tokens to a CTA, their last value not a number and hidden from one
+    query, their first ones seen by all: no wait runs out, and rows beside them are what they
+    were."""
+    from block_sparse_gated_gb300 import api
+    b = _bsfa()
+    L, batch, d, page = 1 << 18, 160, 64, 256
+    q, cache, table, n32, lens, rows, (per_cta, segments) = _call(
+        [L], batch, (20, 1, 2), d, BF, cuda_device, page=page, block=4000)
+    assert per_cta > 2000 and _whole(segments)
+    assert api.device_error() == 0
+    clean = b.decode16(q, cache, table, n32, return_lse=True)
+    cache.v[table[0, L // page - 1].item(), 0, page - 1, 3] = float("nan")
+    cache.v[table[0, 0].item(), 0, 2, 16:] = float("inf")
+    torch.cuda.synchronize()
+    began = time.time()
+    got = b.decode16(q, cache, table, n32, return_lse=True)
+    torch.cuda.synchronize()
+    print(f"{time.time() - began:.3f} s")
+    assert api.device_error() == 0
+    out = got["out"]
+    assert bool((out[..., 16:] == float("inf")).all())
+    assert bool(torch.isnan(out[:, :, 1, 3]).all())
+    same = [0, 1, 2] + list(range(4, 16))
+    assert torch.equal(out[..., same], clean["out"][..., same])
+    assert torch.equal(got["lse"], clean["lse"])
+    # Formed anew: each side within its bound, a rounding and 2^-13, of the same mean.
+    was = clean["out"][:, :, 0, 3].float()
+    size = float(np.abs(rows[0][1][0, :, 3]).mean())
+    assert bool(((out[:, :, 0, 3].float() - was).abs() <= was.abs() * 2.0 ** -7 +
+                 size * 2.0 ** -11).all())
+
+
 @pytest.mark.parametrize("heads", [(40, 1, 1), (32, 2, 12)])
 def test_every_segment_has_its_place_in_the_join(cuda_device, heads):
     """The table that the join reads is written whole by every call, whatever the workspace held:
