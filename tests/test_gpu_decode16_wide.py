@@ -55,6 +55,62 @@ def _check(res, q, rows, lens, dtype, d, some):
                         [rows[i % len(rows)]], [lens[i]], dtype, d)
 
 
+@pytest.mark.parametrize("d,dtype", [(64, HF), (128, BF), (64, BF), (128, HF)])
+@pytest.mark.parametrize("heads", [(40, 1, 1), (20, 1, 3), (32, 2, 8), (50, 1, 5)])
+def test_segments_within_a_cta(cuda_device, d, dtype, heads):
+    """Sequences of one tile to eight, most of them within one CTA, whose two warpgroups share
+    their tiles."""
+    few = [1000, 129, 700, 1, 256, 0, 1024]
+    q, cache, table, n32, lens, rows, (per_cta, segments) = _call(few, 210, heads, d, dtype,
+                                                                  cuda_device)
+    whole = [s for s in _whole(segments) if lens[s[0]] > 128]
+    assert per_cta >= 14 and len(whole) > 30
+    res = _bsfa().decode16(q, cache, table, n32, return_lse=True)
+    _check(res, q, rows, lens, dtype, d, range(0, 210, 5))
+
+
+@pytest.mark.parametrize("d,dtype", [(64, HF), (128, BF)])
+@pytest.mark.parametrize("few", [[17000], [40000], [33000, 16385, 900, 16384]])
+def test_more_tiles_than_a_warpgroup_sums_at_once(cuda_device, d, dtype, few):
+    """Pieces of 134 tiles and more: sums that go to memory in the middle of a segment, of whole
+    ones and of parts, up to exactly 64 and 65 tiles to a warpgroup."""
+    batch = 160 if len(few) == 1 else 260
+    q, cache, table, n32, lens, rows, (per_cta, segments) = _call(
+        few, batch, (12, 1, 4), d, dtype, cuda_device, block=4000)
+    assert per_cta > 2 * RUN + 6
+    long = [s for s in segments if math.ceil(lens[s[0]] / 128) > 2 * RUN]
+    assert [s for s in long if s[2] != s[3]]
+    assert _whole(long)
+    res = _bsfa().decode16(q, cache, table, n32, return_lse=True)
+    _check(res, q, rows, lens, dtype, d, range(0, batch, 37))
+    # The others repeat these; where they are cut differs, so that sums differ by their roundings.
+    first = res["out"][:len(few)].float()
+    again = res["out"].view(-1, len(few), *first.shape[1:]).float()
+    assert bool(((again - first).abs() <= first.abs() * torch.finfo(dtype).eps * 2 + 1e-3).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("d", [64, 128])
+def test_sums_of_values_of_one_sign(cuda_device, dtype, d):
+    """The tensor cores cut off what they add to a sum: at most 2^-23 of it (a step of fp32) at
+    each of the 16 steps of a tile, over 64 tiles, so 2^-13 of O, and always toward zero.  Weights
+    leave 2^-16, the sums in memory and in the join 2^-18.  The one rounding is monotone, so the
+    result lies between the roundings of what those allow."""
+    L, batch = 40000, 160
+    q, cache, table, n32, lens, rows, (per_cta, _) = _call(
+        [L], batch, (48, 1, 1), d, dtype, cuda_device, block=4000, positive=True, scale=0.3)
+    assert per_cta > 2 * RUN + 6
+    res = _bsfa().decode16(q, cache, table, n32, return_lse=True)
+    k, v = rows[0][0][0], rows[0][1][0]
+    s = q[0, :, 0].cpu().double().numpy() @ k.T / math.sqrt(d)
+    p = np.exp(s - s.max(1, keepdims=True))
+    want = torch.from_numpy((p / p.sum(1, keepdims=True)) @ v)
+    got = res["out"][:, :, 0].cpu()
+    near = 2.0 ** -16 + 2.0 ** -18
+    assert bool((got >= (want * (1 - 2.0 ** -13 - near)).to(dtype)).all())
+    assert bool((got <= (want * (1 + near)).to(dtype)).all())
+
+
 def _bad_in(cache, table, seq, token, element, number, page=64):
     at = (table[seq, token // page].item(), slice(None), token % page, element)
     was = cache.v[at].clone()
