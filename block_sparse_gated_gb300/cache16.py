@@ -68,13 +68,55 @@ def rotary(rope: Rope, q, k=None, *, positions=None, start=None, cu_seqlens=None
     axis.  Angles are exact at any position; products are formed in fp32 and
     rounded once.
 
-    ``inverse`` turns back.  It is also the gradient: of the rotated rows' it
-    makes the rows'.  ``out``, a pair of tensors, may be (q, k) themselves; other
-    tensors must not overlap them."""
+    ``inverse`` turns back.  It is also the gradient, of the rotated rows' it
+    makes the rows', and what autograd takes for q and k that require one (zero
+    for rows outside every sequence; frequencies have none).  ``out``, a pair of
+    tensors, may be (q, k) themselves; other tensors must not overlap them, and it
+    takes no part in a recorded graph."""
     f, axes, interleaved = rope
     q_out, k_out = (None, None) if out is None else out
     return _native.binding().rotary(f, axes, interleaved, q, k, positions, start, cu_seqlens,
                                     layout, inverse, q_out, k_out, stream)
+
+
+class _Rotary(torch.autograd.Function):
+    """Recorded rotations: arguments as the binding's, and ``zeros``, whether packed
+    rows outside every sequence are zeros rather than left as they are."""
+
+    @staticmethod
+    def forward(ctx, q, k, f, axes, interleaved, positions, start, cu_seqlens, layout, inverse,
+                zeros, stream):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(f, positions, start, cu_seqlens)
+        ctx.how = axes, interleaved, layout, inverse
+        out = None, None
+        if zeros and cu_seqlens is not None:
+            out = torch.zeros_like(q), None if k is None else torch.zeros_like(k)
+        q1, k1 = _native.binding().rotary(f, axes, interleaved, q, k, positions, start, cu_seqlens,
+                                          layout, inverse, *out, stream)
+        ctx.mark_non_differentiable(*[y for y, needed in zip((q1, k1), ctx.needs_input_grad)
+                                      if y is not None and not needed])
+        return q1, k1
+
+    @staticmethod
+    def backward(ctx, *grads):
+        f, positions, start, cu_seqlens = ctx.saved_tensors
+        axes, interleaved, layout, inverse = ctx.how
+        # Dense and aligned, whatever made them (a sum's gradient has strides of zero).
+        g = [x.contiguous() for x in grads if x is not None]
+        g = [x.clone() if x.data_ptr() % 16 else x for x in g]
+        if not g:
+            return (None,) * 12
+        turned = iter(_Rotary.apply(g[0], g[1] if len(g) > 1 else None, f, axes, interleaved,
+                                    positions, start, cu_seqlens, layout, not inverse, True, None))
+        return *[None if x is None else next(turned) for x in grads], *(None,) * 10
+
+
+def _rotary_recorded(f, axes, interleaved, q, k, positions, start, cu_seqlens, layout, inverse,
+                     q_out, k_out, stream):
+    """What the binding's rotary calls for rows that require a gradient."""
+    return _Rotary.apply(q, k, f, axes, interleaved, positions, start, cu_seqlens, layout, inverse,
+                         False, stream)
 
 
 def cache16_write(cache: KVCache16, k, v, block_table, *, rope: Optional[Rope] = None, q=None,

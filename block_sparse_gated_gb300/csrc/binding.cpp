@@ -11,6 +11,7 @@
 
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty_like.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -42,6 +43,12 @@ const Tensor& needed(PyObject* o, const char* name) {
   const Tensor* t = tensor(o, name);
   if (t == nullptr) refuse(PyExc_TypeError, std::string(name) + " must be a tensor");
   return *t;
+}
+
+// Whether autograd is to record what is made of one of these.
+template <class... T>
+bool recorded(const T*... t) {
+  return c10::GradMode::is_enabled() && ((t != nullptr && t->requires_grad()) || ...);
 }
 
 // A layout by name; `otherwise` for None.
@@ -322,6 +329,19 @@ void arguments(Py_ssize_t got, Py_ssize_t expected) {
   if (got != expected) refuse(PyExc_TypeError, "wrong number of arguments");
 }
 
+// The same call as a node of the autograd graph, which calls back without recording.
+PyObject* rotary_recorded(PyObject* const* a, Py_ssize_t n) {
+  PyObject* m = PyImport_ImportModule("block_sparse_gated_gb300.cache16");
+  if (m == nullptr) throw python_error();
+  PyObject* f = PyObject_GetAttrString(m, "_rotary_recorded");
+  Py_DECREF(m);
+  if (f == nullptr) throw python_error();
+  PyObject* r = PyObject_Vectorcall(f, a, n, nullptr);
+  Py_DECREF(f);
+  if (r == nullptr) throw python_error();
+  return r;
+}
+
 // inv_freq, axes, interleaved, q, k, positions, start, cu_seqlens, layout, inverse, q_out, k_out,
 // stream -> (q_out, k_out)
 PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -332,6 +352,12 @@ PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor *start = tensor(a[6], "start"), *cu = tensor(a[7], "cu_seqlens");
   const Tensor *q_out = tensor(a[10], "out"), *k_out = tensor(a[11], "out");
   const at::Device device = q.device();
+  want(!recorded(&f), "inv_freq has no gradient");
+  if (recorded(&q, k, q_out, k_out)) {
+    want(q_out == nullptr && k_out == nullptr,
+         "out has no gradient: leave it out, or call rotary under torch.no_grad()");
+    return rotary_recorded(a, n);
+  }
   want(q_out == nullptr ? k_out == nullptr : (k_out == nullptr) == (k == nullptr),
        "out must be a pair, with None where there is no k");
   want(k_out == nullptr || q_out->const_data_ptr() != k_out->const_data_ptr() || q.numel() == 0,
