@@ -129,7 +129,9 @@ def cache16_write(cache: KVCache16, k, v, block_table, *, rope: Optional[Rope] =
     position start[b] + i, whatever its rotary positions are: token pos %
     page_size of page block_table[b, pos // page_size].  A position beyond the
     table, or an entry outside the pool, is dropped.  The positions of one call
-    must differ, and k and v must not overlap the pools."""
+    must differ, and k and v must not overlap the pools.  No gradient passes
+    through a cache: tensors that require one are refused while gradients are
+    recorded (``rotary`` has one)."""
     k_pool, v_pool, kv_layout = cache
     f, axes, interleaved = (None, None, False) if rope is None else rope
     return _native.binding().cache16_write(k_pool, v_pool, kv_layout, k, v, block_table, f, axes,
@@ -146,7 +148,7 @@ def decode16(q, cache: KVCache16, block_table, seqlens, *, max_seqlen=None, soft
     of sequence b attends to positions t <= seqlens[b] - n + i, or with
     ``causal=False`` to every t < seqlens[b].  Returns a dict with "out" and, on
     request, "lse" (float32 [Hq, B * n], natural log).  A query that sees nothing
-    gives zeros and -inf.  ``out`` may be q itself.
+    gives zeros and -inf.  ``out`` may be q itself.  No gradient is recorded.
 
     ``max_seqlen`` bounds the lengths (default: what the block table can hold;
     longer entries of seqlens are cut to it); the call reads lengths on the device

@@ -390,14 +390,17 @@ PyObject* py_cache16_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor *f = tensor(a[6], "inv_freq"), *q = tensor(a[9], "q");
   const Tensor *positions = tensor(a[10], "positions"), *start = tensor(a[11], "start");
   const Tensor *cu = tensor(a[12], "cu_seqlens"), *q_out = tensor(a[14], "q_out");
+  const Tensor &k_pool = needed(a[0], "cache.k"), &v_pool = needed(a[1], "cache.v");
   const at::Device device = k.device();
+  want(!recorded(&k, &v, q, q_out, f, &k_pool, &v_pool),
+       "cache16_write records no gradient: call it under torch.no_grad()");
   want(q != nullptr || q_out == nullptr, "q_out without q");
   want(q == nullptr || f != nullptr, "q is only rotated: it needs a rope");
   want(positions == nullptr || f != nullptr, "positions without a rope");
   bsfa_rows16 r = rows_fields(q, &k, &v, q_out, nullptr, a[13], cu, start, device);
   const bsfa_cache16 c =
-      cache_of(needed(a[0], "cache.k"), needed(a[1], "cache.v"), layout_of(a[2], "phtd"),
-               needed(a[5], "block_table"), r.batch, device);
+      cache_of(k_pool, v_pool, layout_of(a[2], "phtd"), needed(a[5], "block_table"), r.batch,
+               device);
   want(c.num_heads_kv == r.num_heads_kv && c.head_dim == r.head_dim && c.dtype == r.dtype,
        "K and V must have the cache's heads, head dimension and type");
   bsfa_rope p{};

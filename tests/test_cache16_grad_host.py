@@ -1,5 +1,5 @@
-"""What rotary positions refuse of tensors that require a gradient, without a GPU: the check comes
-before the one of the device."""
+"""What rotary positions and cache writes refuse of tensors that require a gradient, without a
+GPU: the check comes before the one of the device."""
 import pytest
 import torch
 
@@ -51,3 +51,19 @@ def test_frequencies_have_no_gradient(b):
         b.rotary(rope, _rows(4))
     with torch.no_grad(), pytest.raises(ValueError, match="must be CUDA tensors"):
         b.rotary(rope, _rows(4))
+
+
+def test_cache_writes_record_no_gradient(b):
+    cache = b.cache16_empty(1, 2, 16, 64, device="cpu")
+    table = torch.zeros(1, 1, dtype=torch.int32)
+    rope = b.Rope(torch.ones(32))
+    q, k, v = _rows(4), _rows(2), _rows(2)
+    for kw in (dict(k=_rows(2, True), v=v), dict(k=k, v=_rows(2, True)),
+               dict(k=k, v=v, q=_rows(4, True), rope=rope),
+               dict(k=k, v=v, q=q, rope=rope, q_out=_rows(4, True)),
+               dict(k=k, v=v, rope=b.Rope(torch.ones(32, requires_grad=True)))):
+        k1, v1 = kw.pop("k"), kw.pop("v")
+        with pytest.raises(ValueError, match="records no gradient"):
+            b.cache16_write(cache, k1, v1, table, **kw)
+        with torch.no_grad(), pytest.raises(ValueError, match="must be CUDA tensors"):
+            b.cache16_write(cache, k1, v1, table, **kw)
