@@ -51,6 +51,12 @@ bool recorded(const T*... t) {
   return c10::GradMode::is_enabled() && ((t != nullptr && t->requires_grad()) || ...);
 }
 
+// A caller's tensor that a call has written: counted, so that a graph that keeps its old
+// contents is told (tensors made for inference carry no count).
+void written(const Tensor* t) {
+  if (t != nullptr && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 // A layout by name; `otherwise` for None.
 const char* layout_of(PyObject* o, const char* otherwise) {
   if (o == Py_None) return otherwise;
@@ -375,6 +381,8 @@ PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
   }
   check(bsfa_rotary(&p, &r, place.stream()), "bsfa_rotary");
+  written(q_out);
+  written(k_out);
   PyObject* first = q_out ? Py_NewRef(a[10]) : THPVariable_Wrap(made_q);
   PyObject* second = k_out ? Py_NewRef(a[11]) : k ? THPVariable_Wrap(made_k) : Py_NewRef(Py_None);
   return Py_BuildValue("NN", first, second);
@@ -412,6 +420,7 @@ PyObject* py_cache16_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
     out_of(made, a[13], cu != nullptr, r.q_out, r.q_out_stride);
   }
   check(bsfa_cache16_write(&c, f ? &p : nullptr, &r, place.stream()), "bsfa_cache16_write");
+  for (const Tensor* t : {&k_pool, &v_pool, q_out}) written(t);
   if (q == nullptr) Py_RETURN_NONE;
   return q_out ? Py_NewRef(a[14]) : THPVariable_Wrap(made);
   END_HANDLE_TH_ERRORS
@@ -491,6 +500,7 @@ PyObject* py_decode16(PyObject*, PyObject* const* a, Py_ssize_t n) {
     d.p.workspace_bytes = need;
   }
   check(bsfa_decode16(&d.cache, &d.p, place.stream()), "bsfa_decode16");
+  written(out);
   PyObject* first = out ? Py_NewRef(a[10]) : THPVariable_Wrap(o);
   if (!lse.defined()) return Py_BuildValue("{sN}", "out", first);
   return Py_BuildValue("{sNsN}", "out", first, "lse", THPVariable_Wrap(lse));

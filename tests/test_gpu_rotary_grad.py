@@ -1,4 +1,4 @@
-"""The gradient of rotated rows, by autograd."""
+"""The gradient of rotated rows, by autograd, and the versions of tensors written in place."""
 import pytest
 import torch
 
@@ -178,3 +178,38 @@ def test_a_gradient_step_by_differences(cuda_device):
     # As in the test of the inverse call: sqrt(n) roundings of half a step, six sigma.
     assert abs((lhs - rhs).item()) < 6 * 4 * 2.0 ** -11 * x.numel() ** 0.5
     assert abs(rhs.item()) > 0
+
+
+def test_writes_in_place_are_counted(cuda_device):
+    """What a call writes has a new version, so that a graph that keeps the old contents is told;
+    tensors made for inference have none."""
+    b = _bsfa()
+    rope = b.Rope(cu.inv_freq(32).to(cuda_device))
+    q, k = (cu.rand((1, h, 40, 64), BF, h, cuda_device) for h in (4, 2))
+    cache = b.cache16_empty(3, 2, 16, 64, device=cuda_device)
+    table = torch.arange(3, dtype=torch.int32, device=cuda_device)[None]
+    n32 = cu.i32([40], cuda_device)
+    out = [torch.empty_like(x) for x in (q, k)]
+
+    def versions():
+        return [x._version for x in (*out, cache.k, cache.v, q, k)]
+
+    was = versions()
+    b.rotary(rope, q, k, out=out)
+    assert versions() == [was[0] + 1, was[1] + 1, *was[2:]]
+    b.cache16_write(cache, k, k, table, rope=rope, q=q, q_out=out[0])
+    assert versions() == [was[0] + 2, was[1] + 1, was[2] + 1, was[3] + 1, *was[4:]]
+    b.decode16(q, cache, table, n32, out=out[0])
+    assert versions() == [was[0] + 3, was[1] + 1, was[2] + 1, was[3] + 1, *was[4:]]
+    w = torch.ones(q.shape, device=cuda_device, dtype=BF, requires_grad=True)
+    y = w * out[0]
+    b.rotary(rope, q, out=(out[0], None))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    with torch.inference_mode():
+        made = [torch.empty_like(q), torch.empty_like(k)]
+        store = b.cache16_empty(3, 2, 16, 64, device=cuda_device)
+        b.rotary(rope, q, k, out=made)
+    b.rotary(rope, q, k, out=made)
+    b.cache16_write(store, k, k, table, rope=rope)
+    assert torch.equal(made[0], b.rotary(rope, q)[0])
