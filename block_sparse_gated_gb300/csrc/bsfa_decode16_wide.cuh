@@ -10,7 +10,8 @@
 // Two softmax warpgroups take the tiles in turn, each with a score buffer, an O and a
 // row offset of its own: neither waits for the other, and their results are two parts
 // of the segment, which the join adds along with those of other CTAs.  Of a segment
-// that lies within one CTA the second warpgroup adds them.
+// that lies within one CTA the second warpgroup adds them.  Sums that are not finite
+// are formed anew by the join, where nobody waits for them.
 //
 // Roles (384 threads, one CTA per SM):
 //   warp 0      copies K and V tiles through TMA, one box per lane: a box lies within
@@ -45,8 +46,9 @@ constexpr int WIDE_MIN_UNITS = 1;  // shortest piece of the line worth a CTA (1 
                                    // rows: 13.0 us; at 4 16.1)
 constexpr int WIDE_THREADS = 384;
 // Tiles that a warpgroup sums in TMEM, at most: the tensor cores cut off what they add
-// instead of rounding it, 2^-24 of the sum at each of a tile's sixteen steps.  Longer
-// runs are added in fp32, in the workspace.
+// instead of rounding it, up to 2^-23 of the sum at each of a tile's sixteen steps, so
+// 2^-13 of a run's O at worst (values of one sign over 40000 tokens, fp16: 2^-14 on
+// average).  Longer runs are added in fp32, in the workspace.
 constexpr int WIDE_RUN = 64;
 // Of the key and of the value ring (16 ragged sequences to 32K with 64 rows: 104.7 us; at
 // 2 110.1).

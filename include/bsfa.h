@@ -526,10 +526,11 @@ bsfa_status bsfa_cache16_write(const bsfa_cache16* cache, const bsfa_rope* rope,
  * cache's, the workspace of bsfa_decode16_workspace_size) and the same limits.
  * Products run on the tensor cores in that type with fp32 accumulation; weights take
  * part as the sum of two 16-bit numbers, so O is off by little more than its one
- * rounding.  Values may have any size that their type holds; bf16 results below 2^-85
- * may lose their last bits.  A token that a query does not see has no part in its
- * result, whatever its rows hold.  Scores below -3e38 weigh nothing.  o may be q itself,
- * with the same strides. */
+ * rounding: with more than 32 query rows per KV head by 2^-13 of it at most, toward zero,
+ * as the tensor cores cut off what they add.  Values may have any size that their type
+ * holds; bf16 results below 2^-85 may lose their last bits.  A token that a query does
+ * not see has no part in its result, whatever its rows hold.  Scores below -3e38 weigh
+ * nothing.  o may be q itself, with the same strides. */
 size_t bsfa_decode16_workspace_size(const bsfa_cache16* cache, const bsfa_decode4_params* p);
 bsfa_status bsfa_decode16(const bsfa_cache16* cache, const bsfa_decode4_params* p,
                           bsfa_stream_t stream);
